@@ -17,7 +17,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["rq_gemm_s4.hip", "rq_gemm_s8.hip", "rq_gemm_a4.hip", "rq_gemm_a5.hip",
            "rq_gemm_a6.hip", "rq_gemm_f8.hip",  # the slowest first
            "rq_api.hip", "rq_dequant.hip", "rq_gemv.hip", "rq_gemm.hip", "rq_mv.hip",
-           "rq_probe.hip"]
+           "rq_probe.hip", "rq_lora.hip", "rq_wkv.hip", "rq_shift.hip", "rq_logits.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -15,6 +15,11 @@
 #include "rq_internal.h"
 #include "rq_probe.h"
 
+static_assert(RQ_WKV_HEAD == rq::WKV_HEAD && RQ_LORA_MAX_RANK == rq::LORA_MAX_RANK &&
+              RQ_LORA_MAX_BATCH == rq::LORA_BATCH && RQ_LOGITS_MAX_M == rq::LOGITS_MAX_M &&
+              RQ_LOGITS_MAX_M * 12 <= RQ_LOGITS_WORKSPACE_BYTES,
+              "the interface's limits are the kernels'");
+
 namespace rq {
 
 static Tuning g_tuning;
@@ -272,6 +277,45 @@ Kernel pick_kernel(int fmt, int M, int N, int K, int group, rq::GemvCfg* gc) {
   return k;
 }
 
+// --------------------------------------------------------------------------
+// The calls around the products: an operand is a range of device memory with
+// an alignment, and the ranges a call writes overlap nothing else.
+// --------------------------------------------------------------------------
+struct Operand {
+  const void* p;
+  size_t bytes;
+  size_t align;
+};
+
+Operand index_array(const void* p, size_t n) { return Operand{p, n * 4, 4}; }
+Operand array(const void* p, size_t bytes) { return Operand{p, bytes, 16}; }
+
+rq_status check_align(const Operand* v, int n) {
+  for (int i = 0; i < n; i++)
+    if (v[i].p && (reinterpret_cast<uintptr_t>(v[i].p) & (v[i].align - 1))) return RQ_ERR_ALIGN;
+  return RQ_OK;
+}
+
+// `w` (written) against in[0..n) (NULL or empty ones cannot overlap).
+rq_status check_apart(const Operand& w, const Operand* in, int n) {
+  if (!w.p || !w.bytes) return RQ_OK;
+  for (int i = 0; i < n; i++)
+    if (in[i].p && in[i].bytes &&
+        overlaps(range_of(w.p, w.bytes), range_of(in[i].p, in[i].bytes)))
+      return RQ_ERR_ALIAS;
+  return RQ_OK;
+}
+
+// Sizes of a batch of sequences over stored states.
+rq_status check_batch(const void* state, const int* offsets, const int* slots, int T,
+                      int sequences, int nslots) {
+  if (!offsets) return RQ_ERR_NULL;
+  if (T < 1 || sequences < 1 || nslots < 0) return RQ_ERR_SHAPE;
+  if (!slots && nslots < sequences) return RQ_ERR_SHAPE;
+  if (nslots > 0 && !state) return RQ_ERR_NULL;
+  return RQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -486,6 +530,189 @@ rq_status rq_gemm_smallm_noalloc(const void* qweight, const void* scales, const 
   }
   const hipError_t e = rq::launch_gemm(p, c, ws, s);
   return e == hipSuccess ? RQ_OK : RQ_ERR_LAUNCH;
+}
+
+rq_status rq_shift(const void* x, const void* mu, void* state, void* out, const int* offsets,
+                   const int* slots, int T, int D, int n, int sequences, int nslots,
+                   void* stream) {
+  if (!x || !mu || !out) return RQ_ERR_NULL;
+  rq_status st = check_batch(state, offsets, slots, T, sequences, nslots);
+  if (st != RQ_OK) return st;
+  if (D < 8 || D % 8 != 0 || n < 1 || n > RQ_SHIFT_MAX_MIXES) return RQ_ERR_SHAPE;
+  const size_t row = (size_t)D * 2;
+  const Operand o[] = {array(out, row * T * n), array(state, row * nslots), array(x, row * T),
+                       array(mu, row * n), index_array(offsets, (size_t)sequences + 1),
+                       index_array(slots, sequences)};
+  st = check_align(o, 6);
+  if (st == RQ_OK) st = check_apart(o[0], o + 1, 5);
+  if (st == RQ_OK) st = check_apart(o[1], o + 2, 4);
+  int dev;
+  if (st == RQ_OK) st = check_device(&dev);
+  if (st != RQ_OK) return st;
+  const rq::ShiftArgs a{static_cast<const _Float16*>(x), static_cast<const _Float16*>(mu),
+                        static_cast<_Float16*>(state), static_cast<_Float16*>(out), offsets,
+                        slots, T, D, n, sequences, nslots};
+  return rq::launch_shift(a, static_cast<hipStream_t>(stream)) == hipSuccess ? RQ_OK
+                                                                            : RQ_ERR_LAUNCH;
+}
+
+rq_status rq_wkv7(const void* r, const void* w, const void* k, const void* v, const void* kappa,
+                  const void* eta, int input_type, float* state, float* y, const int* offsets,
+                  const int* slots, int T, int H, int sequences, int nslots, void* stream) {
+  if (!r || !w || !k || !v || !kappa || !eta || !y) return RQ_ERR_NULL;
+  rq_status st = check_batch(state, offsets, slots, T, sequences, nslots);
+  if (st != RQ_OK) return st;
+  if (input_type != RQ_TYPE_F32 && input_type != RQ_TYPE_F16) return RQ_ERR_UNSUPPORTED;
+  if (H < 1 || H > 4096) return RQ_ERR_SHAPE;
+  const size_t n = (size_t)T * H * RQ_WKV_HEAD, e = input_type == RQ_TYPE_F16 ? 2 : 4;
+  const Operand o[] = {array(y, n * 4),
+                       array(state, (size_t)nslots * H * RQ_WKV_HEAD * RQ_WKV_HEAD * 4),
+                       array(r, n * e), array(w, n * e), array(k, n * e), array(v, n * e),
+                       array(kappa, n * e), array(eta, n * e),
+                       index_array(offsets, (size_t)sequences + 1),
+                       index_array(slots, sequences)};
+  st = check_align(o, 10);
+  if (st == RQ_OK) st = check_apart(o[0], o + 1, 9);
+  if (st == RQ_OK) st = check_apart(o[1], o + 2, 8);
+  int dev;
+  if (st == RQ_OK) st = check_device(&dev);
+  if (st != RQ_OK) return st;
+  const rq::WkvArgs a{r, w, k, v, kappa, eta, state, y, offsets, slots,
+                      input_type == RQ_TYPE_F16, T, H, sequences, nslots};
+  return rq::launch_wkv(a, static_cast<hipStream_t>(stream)) == hipSuccess ? RQ_OK
+                                                                          : RQ_ERR_LAUNCH;
+}
+
+// K ranges of a call (the same for all its projections) and its workspace.
+static rq_status lora_plan(const rq_lora_problem* problems, int count, int M, int adapters,
+                           int max_rank, int* splits, size_t* bytes) {
+  if (!problems) return RQ_ERR_NULL;
+  if (count < 1 || count > RQ_LORA_MAX_BATCH || M < 1 || M > RQ_LORA_MAX_M || adapters < 1)
+    return RQ_ERR_SHAPE;
+  if (max_rank < 8 || max_rank > RQ_LORA_MAX_RANK || max_rank % 8 != 0) return RQ_ERR_SHAPE;
+  int k_max = 0;
+  for (int i = 0; i < count; i++) {
+    if (problems[i].N < 1 || problems[i].K < 8 || problems[i].K % 8 != 0) return RQ_ERR_SHAPE;
+    if (problems[i].K > k_max) k_max = problems[i].K;
+  }
+  *splits = rq::lora_splits(count, M, k_max, adapters, max_rank);
+  *bytes = (size_t)count * *splits * M * ((max_rank + 15) / 16 * 16) * sizeof(float);
+  return RQ_OK;
+}
+
+rq_status rq_lora_workspace_size(const rq_lora_problem* problems, int count, int M, int adapters,
+                                 int max_rank, size_t* bytes) {
+  if (!bytes) return RQ_ERR_NULL;
+  *bytes = 0;
+  int splits;
+  return lora_plan(problems, count, M, adapters, max_rank, &splits, bytes);
+}
+
+rq_status rq_lora(const rq_lora_problem* problems, int count, int M, const int* ids,
+                  const int* offsets, const float* scales, int adapters, int total_rank,
+                  int max_rank, void* workspace, size_t workspace_bytes, void* stream) {
+  int splits = 0;
+  size_t need = 0;
+  rq_status st = lora_plan(problems, count, M, adapters, max_rank, &splits, &need);
+  if (st != RQ_OK) return st;
+  if (!ids || !offsets) return RQ_ERR_NULL;
+  if (total_rank < 0) return RQ_ERR_SHAPE;
+  // written: the workspace and every y; read: shared arrays, then per problem
+  Operand in[3 + 4 * RQ_LORA_MAX_BATCH], out[RQ_LORA_MAX_BATCH];
+  in[0] = index_array(ids, M);
+  in[1] = index_array(offsets, (size_t)adapters + 1);
+  in[2] = Operand{scales, (size_t)adapters * 4, 4};
+  rq::LoraBatch bt{};
+  bt.count = count;
+  for (int i = 0; i < count; i++) {
+    const rq_lora_problem& q = problems[i];
+    if (!q.x || !q.y || (total_rank > 0 && (!q.a || !q.b))) return RQ_ERR_NULL;
+    const size_t yb = (size_t)M * q.N * 4;
+    in[3 + 4 * i] = array(q.a, (size_t)total_rank * q.K * 2);
+    in[4 + 4 * i] = array(q.b, (size_t)total_rank * q.N * 2);
+    in[5 + 4 * i] = array(q.x, (size_t)M * q.K * 2);
+    in[6 + 4 * i] = array(q.y_in, yb);
+    out[i] = array(q.y, yb);
+    bt.p[i] = rq::LoraProblem{static_cast<const _Float16*>(q.a), static_cast<const _Float16*>(q.b),
+                              static_cast<const _Float16*>(q.x), q.y_in, q.y, q.N, q.K};
+  }
+  const int nin = 3 + 4 * count;
+  const Operand ws = array(workspace, need);
+  st = check_align(in, nin);
+  if (st == RQ_OK) st = check_align(out, count);
+  if (st == RQ_OK) st = check_align(&ws, 1);
+  if (st != RQ_OK) return st;
+  for (int i = 0; i < count; i++) {
+    for (int j = 0; j < nin; j++) {
+      if (j == 6 + 4 * i && in[j].p == out[i].p) continue;  // in place
+      if (check_apart(out[i], in + j, 1) != RQ_OK) return RQ_ERR_ALIAS;
+    }
+    if (check_apart(out[i], out + i + 1, count - i - 1) != RQ_OK) return RQ_ERR_ALIAS;
+  }
+  if (!workspace || workspace_bytes < need) return RQ_ERR_SCRATCH;
+  if (check_apart(ws, in, nin) != RQ_OK || check_apart(ws, out, count) != RQ_OK)
+    return RQ_ERR_ALIAS;
+  int dev;
+  st = check_device(&dev);
+  if (st != RQ_OK) return st;
+  const rq::LoraArgs a{ids, offsets, scales, static_cast<float*>(workspace), M, adapters,
+                       total_rank, max_rank, (max_rank + 15) / 16 * 16, splits};
+  return rq::launch_lora(bt, a, static_cast<hipStream_t>(stream)) == hipSuccess ? RQ_OK
+                                                                               : RQ_ERR_LAUNCH;
+}
+
+rq_status rq_logits(const rq_logits_args* args, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  if (!args || !args->logits || !args->out) return RQ_ERR_NULL;
+  const rq_logits_args& g = *args;
+  if (g.M < 1 || g.M > RQ_LOGITS_MAX_M || g.V < 1) return RQ_ERR_SHAPE;
+  if (g.history && !g.history_offsets) return RQ_ERR_NULL;
+  if (g.bias_ids && (!g.bias || !g.bias_offsets)) return RQ_ERR_NULL;
+  if (g.masks && !g.mask_ids) return RQ_ERR_NULL;
+  if ((g.history && g.history_len < 0) || (g.bias_ids && g.bias_len < 0) ||
+      (g.masks && g.nmasks < 1))
+    return RQ_ERR_SHAPE;
+  const size_t zb = (size_t)g.M * g.V * 4, m = g.M;
+  const size_t hl = g.history ? g.history_len : 0, bl = g.bias_ids ? g.bias_len : 0;
+  const Operand in[] = {
+      array(g.logits, zb),
+      index_array(g.history, hl),
+      index_array(g.history ? g.history_offsets : nullptr, m + 1),
+      index_array(g.history ? g.prompt : nullptr, m),
+      index_array(g.history ? g.repetition : nullptr, m),
+      index_array(g.history ? g.presence : nullptr, m),
+      index_array(g.history ? g.frequency : nullptr, m),
+      index_array(g.bias_ids, bl),
+      index_array(g.bias_ids ? g.bias : nullptr, bl),
+      index_array(g.bias_ids ? g.bias_offsets : nullptr, m + 1),
+      index_array(g.masks, g.masks ? (size_t)g.nmasks * (((size_t)g.V + 31) / 32) : 0),
+      index_array(g.masks ? g.mask_ids : nullptr, m)};
+  constexpr int NIN = sizeof(in) / sizeof(in[0]);
+  const bool uses_ws = g.tokens != nullptr;
+  const Operand out[] = {array(g.out, zb), index_array(g.tokens, m),
+                         array(uses_ws ? workspace : nullptr, RQ_LOGITS_WORKSPACE_BYTES)};
+  rq_status st = check_align(in, NIN);
+  if (st == RQ_OK) st = check_align(out, 3);
+  if (st != RQ_OK) return st;
+  const int first = g.out == g.logits ? 1 : 0;  // in place
+  if (check_apart(out[0], in + first, NIN - first) != RQ_OK ||
+      check_apart(out[0], out + 1, 2) != RQ_OK)
+    return RQ_ERR_ALIAS;
+  if (check_apart(out[1], in, NIN) != RQ_OK || check_apart(out[1], out + 2, 1) != RQ_OK)
+    return RQ_ERR_ALIAS;
+  if (uses_ws && (!workspace || workspace_bytes < RQ_LOGITS_WORKSPACE_BYTES))
+    return RQ_ERR_SCRATCH;
+  if (check_apart(out[2], in, NIN) != RQ_OK) return RQ_ERR_ALIAS;
+  int dev;
+  st = check_device(&dev);
+  if (st != RQ_OK) return st;
+  const rq::LogitsArgs a{g.logits, g.out, g.tokens, g.history, g.history_offsets, g.prompt,
+                         g.repetition, g.presence, g.frequency, g.bias_ids, g.bias,
+                         g.bias_offsets, g.masks, g.mask_ids, g.M, g.V, (int)hl, (int)bl,
+                         g.nmasks};
+  return rq::launch_logits(a, workspace, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? RQ_OK
+             : RQ_ERR_LAUNCH;
 }
 
 const char* rq_status_string(int status) {

@@ -88,4 +88,72 @@ hipError_t launch_dequant(const void* qweight, const void* scales, const void* z
                           void* out, int N, int K, int group, int fmt, int out_kind,
                           hipStream_t s);
 
+// Token shift (rq_shift.hip); pointers as in rq.h.
+struct ShiftArgs {
+  const _Float16* x;   // [T][D]
+  const _Float16* mu;  // [n][D]
+  _Float16* state;     // [nslots][D]
+  _Float16* out;       // [n][T][D]
+  const int* offsets;  // [sequences + 1]
+  const int* slots;    // [sequences] or NULL
+  int T, D, n, sequences, nslots;
+};
+hipError_t launch_shift(const ShiftArgs& a, hipStream_t s);
+
+// RWKV-7 state recurrence (rq_wkv.hip).
+constexpr int WKV_HEAD = 64;
+struct WkvArgs {
+  const void *r, *w, *k, *v, *kappa, *eta;  // [T][H * 64], binary16 or binary32
+  float* state;                             // [nslots][H][64][64]
+  float* y;                                 // [T][H * 64]
+  const int* offsets;
+  const int* slots;
+  int half, T, H, sequences, nslots;
+};
+hipError_t launch_wkv(const WkvArgs& a, hipStream_t s);
+
+// Low-rank adapters (rq_lora.hip).
+constexpr int LORA_MAX_RANK = 128;
+constexpr int LORA_BATCH = 8;
+constexpr int LORA_MAX_SPLITS = 16;
+struct LoraProblem {
+  const _Float16 *a, *b, *x;
+  const float* y_in;  // NULL: zero
+  float* y;
+  int N, K;
+};
+struct LoraBatch {
+  LoraProblem p[LORA_BATCH];
+  int count;
+};
+struct LoraArgs {
+  const int* ids;       // [M]
+  const int* offsets;   // [adapters + 1]
+  const float* scales;  // [adapters] or NULL
+  float* ws;            // [count][splits][M][rank_ld]
+  int M, adapters, total_rank, max_rank, rank_ld, splits;
+};
+int lora_splits(int count, int M, int K, int adapters, int max_rank);
+hipError_t launch_lora(const LoraBatch& bt, const LoraArgs& a, hipStream_t s);
+
+// Logits (rq_logits.hip).
+constexpr int LOGITS_MAX_M = 4096;
+struct LogitsArgs {
+  const float* logits;
+  float* out;
+  int* tokens;  // NULL: no choice
+  const int *history, *history_offsets, *prompt;
+  const float *repetition, *presence, *frequency;
+  const int* bias_ids;
+  const float* bias;
+  const int* bias_offsets;
+  const unsigned* masks;
+  const int* mask_ids;
+  int M, V, history_len, bias_len, nmasks;
+};
+int logits_slices(int V);
+// ws: LOGITS_MAX_M 8-byte maxima, then as many 4-byte counters, zero between
+// launches (unused with one slice or without tokens)
+hipError_t launch_logits(const LogitsArgs& a, void* ws, hipStream_t s);
+
 }  // namespace rq

@@ -257,6 +257,176 @@ rq_status rq_gemm_smallm_noalloc(const void* qweight, const void* scales, const 
                                  const void* x, float* y, int M, int N, int K, int bits,
                                  int group, int layout, void* stream);
 
+/*
+ * Around the products.  The calls below do what a serving step needs next to
+ * the packed projections: per-request adapters, the token shift, the state
+ * recurrence and the treatment of the head's logits.  They keep the rules
+ * above (caller-owned 16-byte-aligned device memory, host-side checks before
+ * any HIP call, work enqueued on `stream`, no allocation, no
+ * synchronization), with two differences: operands may exceed 2 GiB, and index
+ * arrays (ids, offsets, slots, ...) are device memory of int32 with 4-byte
+ * alignment.  Their contents are read on the device only, so they may change between
+ * replays of a captured graph; every index read from them is checked there
+ * against the sizes of the call, and what lies outside is treated as said at
+ * each call, so no content makes a kernel leave its operands.
+ *
+ * A batch of sequences is described by offsets[sequences + 1]: sequence q is
+ * the rows offsets[q] .. offsets[q+1] - 1 of the token arrays (0 <= offsets[0]
+ * <= ... <= offsets[sequences] <= T); a sequence may be empty, one token, or a
+ * prompt.  slots[q] is its row in a pool of nslots stored states, in which it
+ * starts and to which it returns (slots NULL: slot q); a slot outside
+ * 0 .. nslots-1 means a zero start and nothing stored.  Two sequences of a
+ * call must not share a slot unless one is empty.
+ */
+
+/* Largest n of rq_shift. */
+#define RQ_SHIFT_MAX_MIXES 8
+
+/*
+ * rq_shift -- the token shift that makes the inputs of a layer's projections:
+ *   out[i][t] = x[t] + (prev[t] - x[t]) * mu[i],   i < n,
+ * prev[t] = x[t-1], or the stored row state[slot] for a sequence's first
+ * token; then state[slot] = the sequence's last row.  A causal convolution of
+ * two taps, n of them over one input (RWKV-7's time mix takes six).
+ *   x: binary16 [T][D].  mu: binary16 [n][D].  state: binary16 [nslots][D].
+ *   out: binary16 [n][T][D], computed in binary32 and rounded once.
+ * Rows of x that no sequence covers leave unspecified rows in out.
+ * Shape rules: T >= 1, D >= 8, D % 8 == 0, 1 <= n <= RQ_SHIFT_MAX_MIXES,
+ * sequences >= 1, nslots >= 0 (at least `sequences` when slots is NULL; state
+ * may be NULL when nslots is 0, which needs slots).
+ */
+rq_status rq_shift(const void* x, const void* mu, void* state, void* out, const int* offsets,
+                   const int* slots, int T, int D, int n, int sequences, int nslots,
+                   void* stream);
+
+/* Channels of a head of rq_wkv7. */
+#define RQ_WKV_HEAD 64
+
+/* Types of rq_wkv7's inputs. */
+typedef enum { RQ_TYPE_F32 = 0, RQ_TYPE_F16 = 1 } rq_type;
+
+/*
+ * rq_wkv7 -- the RWKV-7 state recurrence between the receptance/key/value
+ * projections and the output projection.  Per head, S binary32 [64 values i]
+ * [64 keys j], and per token t of a sequence, in order:
+ *   d_j = exp(-exp(-1/2) * sigmoid(w_j))           (between 0.545 and 1)
+ *   S   = S diag(d) - (S kappa) (eta * kappa)^T + v k^T
+ *   y_i = sum_j S_ij r_j
+ *   r, w, k, v, kappa, eta: [T][H*64], all of input_type.  w is the decay
+ *   before its two activations, kappa the removal key, eta its learning rate.
+ *   state: float [nslots][H][64][64], read and overwritten for every
+ *   sequence that has a token.  y: float [T][H*64]; rows that no sequence
+ *   covers are not written.
+ * All sums and the state are binary32.  Non-finite inputs reach the outputs of
+ * their own token and later ones only.
+ * Shape rules: T >= 1, 1 <= H <= 4096, sequences >= 1, nslots as for rq_shift.
+ */
+rq_status rq_wkv7(const void* r, const void* w, const void* k, const void* v, const void* kappa,
+                  const void* eta, int input_type, float* state, float* y, const int* offsets,
+                  const int* slots, int T, int H, int sequences, int nslots, void* stream);
+
+/* Limits of rq_lora. */
+#define RQ_LORA_MAX_M 8192
+#define RQ_LORA_MAX_RANK 128
+#define RQ_LORA_MAX_BATCH 8
+
+/* One projection of rq_lora.  Adapter i has rank r_i = offsets[i+1] -
+ * offsets[i], the A rows offsets[i] .. offsets[i+1] - 1, and the block of B
+ * [N][r_i] that starts at value offsets[i] * N. */
+typedef struct {
+    const void* a;     /* binary16 [total_rank][K]: the A rows of all adapters */
+    const void* b;     /* binary16, total_rank * N values: the B blocks         */
+    const void* x;     /* binary16 [M][K]                                       */
+    const float* y_in; /* float [M][N], NULL for zero; y itself, or disjoint    */
+    float* y;          /* float [M][N]                                          */
+    int N;
+    int K;
+} rq_lora_problem;
+
+/*
+ * rq_lora -- adapters of many requests beside a shared projection: with
+ * i = ids[m],
+ *   y[m] = y_in[m] + scales[i] * B_i (A_i x[m]),
+ * for `count` projections (receptance, key and value, say) in two launches.
+ * y_in is the shared projection's output, y usually the same array.  A row
+ * whose id lies outside 0 .. adapters-1, or whose adapter has rank 0, gets
+ * y[m] = y_in[m].  So does one whose rank is not a multiple of 8, exceeds
+ * max_rank or leaves 0 .. total_rank.  A_i x is kept in binary32.
+ *   ids: [M].  offsets: [adapters + 1], multiples of 8.  scales: float
+ *   [adapters], NULL for 1.  workspace: device memory of at least
+ *   rq_lora_workspace_size bytes, 16-byte aligned, that overlaps nothing else; it needs
+ *   no clearing and holds nothing between calls.
+ * Results do not depend on which other rows share the call's blocks of rows,
+ * beyond the split of K, which follows the call's sizes.
+ * Shape rules: 1 <= count <= RQ_LORA_MAX_BATCH, 1 <= M <= RQ_LORA_MAX_M, N >=
+ * 1, K >= 8, K % 8 == 0, adapters >= 1, total_rank >= 0, 8 <= max_rank <=
+ * RQ_LORA_MAX_RANK, max_rank % 8 == 0.  RQ_ERR_SCRATCH: the workspace is NULL
+ * or too small.  `problems` is a host array the call reads before it returns.
+ */
+rq_status rq_lora(const rq_lora_problem* problems, int count, int M, const int* ids,
+                  const int* offsets, const float* scales, int adapters, int total_rank,
+                  int max_rank, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The workspace rq_lora uses at these arguments (N, K of `problems` only).
+ * Host-only. */
+rq_status rq_lora_workspace_size(const rq_lora_problem* problems, int count, int M, int adapters,
+                                 int max_rank, size_t* bytes);
+
+/* Limits and workspace of rq_logits. */
+#define RQ_LOGITS_MAX_M 4096
+#define RQ_LOGITS_WORKSPACE_BYTES (64 << 10)
+
+/* Arguments of rq_logits; a NULL first pointer of a group leaves the group's
+ * step out. */
+typedef struct {
+    const float* logits; /* [M][V]                                                */
+    float* out;          /* [M][V]; logits itself, or disjoint                    */
+    int* tokens;         /* [M], the greatest entry of each row; NULL: not wanted */
+    int M;
+    int V;
+    /* tokens so far: row m's are history[history_offsets[m] .. [m+1] - 1], the
+     * first prompt[m] of them given, the others generated */
+    const int* history;
+    const int* history_offsets; /* [M + 1]                                        */
+    const int* prompt;          /* [M], NULL for none                             */
+    int history_len;            /* entries of history                             */
+    const float* repetition;    /* [M], > 0, NULL for 1; only with a history      */
+    const float* presence;      /* [M], NULL for 0                                */
+    const float* frequency;     /* [M], NULL for 0                                */
+    /* additions: row m's are entries bias_offsets[m] .. [m+1] - 1 */
+    const int* bias_ids;
+    const float* bias;
+    const int* bias_offsets; /* [M + 1]                                           */
+    int bias_len;
+    /* allowed tokens: bit v % 32 of masks[mask_ids[m]][v / 32] */
+    const unsigned* masks; /* [nmasks][(V + 31) / 32]                             */
+    const int* mask_ids;   /* [M]; outside 0 .. nmasks-1: every token allowed     */
+    int nmasks;
+} rq_logits_args;
+
+/*
+ * rq_logits -- penalties, biases and masks on the head's logits, and the
+ * greatest.  For every value z of row m, token v, with c its occurrences in
+ * the generated part of the row's history:
+ *   v anywhere in the history:  z = z > 0 ? z / repetition : z * repetition,
+ *                               z = z - frequency * c,  c > 0: z = z - presence;
+ *   v among the row's biases:   z = z + bias, of its last entry;
+ *   v not allowed:              z = -infinity, whatever it was.
+ * Each operation is rounded to binary32 on its own, in this order.  tokens[m]
+ * is the lowest v of the greatest z; NaN is never chosen, and a row with
+ * nothing above -infinity gives -1.  History and bias entries outside 0 ..
+ * V-1 are ignored.
+ *   workspace: needed when tokens is not NULL; RQ_LOGITS_WORKSPACE_BYTES of
+ *   device memory, 16-byte aligned, overlapping nothing else, zero before its first
+ *   use; every call leaves it zero (the first 64 KiB of a workspace of
+ *   rq_gemm_smallm_ws will do).  Calls that share it must not overlap in time.
+ *   RQ_ERR_SCRATCH: NULL or too small.
+ * Shape rules: 1 <= M <= RQ_LOGITS_MAX_M, V >= 1, lengths >= 0, nmasks >= 1
+ * with masks.
+ */
+rq_status rq_logits(const rq_logits_args* args, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
 /* A static, NUL-terminated English description of a status value. */
 const char* rq_status_string(int status);
 
