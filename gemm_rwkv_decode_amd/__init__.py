@@ -43,6 +43,7 @@ RQ_LAYOUT_SYM, RQ_LAYOUT_ASYM_SB, RQ_LAYOUT_FP8_TENSOR = 0, 1, 2
 RQ_OUT_F32, RQ_OUT_CODES_I8 = 0, 1
 RQ_MAX_M = 64
 RQ_MAX_BATCH = 64
+RQ_MAX_SEQUENCES = 65536
 RQ_SHIFT_MAX_MIXES = 8
 RQ_WKV_HEAD = 64
 RQ_TYPE_F32, RQ_TYPE_F16 = 0, 1

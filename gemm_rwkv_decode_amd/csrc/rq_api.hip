@@ -310,7 +310,7 @@ rq_status check_apart(const Operand& w, const Operand* in, int n) {
 rq_status check_batch(const void* state, const int* offsets, const int* slots, int T,
                       int sequences, int nslots) {
   if (!offsets) return RQ_ERR_NULL;
-  if (T < 1 || sequences < 1 || nslots < 0) return RQ_ERR_SHAPE;
+  if (T < 1 || sequences < 1 || sequences > RQ_MAX_SEQUENCES || nslots < 0) return RQ_ERR_SHAPE;
   if (!slots && nslots < sequences) return RQ_ERR_SHAPE;
   if (nslots > 0 && !state) return RQ_ERR_NULL;
   return RQ_OK;

@@ -40,7 +40,7 @@ __device__ __forceinline__ f4 load4(const T* p) {
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_wkv_seq(const WkvArgs a) {
-  const int q = blockIdx.x, h = blockIdx.y;
+  const int q = blockIdx.x / a.H, h = blockIdx.x % a.H;
   const int lo = max(a.offsets[q], 0), hi = min(a.offsets[q + 1], a.T);
   if (lo >= hi) return;
   const int slot = a.slots ? a.slots[q] : q;
@@ -133,30 +133,47 @@ constexpr int LDR = 68;     // floats between rows of a [16][64] operand (bank o
 constexpr int LDT = 20;     // floats between rows of a [64][16] or [16][16] operand
 constexpr int PRODUCERS = 3;
 
+// What a chunk's state waves read.  With one state wave per workgroup the
+// producers also make the products with V, which leaves the state wave with
+// what depends on the state.
+template <int NR>
 struct ChunkOps {
-  float ah[CH * LDR];     // kappa_t o P_{t-1}
-  float rh[CH * LDR];     // r_t o P_t
-  float bcT[HD * LDT];    // [key][token]
-  float kcT[HD * LDT];
-  float x[CH * LDT];      // (I - Mb)^-1
-  float mk[CH * LDT], nb[CH * LDT], nk[CH * LDT];
-  float pc[HD];           // P_16
-  int bad;                // a value that is not finite: token by token
+  float ah[CH * LDR];   // kappa_t o P_{t-1}
+  float rh[CH * LDR];   // r_t o P_t
+  float bcT[HD * LDT];  // [key][token]
+  float x[CH * LDT];    // (I - Mb)^-1
+  float nb[CH * LDT];
+  float pc[HD];         // P_16
+  int bad;              // a value that is not finite: token by token
+  // NR = 4: kcT and the matrices that multiply V; NR = 1: the products
+  // themselves, as accumulators [j][lane] of kc^T V, then Mk V and Nk V
+  float v[NR == 1 ? 6 * 256 : HD * LDT + 2 * CH * LDT];
+  __device__ __forceinline__ float* kcT() { return v; }
+  __device__ __forceinline__ float* mk() { return v + HD * LDT; }
+  __device__ __forceinline__ float* nk() { return v + HD * LDT + CH * LDT; }
 };
 
-// product over the lanes of a row of 16 up to this one
-template <int CTRL>
-__device__ __forceinline__ float dpp_or_one(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
-                                       0x3f800000, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF,
-                                       false));
+// product over the lanes of a row of 16 up to this one, for four values: a
+// lane without a left neighbour at the distance keeps its value (a DPP read
+// needs two wait states after its register was written: the s_nops, and between
+// the steps the other three values)
+__device__ __forceinline__ void row_scan4(f4& p) {
+  float a = p[0], b = p[1], c = p[2], d = p[3];
+#define RQ_SCAN_STEP(n)                                              \
+  "v_mul_f32_dpp %0, %0, %0 row_shr:" #n " row_mask:0xf bank_mask:0xf\n" \
+  "v_mul_f32_dpp %1, %1, %1 row_shr:" #n " row_mask:0xf bank_mask:0xf\n" \
+  "v_mul_f32_dpp %2, %2, %2 row_shr:" #n " row_mask:0xf bank_mask:0xf\n" \
+  "v_mul_f32_dpp %3, %3, %3 row_shr:" #n " row_mask:0xf bank_mask:0xf\n"
+  asm("s_nop 1\n" RQ_SCAN_STEP(1) RQ_SCAN_STEP(2) RQ_SCAN_STEP(4) RQ_SCAN_STEP(8) "s_nop 1\n"
+      : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+#undef RQ_SCAN_STEP
+  p = f4{a, b, c, d};
 }
-__device__ __forceinline__ float row_scan(float v) {
-  v *= dpp_or_one<0x111>(v);  // row_shr:1
-  v *= dpp_or_one<0x112>(v);
-  v *= dpp_or_one<0x114>(v);
-  v *= dpp_or_one<0x118>(v);
-  return v;
+// the left neighbour's value, 1 in a row's first lane
+__device__ __forceinline__ float left_or_one(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                       0x3f800000, __builtin_bit_cast(int, v), 0x111, 0xF, 0xF,
+                                       false));
 }
 
 __device__ __forceinline__ f4 mma4(const f4& a, const f4& b, f4 c) {
@@ -165,69 +182,132 @@ __device__ __forceinline__ f4 mma4(const f4& a, const f4& b, f4 c) {
   return c;
 }
 
-__device__ __forceinline__ void step_barrier() { __syncthreads(); }
+// Barrier that waits for this wave's LDS accesses only: loads of later chunks
+// and stores of outputs stay in flight across it (s_waitcnt with lgkmcnt 0,
+// the other counters at their maxima).
+__device__ __forceinline__ void step_barrier() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
 
 // Inputs of one chunk as a producer lane holds them: token lane mod 16, keys
-// 16 jt + 4 (lane / 16) .. + 3.
+// 16 jt + 4 (lane / 16) .. + 3.  They stay as they were loaded until they are
+// used: a conversion here would wait for them.
+template <typename T>
+struct Vec4;
+template <>
+struct Vec4<float> {
+  typedef f4 type;
+};
+template <>
+struct Vec4<_Float16> {
+  typedef h4 type;
+};
 template <typename T>
 struct ChunkIn {
-  f4 w[4], k[4], kap[4], eta[4], r[4];
-  __device__ __forceinline__ void load(const WkvArgs& a, size_t at, bool in) {
+  typedef typename Vec4<T>::type vec;
+  vec w[4], k[4], kap[4], eta[4], r[4];
+  __device__ __forceinline__ void load(const WkvArgs& a, size_t at) {
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      w[j] = load4(static_cast<const T*>(a.w) + at + 16 * j);
-      k[j] = load4(static_cast<const T*>(a.k) + at + 16 * j);
-      kap[j] = load4(static_cast<const T*>(a.kappa) + at + 16 * j);
-      eta[j] = load4(static_cast<const T*>(a.eta) + at + 16 * j);
-      r[j] = load4(static_cast<const T*>(a.r) + at + 16 * j);
-    }
-    // tokens past the sequence's end: nothing decays, nothing is added
-    if (!in) {
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        k[j] = kap[j] = eta[j] = r[j] = f4{0, 0, 0, 0};
-        w[j] = f4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      }
+      w[j] = *reinterpret_cast<const vec*>(static_cast<const T*>(a.w) + at + 16 * j);
+      k[j] = *reinterpret_cast<const vec*>(static_cast<const T*>(a.k) + at + 16 * j);
+      kap[j] = *reinterpret_cast<const vec*>(static_cast<const T*>(a.kappa) + at + 16 * j);
+      eta[j] = *reinterpret_cast<const vec*>(static_cast<const T*>(a.eta) + at + 16 * j);
+      r[j] = *reinterpret_cast<const vec*>(static_cast<const T*>(a.r) + at + 16 * j);
     }
   }
 };
 
+// (tokens, keys) x V: kc^T V into z, Mk V into mv, Nk V into nv.
+__device__ __forceinline__ void v_products(const float* kcT, const float* mk, const float* nk,
+                                           const f4& V, f4* z, f4* mv, f4* nv) {
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  const int at = l16 * LDT + 4 * g;
+  f4 k[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) k[j] = *reinterpret_cast<const f4*>(&kcT[16 * j * LDT + at]);
+  const f4 m = *reinterpret_cast<const f4*>(&mk[at]);
+  const f4 n = *reinterpret_cast<const f4*>(&nk[at]);
+  // six independent sums, so no MFMA waits for the one before it
+#pragma unroll
+  for (int v = 0; v < 4; v++) {
+    *mv = __builtin_amdgcn_mfma_f32_16x16x4f32(m[v], V[v], *mv, 0, 0, 0);
+    *nv = __builtin_amdgcn_mfma_f32_16x16x4f32(n[v], V[v], *nv, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      z[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(k[j][v], V[v], z[j], 0, 0, 0);
+  }
+}
+
+// V of a chunk as a right operand: tokens 4 g + v of the lane's value row, as
+// loaded; tokens past the end repeat the last one until they are used.
 template <typename T>
-__device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, float* scratch, int p,
-                                        int lo, int hi, size_t base, size_t ld) {
+struct ChunkV {
+  T v[4];
+  __device__ __forceinline__ void load(const T* col, size_t ld, int t0, int hi) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = col[(size_t)min(t0 + 4 * g + i, hi - 1) * ld];
+  }
+  __device__ __forceinline__ f4 get(int t0, int hi) const {
+    const int g = (threadIdx.x & 63) >> 4;
+    f4 r;
+#pragma unroll
+    for (int i = 0; i < 4; i++) r[i] = t0 + 4 * g + i < hi ? (float)v[i] : 0.0f;
+    return r;
+  }
+};
+
+template <typename T, int NR>
+__device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, float* scratch,
+                                        int p, int lo, int hi, size_t base, size_t ld, int row) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int n = (hi - lo + CH - 1) / CH;
+  const T* vp = static_cast<const T*>(a.v) + base + row;
   ChunkIn<T> in;
+  ChunkV<T> vin;
   auto fetch = [&](int c) {
-    const int t = lo + c * CH + l16;
-    in.load(a, (size_t)min(t, hi - 1) * ld + base + 4 * g, t < hi);
+    const int t0 = lo + c * CH;
+    in.load(a, (size_t)min(t0 + l16, hi - 1) * ld + base + 4 * g);
+    if constexpr (NR == 1) vin.load(vp, ld, t0, hi);
   };
   if (p < n) fetch(p);
   int steps = p;
   for (int i = 0; i < p; i++) step_barrier();
   for (int c = p; c < n; c += PRODUCERS) {
+    const int t0 = lo + c * CH;
     // segment 1: decays and the scaled operands
-    f4 ah[4], rh[4], bh[4], kh[4], pc[4];
-    float zero = 0.0f;  // NaN as soon as anything is not finite
+    f4 ah[4], rh[4], bh[4], kh[4], pc[4], V = {0, 0, 0, 0};
+    const bool live = t0 + l16 < hi;
+    if (t0 + CH > hi && !live) {  // past the end: nothing decays, nothing is added
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-#pragma unroll
-      for (int v = 0; v < 4; v++) {
-        const float P = row_scan(decay_of(in.w[j][v]));
-        const float before = dpp_or_one<0x111>(P);
-        const float inv = __builtin_amdgcn_rcpf(P);
-        pc[j][v] = dpp_mov<0x15F>(P);  // lane 15 of the row
-        ah[j][v] = in.kap[j][v] * before;
-        rh[j][v] = in.r[j][v] * P;
-        bh[j][v] = -(in.eta[j][v] * in.kap[j][v]) * inv;
-        kh[j][v] = in.k[j][v] * inv;
-        zero = __builtin_fmaf(ah[j][v], 0.0f, zero);
-        zero = __builtin_fmaf(rh[j][v], 0.0f, zero);
-        zero = __builtin_fmaf(bh[j][v], 0.0f, zero);
-        zero = __builtin_fmaf(kh[j][v], 0.0f, zero);
+      for (int j = 0; j < 4; j++) {
+        in.k[j] = in.kap[j] = in.eta[j] = in.r[j] = T(0);
+        in.w[j] = T(-INFINITY);
       }
     }
-    const bool bad = __ballot(!(zero == 0.0f)) != 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      f4 P;
+#pragma unroll
+      for (int v = 0; v < 4; v++) P[v] = decay_of((float)in.w[j][v]);
+      row_scan4(P);
+#pragma unroll
+      for (int v = 0; v < 4; v++) {
+        const float kap = (float)in.kap[j][v];
+        const float inv = __builtin_amdgcn_rcpf(P[v]);
+        pc[j][v] = dpp_mov<0x15F>(P[v]);  // lane 15 of the row
+        ah[j][v] = kap * left_or_one(P[v]);
+        rh[j][v] = (float)in.r[j][v] * P[v];
+        bh[j][v] = -((float)in.eta[j][v] * kap) * inv;
+        kh[j][v] = (float)in.k[j][v] * inv;
+      }
+    }
+    if constexpr (NR == 1) V = vin.get(t0, hi);
+    if (c + PRODUCERS < n) fetch(c + PRODUCERS);  // two steps ahead of its use
     step_barrier();
     // segment 2: the four products, rows t = 4 g + v, columns s = lane mod 16
     f4 mb = {0, 0, 0, 0}, mk = mb, nb = mb, nk = mb;
@@ -241,17 +321,58 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, float* 
         nk = __builtin_amdgcn_mfma_f32_16x16x4f32(rh[j][v], kh[j][v], nk, 0, 0, 0);
       }
     }
+    // a value that is not finite leaves none of its row's or column's sums finite
+    float zero = 0.0f;
+    float* const kcT = NR == 1 ? scratch + CH * LDT : ops[c & 1].kcT();
+    float* const mks = kcT + HD * LDT;
+    float* const nks = mks + CH * LDT;
 #pragma unroll
     for (int v = 0; v < 4; v++) {
       const int t = 4 * g + v;
+      zero = __builtin_fmaf(mb[v], 0.0f, __builtin_fmaf(mk[v], 0.0f, zero));
+      zero = __builtin_fmaf(nb[v], 0.0f, __builtin_fmaf(nk[v], 0.0f, zero));
       if (l16 >= t) mb[v] = mk[v] = 0.0f;
       if (l16 > t) nb[v] = nk[v] = 0.0f;
       scratch[t * LDT + l16] = mb[v];
     }
     step_barrier();
-    // segment 3: column l16 of X by forward substitution, then everything to
-    // the chunk's buffer
-    ChunkOps& o = ops[c & 1];
+    // segment 3: the rest, into the chunk's buffer
+    ChunkOps<NR>& o = ops[c & 1];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+#pragma unroll
+      for (int v = 0; v < 4; v++) {
+        const int key = 16 * j + 4 * g + v;
+        kcT[key * LDT + l16] = kh[j][v] * pc[j][v];
+        o.bcT[key * LDT + l16] = bh[j][v] * pc[j][v];
+      }
+      *reinterpret_cast<f4*>(&o.ah[l16 * LDR + 16 * j + 4 * g]) = ah[j];
+      *reinterpret_cast<f4*>(&o.rh[l16 * LDR + 16 * j + 4 * g]) = rh[j];
+      if (l16 == 0) *reinterpret_cast<f4*>(&o.pc[16 * j + 4 * g]) = pc[j];
+    }
+#pragma unroll
+    for (int v = 0; v < 4; v++) {
+      const int at = (4 * g + v) * LDT + l16;
+      mks[at] = mk[v];
+      nks[at] = nk[v];
+      o.nb[at] = nb[v];
+    }
+    if constexpr (NR == 1) {
+      // this wave's own writes, read back transposed (LDS keeps a wave's order)
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      f4 z[4], mv = {0, 0, 0, 0}, nv = mv;
+#pragma unroll
+      for (int j = 0; j < 4; j++) z[j] = f4{0, 0, 0, 0};
+      v_products(kcT, mks, nks, V, z, &mv, &nv);
+      f4* dst = reinterpret_cast<f4*>(o.v) + lane;
+#pragma unroll
+      for (int j = 0; j < 4; j++) dst[64 * j] = z[j];
+      dst[256] = mv;
+      dst[320] = nv;
+#pragma unroll
+      for (int v = 0; v < 4; v++) zero = __builtin_fmaf(z[0][v], 0.0f, zero);
+    }
+    // column l16 of X by forward substitution
     float x[CH];
 #pragma unroll
     for (int t = 0; t < CH; t++) {
@@ -264,27 +385,8 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, float* 
       }
       o.x[t * LDT + l16] = x[t];
     }
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      *reinterpret_cast<f4*>(&o.ah[l16 * LDR + 16 * j + 4 * g]) = ah[j];
-      *reinterpret_cast<f4*>(&o.rh[l16 * LDR + 16 * j + 4 * g]) = rh[j];
-      if (l16 == 0) *reinterpret_cast<f4*>(&o.pc[16 * j + 4 * g]) = pc[j];
-#pragma unroll
-      for (int v = 0; v < 4; v++) {
-        const int key = 16 * j + 4 * g + v;
-        o.bcT[key * LDT + l16] = bh[j][v] * pc[j][v];
-        o.kcT[key * LDT + l16] = kh[j][v] * pc[j][v];
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < 4; v++) {
-      const int at = (4 * g + v) * LDT + l16;
-      o.mk[at] = mk[v];
-      o.nb[at] = nb[v];
-      o.nk[at] = nk[v];
-    }
+    const bool bad = __ballot(!(zero == 0.0f)) != 0;
     if (lane == 0) o.bad = bad;
-    if (c + PRODUCERS < n) fetch(c + PRODUCERS);
     step_barrier();
     steps += 3;
   }
@@ -294,20 +396,22 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, float* 
 template <typename T, int NR>
 __global__ void __launch_bounds__(64 * (NR + PRODUCERS))
 k_wkv_chunk(const WkvArgs a) {
-  __shared__ __align__(16) ChunkOps ops[2];
-  __shared__ __align__(16) float scratch[PRODUCERS][CH * LDT];
-  const int q = blockIdx.x, h = blockIdx.y / (4 / NR);
+  __shared__ __align__(16) ChunkOps<NR> ops[2];
+  __shared__ __align__(16) float scratch[PRODUCERS][(NR == 1 ? 3 * CH + HD : CH) * LDT];
+  // heads are the fast index: a sequence's workgroups go to all XCDs
+  constexpr int TILES = 4 / NR;
+  const int q = blockIdx.x / (a.H * TILES), h = blockIdx.x % (a.H * TILES) / TILES;
   const int lo = max(a.offsets[q], 0), hi = min(a.offsets[q + 1], a.T);
   if (lo >= hi) return;
   const int n = (hi - lo + CH - 1) / CH;
   const size_t ld = (size_t)a.H * HD, base = (size_t)h * HD;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  const int i = 16 * (NR == 4 ? wave % 4 : blockIdx.x % 4) + l16;  // the lane's value row
   if (wave >= NR) {
-    produce<T>(a, ops, scratch[wave - NR], wave - NR, lo, hi, base, ld);
+    produce<T, NR>(a, ops, scratch[wave - NR], wave - NR, lo, hi, base, ld, i);
     return;
   }
-  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-  const int i = 16 * (NR == 4 ? wave : blockIdx.y % 4) + l16;  // the lane's value row
   const int slot = a.slots ? a.slots[q] : q;
   const bool stored = slot >= 0 && slot < a.nslots;
   float* st = a.state + (((size_t)(stored ? slot : 0) * a.H + h) * HD + i) * HD + 4 * g;
@@ -319,55 +423,61 @@ k_wkv_chunk(const WkvArgs a) {
   }
   const T* vp = static_cast<const T*>(a.v) + base + i;
   float* yp = a.y + base + i;
-  f4 V;  // tokens 4 g + v of the next chunk
-  auto fetch_v = [&](int c) {
-#pragma unroll
-    for (int v = 0; v < 4; v++) {
-      const int t = lo + c * CH + 4 * g + v;
-      V[v] = t < hi ? (float)vp[(size_t)t * ld] : 0.0f;
-    }
-  };
-  fetch_v(0);
+  ChunkV<T> vin;
+  if constexpr (NR == 4) vin.load(vp, ld, lo, hi);
   for (int s = 0; s < 3; s++) step_barrier();
   for (int c = 0; c < n; c++) {
-    const ChunkOps& o = ops[c & 1];
+    ChunkOps<NR>& o = ops[c & 1];
     const int t0 = lo + c * CH;
-    const f4 Vc = V;
+    const int at = l16 * LDT + 4 * g;
+    f4 u = {0, 0, 0, 0}, y = u, z[4];
     float zero = 0.0f;
+    if constexpr (NR == 4) {
+      const f4 V = vin.get(t0, hi);
+      if (c + 1 < n) vin.load(vp, ld, t0 + CH, hi);
 #pragma unroll
-    for (int v = 0; v < 4; v++) {
-      zero = __builtin_fmaf(Vc[v], 0.0f, zero);
+      for (int j = 0; j < 4; j++) z[j] = u;
+      v_products(o.kcT(), o.mk(), o.nk(), V, z, &u, &y);
 #pragma unroll
-      for (int j = 0; j < 4; j++) zero = __builtin_fmaf(S[j][v], 0.0f, zero);
+      for (int v = 0; v < 4; v++) zero = __builtin_fmaf(z[0][v], 0.0f, zero);
+    } else {
+      const f4* src = reinterpret_cast<const f4*>(o.v) + lane;
+#pragma unroll
+      for (int j = 0; j < 4; j++) z[j] = src[64 * j];
+      u = src[256];
+      y = src[320];
     }
-    if (c + 1 < n) fetch_v(c + 1);
-    if (!o.bad && __ballot(!(zero == 0.0f)) == 0) {
-      f4 u = {0, 0, 0, 0}, y = u;
-      const int at = l16 * LDT + 4 * g;
-      u = mma4(*reinterpret_cast<const f4*>(&o.mk[at]), Vc, u);
-      y = mma4(*reinterpret_cast<const f4*>(&o.nk[at]), Vc, y);
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const f4 ah = *reinterpret_cast<const f4*>(&o.ah[l16 * LDR + 16 * j + 4 * g]);
-        const f4 rh = *reinterpret_cast<const f4*>(&o.rh[l16 * LDR + 16 * j + 4 * g]);
+    for (int j = 0; j < 4; j++) {
+      const f4 ah = *reinterpret_cast<const f4*>(&o.ah[l16 * LDR + 16 * j + 4 * g]);
+      const f4 rh = *reinterpret_cast<const f4*>(&o.rh[l16 * LDR + 16 * j + 4 * g]);
 #pragma unroll
-        for (int v = 0; v < 4; v++) {
-          u = __builtin_amdgcn_mfma_f32_16x16x4f32(ah[v], S[j][v], u, 0, 0, 0);
-          y = __builtin_amdgcn_mfma_f32_16x16x4f32(rh[v], S[j][v], y, 0, 0, 0);
-        }
+      for (int v = 0; v < 4; v++) {
+        u = __builtin_amdgcn_mfma_f32_16x16x4f32(ah[v], S[j][v], u, 0, 0, 0);
+        y = __builtin_amdgcn_mfma_f32_16x16x4f32(rh[v], S[j][v], y, 0, 0, 0);
       }
-      const f4 zeros = {0, 0, 0, 0};
-      const f4 U = mma4(*reinterpret_cast<const f4*>(&o.x[at]), u, zeros);
+    }
+    // a state that is not finite leaves none of its row's u finite
+#pragma unroll
+    for (int v = 0; v < 4; v++) zero = __builtin_fmaf(u[v], 0.0f, zero);
+    if (!o.bad && __ballot(!(zero == 0.0f)) == 0) {
+      const f4 U = mma4(*reinterpret_cast<const f4*>(&o.x[at]), u, f4{0, 0, 0, 0});
+      f4 bc[4];
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         const f4 pc = *reinterpret_cast<const f4*>(&o.pc[16 * j + 4 * g]);
+        bc[j] = *reinterpret_cast<const f4*>(&o.bcT[16 * j * LDT + at]);
 #pragma unroll
-        for (int v = 0; v < 4; v++) S[j][v] *= pc[v];
-        const int key = (16 * j + l16) * LDT + 4 * g;
-        S[j] = mma4(*reinterpret_cast<const f4*>(&o.kcT[key]), Vc, S[j]);
-        S[j] = mma4(*reinterpret_cast<const f4*>(&o.bcT[key]), U, S[j]);
+        for (int v = 0; v < 4; v++) S[j][v] = __builtin_fmaf(S[j][v], pc[v], z[j][v]);
       }
-      y = mma4(*reinterpret_cast<const f4*>(&o.nb[at]), U, y);
+      const f4 nb = *reinterpret_cast<const f4*>(&o.nb[at]);
+#pragma unroll
+      for (int v = 0; v < 4; v++) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          S[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(bc[j][v], U[v], S[j], 0, 0, 0);
+        y = __builtin_amdgcn_mfma_f32_16x16x4f32(nb[v], U[v], y, 0, 0, 0);
+      }
 #pragma unroll
       for (int v = 0; v < 4; v++) {
         const int t = t0 + 4 * g + v;
@@ -416,13 +526,13 @@ k_wkv_chunk(const WkvArgs a) {
 
 template <typename T>
 void launch(const WkvArgs& a, hipStream_t s) {
-  if (a.T - a.sequences < 32) {
-    hipLaunchKernelGGL((k_wkv_seq<T>), dim3(a.sequences, a.H), dim3(256), 0, s, a);
-  } else if ((long long)a.sequences * a.H >= 256) {
-    hipLaunchKernelGGL((k_wkv_chunk<T, 4>), dim3(a.sequences, a.H), dim3(64 * 7), 0, s, a);
-  } else {
-    hipLaunchKernelGGL((k_wkv_chunk<T, 1>), dim3(a.sequences, a.H * 4), dim3(64 * 4), 0, s, a);
-  }
+  const unsigned heads = (unsigned)a.sequences * a.H;
+  if (a.T - a.sequences < 32)
+    hipLaunchKernelGGL((k_wkv_seq<T>), dim3(heads), dim3(256), 0, s, a);
+  else if (heads >= 256)
+    hipLaunchKernelGGL((k_wkv_chunk<T, 4>), dim3(heads), dim3(64 * 7), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_wkv_chunk<T, 1>), dim3(heads * 4), dim3(64 * 4), 0, s, a);
 }
 
 }  // namespace

@@ -279,6 +279,9 @@ rq_status rq_gemm_smallm_noalloc(const void* qweight, const void* scales, const 
  * call must not share a slot unless one is empty.
  */
 
+/* Largest number of sequences in a call of rq_shift or rq_wkv7. */
+#define RQ_MAX_SEQUENCES 65536
+
 /* Largest n of rq_shift. */
 #define RQ_SHIFT_MAX_MIXES 8
 
@@ -292,7 +295,7 @@ rq_status rq_gemm_smallm_noalloc(const void* qweight, const void* scales, const 
  *   out: binary16 [n][T][D], computed in binary32 and rounded once.
  * Rows of x that no sequence covers leave unspecified rows in out.
  * Shape rules: T >= 1, D >= 8, D % 8 == 0, 1 <= n <= RQ_SHIFT_MAX_MIXES,
- * sequences >= 1, nslots >= 0 (at least `sequences` when slots is NULL; state
+ * 1 <= sequences <= RQ_MAX_SEQUENCES, nslots >= 0 (at least `sequences` when slots is NULL; state
  * may be NULL when nslots is 0, which needs slots).
  */
 rq_status rq_shift(const void* x, const void* mu, void* state, void* out, const int* offsets,
@@ -319,7 +322,8 @@ typedef enum { RQ_TYPE_F32 = 0, RQ_TYPE_F16 = 1 } rq_type;
  *   covers are not written.
  * All sums and the state are binary32.  Non-finite inputs reach the outputs of
  * their own token and later ones only.
- * Shape rules: T >= 1, 1 <= H <= 4096, sequences >= 1, nslots as for rq_shift.
+ * Shape rules: T >= 1, 1 <= H <= 4096, sequences and nslots as for
+ * rq_shift.
  */
 rq_status rq_wkv7(const void* r, const void* w, const void* k, const void* v, const void* kappa,
                   const void* eta, int input_type, float* state, float* y, const int* offsets,
