@@ -137,17 +137,17 @@ constexpr int PRODUCERS = 3;
 // producers also make the products with V, which leaves the state wave with
 // what depends on the state.
 template <int NR>
-struct ChunkOps {
+struct alignas(16) ChunkOps {
   float ah[CH * LDR];   // kappa_t o P_{t-1}
   float rh[CH * LDR];   // r_t o P_t
   float bcT[HD * LDT];  // [key][token]
   float x[CH * LDT];    // (I - Mb)^-1
   float nb[CH * LDT];
   float pc[HD];         // P_16
-  int bad;              // a value that is not finite: token by token
-  // NR = 4: kcT and the matrices that multiply V; NR = 1: the products
+  // NR > 1: kcT and the matrices that multiply V; NR = 1: the products
   // themselves, as accumulators [j][lane] of kc^T V, then Mk V and Nk V
   float v[NR == 1 ? 6 * 256 : HD * LDT + 2 * CH * LDT];
+  int bad;              // a value that is not finite: token by token
   __device__ __forceinline__ float* kcT() { return v; }
   __device__ __forceinline__ float* mk() { return v + HD * LDT; }
   __device__ __forceinline__ float* nk() { return v + HD * LDT + CH * LDT; }
@@ -184,11 +184,15 @@ __device__ __forceinline__ f4 mma4(const f4& a, const f4& b, f4 c) {
 
 // Barrier that waits for this wave's LDS accesses only: loads of later chunks
 // and stores of outputs stay in flight across it (s_waitcnt with lgkmcnt 0,
-// the other counters at their maxima).
+// the other counters at their maxima).  Nothing is scheduled across it: what
+// the compiler moved over a barrier to fill one wave's gaps made another wave's
+// step longer.
 __device__ __forceinline__ void step_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
   __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
@@ -221,24 +225,33 @@ struct ChunkIn {
   }
 };
 
-// (tokens, keys) x V: kc^T V into z, Mk V into mv, Nk V into nv.
-__device__ __forceinline__ void v_products(const float* kcT, const float* mk, const float* nk,
-                                           const f4& V, f4* z, f4* mv, f4* nv) {
-  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-  const int at = l16 * LDT + 4 * g;
+// z = kc^T V, from kcT [key][token] in LDS
+__device__ __forceinline__ void keys_times_v(const float* kcT, const f4& V, f4* z) {
+  const int lane = threadIdx.x & 63;
   f4 k[4];
 #pragma unroll
-  for (int j = 0; j < 4; j++) k[j] = *reinterpret_cast<const f4*>(&kcT[16 * j * LDT + at]);
+  for (int j = 0; j < 4; j++) {
+    k[j] = *reinterpret_cast<const f4*>(&kcT[(16 * j + (lane & 15)) * LDT + 4 * (lane >> 4)]);
+    z[j] = f4{0, 0, 0, 0};
+  }
+  // four independent sums, so no MFMA waits for the one before it
+#pragma unroll
+  for (int v = 0; v < 4; v++)
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      z[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(k[j][v], V[v], z[j], 0, 0, 0);
+}
+// mv = Mk V, nv = Nk V
+__device__ __forceinline__ void tokens_times_v(const float* mk, const float* nk, const f4& V,
+                                               f4* mv, f4* nv) {
+  const int lane = threadIdx.x & 63, at = (lane & 15) * LDT + 4 * (lane >> 4);
   const f4 m = *reinterpret_cast<const f4*>(&mk[at]);
   const f4 n = *reinterpret_cast<const f4*>(&nk[at]);
-  // six independent sums, so no MFMA waits for the one before it
+  *mv = *nv = f4{0, 0, 0, 0};
 #pragma unroll
   for (int v = 0; v < 4; v++) {
     *mv = __builtin_amdgcn_mfma_f32_16x16x4f32(m[v], V[v], *mv, 0, 0, 0);
     *nv = __builtin_amdgcn_mfma_f32_16x16x4f32(n[v], V[v], *nv, 0, 0, 0);
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-      z[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(k[j][v], V[v], z[j], 0, 0, 0);
   }
 }
 
@@ -308,8 +321,23 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, flo
     }
     if constexpr (NR == 1) V = vin.get(t0, hi);
     if (c + PRODUCERS < n) fetch(c + PRODUCERS);  // two steps ahead of its use
+    float* const kcT = NR == 1 ? scratch : ops[c & 1].kcT();
+    f4 z[4];
+    if constexpr (NR == 1) {
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+#pragma unroll
+        for (int v = 0; v < 4; v++)
+          kcT[(16 * j + 4 * g + v) * LDT + l16] = kh[j][v] * pc[j][v];
+      // this wave's own writes, read back transposed (LDS keeps a wave's order)
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      keys_times_v(kcT, V, z);
+    }
     step_barrier();
     // segment 2: the four products, rows t = 4 g + v, columns s = lane mod 16
+    // (kept on this side of the barrier: the segments are of about one length)
+#pragma unroll
+    for (int j = 0; j < 4; j++) asm volatile("" : "+v"(ah[j]), "+v"(rh[j]));
     f4 mb = {0, 0, 0, 0}, mk = mb, nb = mb, nk = mb;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -323,7 +351,6 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, flo
     }
     // a value that is not finite leaves none of its row's or column's sums finite
     float zero = 0.0f;
-    float* const kcT = NR == 1 ? scratch + CH * LDT : ops[c & 1].kcT();
     float* const mks = kcT + HD * LDT;
     float* const nks = mks + CH * LDT;
 #pragma unroll
@@ -333,7 +360,6 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, flo
       zero = __builtin_fmaf(nb[v], 0.0f, __builtin_fmaf(nk[v], 0.0f, zero));
       if (l16 >= t) mb[v] = mk[v] = 0.0f;
       if (l16 > t) nb[v] = nk[v] = 0.0f;
-      scratch[t * LDT + l16] = mb[v];
     }
     step_barrier();
     // segment 3: the rest, into the chunk's buffer
@@ -343,7 +369,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, flo
 #pragma unroll
       for (int v = 0; v < 4; v++) {
         const int key = 16 * j + 4 * g + v;
-        kcT[key * LDT + l16] = kh[j][v] * pc[j][v];
+        if constexpr (NR > 1) kcT[key * LDT + l16] = kh[j][v] * pc[j][v];
         o.bcT[key * LDT + l16] = bh[j][v] * pc[j][v];
       }
       *reinterpret_cast<f4*>(&o.ah[l16 * LDR + 16 * j + 4 * g]) = ah[j];
@@ -358,12 +384,9 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, flo
       o.nb[at] = nb[v];
     }
     if constexpr (NR == 1) {
-      // this wave's own writes, read back transposed (LDS keeps a wave's order)
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
-      f4 z[4], mv = {0, 0, 0, 0}, nv = mv;
-#pragma unroll
-      for (int j = 0; j < 4; j++) z[j] = f4{0, 0, 0, 0};
-      v_products(kcT, mks, nks, V, z, &mv, &nv);
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);  // as above
+      f4 mv, nv;
+      tokens_times_v(mks, nks, V, &mv, &nv);
       f4* dst = reinterpret_cast<f4*>(o.v) + lane;
 #pragma unroll
       for (int j = 0; j < 4; j++) dst[64 * j] = z[j];
@@ -372,19 +395,22 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, flo
 #pragma unroll
       for (int v = 0; v < 4; v++) zero = __builtin_fmaf(z[0][v], 0.0f, zero);
     }
-    // column l16 of X by forward substitution
+    // column l16 of X by forward substitution; Mb[t][s] is in lane 16 (t / 4) +
+    // s and goes through a scalar register
     float x[CH];
 #pragma unroll
-    for (int t = 0; t < CH; t++) {
-      x[t] = l16 == t ? 1.0f : 0.0f;
+    for (int t = 0; t < CH; t++) x[t] = l16 == t ? 1.0f : 0.0f;
 #pragma unroll
-      for (int s4 = 0; s4 < t; s4 += 4) {
-        const f4 m = *reinterpret_cast<const f4*>(&scratch[t * LDT + s4]);
+    for (int s = 0; s < CH - 1; s++) {
 #pragma unroll
-        for (int s = s4; s < s4 + 4 && s < t; s++) x[t] = __builtin_fmaf(m[s - s4], x[s], x[t]);
+      for (int t = s + 1; t < CH; t++) {
+        const float m = __builtin_bit_cast(
+            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mb[t % 4]), 16 * (t / 4) + s));
+        x[t] = __builtin_fmaf(m, x[s], x[t]);
       }
-      o.x[t * LDT + l16] = x[t];
     }
+#pragma unroll
+    for (int t = 0; t < CH; t++) o.x[t * LDT + l16] = x[t];
     const bool bad = __ballot(!(zero == 0.0f)) != 0;
     if (lane == 0) o.bad = bad;
     step_barrier();
@@ -397,7 +423,8 @@ template <typename T, int NR>
 __global__ void __launch_bounds__(64 * (NR + PRODUCERS))
 k_wkv_chunk(const WkvArgs a) {
   __shared__ __align__(16) ChunkOps<NR> ops[2];
-  __shared__ __align__(16) float scratch[PRODUCERS][(NR == 1 ? 3 * CH + HD : CH) * LDT];
+  // the producers' own copies of kcT, mk and nk
+  __shared__ __align__(16) float scratch[NR == 1 ? PRODUCERS : 1][NR == 1 ? (2 * CH + HD) * LDT : 1];
   // heads are the fast index: a sequence's workgroups go to all XCDs
   constexpr int TILES = 4 / NR;
   const int q = blockIdx.x / (a.H * TILES), h = blockIdx.x % (a.H * TILES) / TILES;
@@ -407,9 +434,9 @@ k_wkv_chunk(const WkvArgs a) {
   const size_t ld = (size_t)a.H * HD, base = (size_t)h * HD;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-  const int i = 16 * (NR == 4 ? wave % 4 : blockIdx.x % 4) + l16;  // the lane's value row
+  const int i = 16 * (blockIdx.x % TILES * NR + wave % NR) + l16;  // the lane's value row
   if (wave >= NR) {
-    produce<T, NR>(a, ops, scratch[wave - NR], wave - NR, lo, hi, base, ld, i);
+    produce<T, NR>(a, ops, scratch[NR == 1 ? wave - NR : 0], wave - NR, lo, hi, base, ld, i);
     return;
   }
   const int slot = a.slots ? a.slots[q] : q;
@@ -424,22 +451,43 @@ k_wkv_chunk(const WkvArgs a) {
   const T* vp = static_cast<const T*>(a.v) + base + i;
   float* yp = a.y + base + i;
   ChunkV<T> vin;
-  if constexpr (NR == 4) vin.load(vp, ld, lo, hi);
+  if constexpr (NR > 1) vin.load(vp, ld, lo, hi);
   for (int s = 0; s < 3; s++) step_barrier();
+  // the state has arrived before the loop, so that no wait inside it stands
+  // for these loads (and with them for the stores of y)
+#pragma unroll
+  for (int j = 0; j < 4; j++) asm volatile("" : "+v"(S[j]));
   for (int c = 0; c < n; c++) {
     ChunkOps<NR>& o = ops[c & 1];
     const int t0 = lo + c * CH;
     const int at = l16 * LDT + 4 * g;
-    f4 u = {0, 0, 0, 0}, y = u, z[4];
-    float zero = 0.0f;
-    if constexpr (NR == 4) {
+    f4 u, y, z[4], ah[4], rh[4], bc[4], pc[4];
+    // all of the chunk's operands are asked for at once
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      ah[j] = *reinterpret_cast<const f4*>(&o.ah[l16 * LDR + 16 * j + 4 * g]);
+      rh[j] = *reinterpret_cast<const f4*>(&o.rh[l16 * LDR + 16 * j + 4 * g]);
+    }
+    const int bad = o.bad;
+    const f4 x = *reinterpret_cast<const f4*>(&o.x[at]);
+    const f4 nb = *reinterpret_cast<const f4*>(&o.nb[at]);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      bc[j] = *reinterpret_cast<const f4*>(&o.bcT[16 * j * LDT + at]);
+      pc[j] = *reinterpret_cast<const f4*>(&o.pc[16 * j + 4 * g]);
+    }
+    float zero = 0.0f;  // NaN where a state is not finite
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+#pragma unroll
+      for (int v = 0; v < 4; v++) zero = __builtin_fmaf(S[j][v], 0.0f, zero);
+    if constexpr (NR > 1) {
       const f4 V = vin.get(t0, hi);
       if (c + 1 < n) vin.load(vp, ld, t0 + CH, hi);
 #pragma unroll
-      for (int j = 0; j < 4; j++) z[j] = u;
-      v_products(o.kcT(), o.mk(), o.nk(), V, z, &u, &y);
-#pragma unroll
-      for (int v = 0; v < 4; v++) zero = __builtin_fmaf(z[0][v], 0.0f, zero);
+      for (int v = 0; v < 4; v++) zero = __builtin_fmaf(V[v], 0.0f, zero);
+      keys_times_v(o.kcT(), V, z);
+      tokens_times_v(o.mk(), o.nk(), V, &u, &y);
     } else {
       const f4* src = reinterpret_cast<const f4*>(o.v) + lane;
 #pragma unroll
@@ -449,28 +497,18 @@ k_wkv_chunk(const WkvArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      const f4 ah = *reinterpret_cast<const f4*>(&o.ah[l16 * LDR + 16 * j + 4 * g]);
-      const f4 rh = *reinterpret_cast<const f4*>(&o.rh[l16 * LDR + 16 * j + 4 * g]);
 #pragma unroll
       for (int v = 0; v < 4; v++) {
-        u = __builtin_amdgcn_mfma_f32_16x16x4f32(ah[v], S[j][v], u, 0, 0, 0);
-        y = __builtin_amdgcn_mfma_f32_16x16x4f32(rh[v], S[j][v], y, 0, 0, 0);
+        u = __builtin_amdgcn_mfma_f32_16x16x4f32(ah[j][v], S[j][v], u, 0, 0, 0);
+        y = __builtin_amdgcn_mfma_f32_16x16x4f32(rh[j][v], S[j][v], y, 0, 0, 0);
       }
     }
-    // a state that is not finite leaves none of its row's u finite
+    if (!bad && __ballot(!(zero == 0.0f)) == 0) {
+      const f4 U = mma4(x, u, f4{0, 0, 0, 0});
 #pragma unroll
-    for (int v = 0; v < 4; v++) zero = __builtin_fmaf(u[v], 0.0f, zero);
-    if (!o.bad && __ballot(!(zero == 0.0f)) == 0) {
-      const f4 U = mma4(*reinterpret_cast<const f4*>(&o.x[at]), u, f4{0, 0, 0, 0});
-      f4 bc[4];
+      for (int j = 0; j < 4; j++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const f4 pc = *reinterpret_cast<const f4*>(&o.pc[16 * j + 4 * g]);
-        bc[j] = *reinterpret_cast<const f4*>(&o.bcT[16 * j * LDT + at]);
-#pragma unroll
-        for (int v = 0; v < 4; v++) S[j][v] = __builtin_fmaf(S[j][v], pc[v], z[j][v]);
-      }
-      const f4 nb = *reinterpret_cast<const f4*>(&o.nb[at]);
+        for (int v = 0; v < 4; v++) S[j][v] = __builtin_fmaf(S[j][v], pc[j][v], z[j][v]);
 #pragma unroll
       for (int v = 0; v < 4; v++) {
 #pragma unroll
@@ -478,10 +516,14 @@ k_wkv_chunk(const WkvArgs a) {
           S[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(bc[j][v], U[v], S[j], 0, 0, 0);
         y = __builtin_amdgcn_mfma_f32_16x16x4f32(nb[v], U[v], y, 0, 0, 0);
       }
+      float* yt = yp + (size_t)(t0 + 4 * g) * ld;
+      if (t0 + CH <= hi) {
 #pragma unroll
-      for (int v = 0; v < 4; v++) {
-        const int t = t0 + 4 * g + v;
-        if (t < hi) yp[(size_t)t * ld] = y[v];
+        for (int v = 0; v < 4; v++) yt[v * ld] = y[v];
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; v++)
+          if (t0 + 4 * g + v < hi) yt[v * ld] = y[v];
       }
     } else {
       // a value that is not finite must not reach earlier tokens through
@@ -524,15 +566,23 @@ k_wkv_chunk(const WkvArgs a) {
   }
 }
 
+template <typename T, int NR>
+void launch_chunks(const WkvArgs& a, unsigned heads, hipStream_t s) {
+  hipLaunchKernelGGL((k_wkv_chunk<T, NR>), dim3(heads * (4 / NR)), dim3(64 * (NR + PRODUCERS)), 0,
+                     s, a);
+}
+
 template <typename T>
 void launch(const WkvArgs& a, hipStream_t s) {
   const unsigned heads = (unsigned)a.sequences * a.H;
   if (a.T - a.sequences < 32)
     hipLaunchKernelGGL((k_wkv_seq<T>), dim3(heads), dim3(256), 0, s, a);
-  else if (heads >= 256)
-    hipLaunchKernelGGL((k_wkv_chunk<T, 4>), dim3(heads), dim3(64 * 7), 0, s, a);
+  else if (heads <= 80)
+    launch_chunks<T, 1>(a, heads, s);
+  else if (heads < 256)
+    launch_chunks<T, 2>(a, heads, s);
   else
-    hipLaunchKernelGGL((k_wkv_chunk<T, 1>), dim3(heads * 4), dim3(64 * 4), 0, s, a);
+    launch_chunks<T, 4>(a, heads, s);
 }
 
 }  // namespace
