@@ -274,6 +274,32 @@ struct ChunkV {
   }
 };
 
+// The value that lanes 16 G .. 16 G + 15 hold, in every row of 16 lanes.
+template <int G>
+__device__ __forceinline__ float row_of(float v) {
+  const u32 u = __builtin_bit_cast(u32, v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);  // rows 0 0 2 2, 1 1 3 3
+  const u32 w = a[G & 1];
+  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  const u32 r = b[G >> 1];
+  return __builtin_bit_cast(float, r);
+}
+// Rows after S of x += column S of the strictly lower triangular m times row
+// S of x (accumulator layout: rows 4 g + v, columns lane mod 16), then the
+// rows after S + 1, and so on.
+template <int S>
+__device__ __forceinline__ void eliminate(const f4& m, f4& x) {
+  if constexpr (S < CH - 1) {
+    const float xs = row_of<S / 4>(x[S % 4]);
+#pragma unroll
+    for (int v = 0; v < 4; v++) {
+      const float mv = m[v];
+      x[v] = __builtin_fmaf(dpp_mov<0x150 + S>(mv), xs, x[v]);  // lane S of the row
+    }
+    eliminate<S + 1>(m, x);
+  }
+}
+
 template <typename T, int NR>
 __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, float* scratch,
                                         int p, int lo, int hi, size_t base, size_t ld, int row) {
@@ -361,6 +387,16 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, flo
       if (l16 >= t) mb[v] = mk[v] = 0.0f;
       if (l16 > t) nb[v] = nk[v] = 0.0f;
     }
+    f4 mv, nv;
+    if constexpr (NR == 1) {
+#pragma unroll
+      for (int v = 0; v < 4; v++) {
+        mks[(4 * g + v) * LDT + l16] = mk[v];
+        nks[(4 * g + v) * LDT + l16] = nk[v];
+      }
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);  // as above
+      tokens_times_v(mks, nks, V, &mv, &nv);
+    }
     step_barrier();
     // segment 3: the rest, into the chunk's buffer
     ChunkOps<NR>& o = ops[c & 1];
@@ -379,14 +415,13 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, flo
 #pragma unroll
     for (int v = 0; v < 4; v++) {
       const int at = (4 * g + v) * LDT + l16;
-      mks[at] = mk[v];
-      nks[at] = nk[v];
+      if constexpr (NR > 1) {
+        mks[at] = mk[v];
+        nks[at] = nk[v];
+      }
       o.nb[at] = nb[v];
     }
     if constexpr (NR == 1) {
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);  // as above
-      f4 mv, nv;
-      tokens_times_v(mks, nks, V, &mv, &nv);
       f4* dst = reinterpret_cast<f4*>(o.v) + lane;
 #pragma unroll
       for (int j = 0; j < 4; j++) dst[64 * j] = z[j];
@@ -395,22 +430,14 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, flo
 #pragma unroll
       for (int v = 0; v < 4; v++) zero = __builtin_fmaf(z[0][v], 0.0f, zero);
     }
-    // column l16 of X by forward substitution; Mb[t][s] is in lane 16 (t / 4) +
-    // s and goes through a scalar register
-    float x[CH];
+    // X by forward substitution: row s is final once the rows before it have
+    // been taken off; it goes to all lanes, and every row takes its share
+    f4 x;
 #pragma unroll
-    for (int t = 0; t < CH; t++) x[t] = l16 == t ? 1.0f : 0.0f;
+    for (int v = 0; v < 4; v++) x[v] = l16 == 4 * g + v ? 1.0f : 0.0f;
+    eliminate<0>(mb, x);
 #pragma unroll
-    for (int s = 0; s < CH - 1; s++) {
-#pragma unroll
-      for (int t = s + 1; t < CH; t++) {
-        const float m = __builtin_bit_cast(
-            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mb[t % 4]), 16 * (t / 4) + s));
-        x[t] = __builtin_fmaf(m, x[s], x[t]);
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < CH; t++) o.x[t * LDT + l16] = x[t];
+    for (int v = 0; v < 4; v++) o.x[(4 * g + v) * LDT + l16] = x[v];
     const bool bad = __ballot(!(zero == 0.0f)) != 0;
     if (lane == 0) o.bad = bad;
     step_barrier();
