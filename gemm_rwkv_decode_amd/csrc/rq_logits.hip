@@ -47,12 +47,14 @@ __device__ __forceinline__ u32 order_of(float z) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// Contraction is off: freq * n and the subtraction round on their own.
 __device__ __forceinline__ float apply_one(float z, u32 c, float rep, float freq, float pres) {
+#pragma clang fp contract(off)
   if (c == 0) return z;
-  z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+  z = z > 0.0f ? z / rep : z * rep;
   const u32 n = c & ~SEEN;
-  z = __fsub_rn(z, __fmul_rn(freq, (float)n));
-  return n ? __fsub_rn(z, pres) : z;
+  z = z - freq * (float)n;
+  return n ? z - pres : z;
 }
 
 template <int SL>
@@ -132,7 +134,7 @@ k_logits(const LogitsArgs a, u64* best, u32* arrived) {
       const u32x4 b = *reinterpret_cast<const u32x4*>(ent + e);
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        if (b[i]) z[q][i] = __fadd_rn(z[q][i], a.bias[b[i] - 1]);
+        if (b[i]) z[q][i] += a.bias[b[i] - 1];
     }
 #pragma unroll
     for (int i = 0; i < 4; i++)
