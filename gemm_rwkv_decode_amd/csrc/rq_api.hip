@@ -17,7 +17,7 @@
 
 static_assert(RQ_WKV_HEAD == rq::WKV_HEAD && RQ_LORA_MAX_RANK == rq::LORA_MAX_RANK &&
               RQ_LORA_MAX_BATCH == rq::LORA_BATCH && RQ_LOGITS_MAX_M == rq::LOGITS_MAX_M &&
-              RQ_LOGITS_MAX_M * 12 <= RQ_LOGITS_WORKSPACE_BYTES,
+              RQ_LOGITS_MAX_M * 16 <= RQ_LOGITS_WORKSPACE_BYTES,
               "the interface's limits are the kernels'");
 
 namespace rq {

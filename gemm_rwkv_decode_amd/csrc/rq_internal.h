@@ -151,9 +151,8 @@ struct LogitsArgs {
   const int* mask_ids;
   int M, V, history_len, bias_len, nmasks;
 };
-int logits_slices(int V);
-// ws: LOGITS_MAX_M 8-byte maxima, then as many 4-byte counters, zero between
-// launches (unused with one slice or without tokens)
+// ws: 16 bytes per row (LOGITS_MAX_M of them), zero between launches (unused
+// without tokens)
 hipError_t launch_logits(const LogitsArgs& a, void* ws, hipStream_t s);
 
 }  // namespace rq
