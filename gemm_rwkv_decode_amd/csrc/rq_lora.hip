@@ -18,6 +18,8 @@
 // binary16: it is split into two binary16 parts, t = 2^e (hi + lo), with e the
 // row's own power of two, so B t loses nothing above 2^-22 of the row's largest
 // t and cannot overflow for a large x.
+#include <algorithm>
+
 #include "rq_common.h"
 #include "rq_internal.h"
 
@@ -25,7 +27,7 @@ namespace rq {
 namespace {
 
 constexpr int ROWS = 64;  // rows of a block: one per lane
-constexpr int UP_N = 256; // outputs of a workgroup of k_lora_up
+constexpr long long LORA_WORKGROUPS = 1024;
 
 typedef unsigned long long u64;
 
@@ -36,26 +38,49 @@ struct Group {
   int off, r;  // its first A row and its rank (0: no adapter)
 };
 
-__device__ __forceinline__ Group find_group(const LoraArgs& a, int base, int g) {
+struct Rows {
+  int id;       // of the lane's row; a.adapters: none
+  int offsets;  // offsets[lane] where all of them fit in a wave
+  u64 same;     // the rows with the lane's id
+  u64 leaders;  // the first row of every id
+};
+
+__device__ __forceinline__ Rows load_rows(const LoraArgs& a, int base) {
   const int lane = threadIdx.x & 63;
   const bool in = base + lane < a.M;
-  int id = in ? a.ids[base + lane] : 0;
-  if (id < 0 || id > a.adapters) id = a.adapters;
-  u64 same = __ballot(in);
-  const u64 all = same;
+  Rows q;
+  q.id = in ? a.ids[base + lane] : 0;
+  // asked for beside the ids, not after them
+  q.offsets = a.adapters < 64 ? a.offsets[min(lane, a.adapters)] : 0;
+  if (q.id < 0 || q.id > a.adapters) q.id = a.adapters;
+  q.same = __ballot(in);
   for (int b = 0; (a.adapters >> b) != 0; b++) {
-    const u64 set = __ballot((id >> b) & 1);
-    same &= ((id >> b) & 1) ? set : ~set;
+    const u64 set = __ballot((q.id >> b) & 1);
+    q.same &= ((q.id >> b) & 1) ? set : ~set;
   }
-  u64 leaders = __ballot(in && (same & ((1ull << lane) - 1)) == 0) & all;
+  q.leaders = __ballot(in && (q.same & ((1ull << lane) - 1)) == 0);
+  return q;
+}
+
+// The g-th distinct adapter of the block.
+__device__ __forceinline__ Group find_group(const LoraArgs& a, const Rows& w, int g) {
+  u64 leaders = w.leaders;
   for (int i = 0; i < g; i++) leaders &= leaders - 1;
   Group q{0, 0, 0, 0};
   if (!leaders) return q;
   const int lead = __builtin_amdgcn_readfirstlane(__builtin_ctzll(leaders));
-  q.id = __builtin_amdgcn_readlane(id, lead);
-  q.rows = __ballot(in && id == q.id);
+  q.id = __builtin_amdgcn_readlane(w.id, lead);
+  q.rows = (u64)(u32)__builtin_amdgcn_readlane((int)(u32)w.same, lead) |
+           (u64)(u32)__builtin_amdgcn_readlane((int)(u32)(w.same >> 32), lead) << 32;
   if (q.id < a.adapters) {
-    const int o = a.offsets[q.id], e = a.offsets[q.id + 1];
+    int o, e;
+    if (a.adapters < 64) {
+      o = __builtin_amdgcn_readlane(w.offsets, q.id);
+      e = __builtin_amdgcn_readlane(w.offsets, q.id + 1);
+    } else {
+      o = a.offsets[q.id];
+      e = a.offsets[q.id + 1];
+    }
     // anything but a whole rank inside the pool counts as no adapter
     if (o >= 0 && e > o && e <= a.total_rank && e - o <= a.max_rank && o % 8 == 0 &&
         (e - o) % 8 == 0) {
@@ -73,188 +98,298 @@ __device__ __forceinline__ int list_rows(u64 rows, unsigned char* list) {
   return __popcll(rows);
 }
 
-// t of one rank tile (16 A rows) for a group's rows, over one K range.  The
-// four waves split the range; their sums are added in wave order through LDS.
-// MFMA: A operand = adapter rows, B operand = activation rows, so a lane ends
-// with four consecutive rank entries of one row.
-__global__ void __launch_bounds__(256)
-k_lora_down(const LoraBatch bt, const LoraArgs a) {
-  __shared__ unsigned char list[ROWS];
-  __shared__ f4 part[4][4][64];
-  const int blocks = (a.M + ROWS - 1) / ROWS;
-  const LoraProblem& p = bt.p[blockIdx.z / blocks];
-  const int base = (blockIdx.z % blocks) * ROWS;
-  const int rt = blockIdx.x / a.splits, sp = blockIdx.x % a.splits;
-  const Group g = find_group(a, base, blockIdx.y);
-  if (rt * 16 >= g.r) return;
-  const int cnt = list_rows(g.rows, list);
-  __syncthreads();
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int l16 = lane & 15, h = lane >> 4;
-  const int tiles = (cnt + 15) / 16;
-  const int K = p.K;
-  const int steps = (K + 31) / 32;
-  const int ranges = 4 * a.splits, mine = sp * 4 + wave;
-  const int s0 = (int)((long long)steps * mine / ranges);
-  const int s1 = (int)((long long)steps * (mine + 1) / ranges);
-  // rows past the rank or the group repeat a valid one; their results are not stored
-  const _Float16* ap = p.a + (size_t)(g.off + min(rt * 16 + l16, g.r - 1)) * K + 8 * h;
-  const _Float16* xp[4];
+// Products of 16 A rows with TILES tiles of 16 activation rows over a wave's
+// share of K: rounds of 128 columns, every `stride`-th one.  MFMA: A operand =
+// adapter rows, B operand = activation rows, so a lane ends with four
+// consecutive rank entries of one row.  The 16-byte loads of U rounds are asked
+// for before their first product.  (Rounds are
+// dealt out in turn because rows are a power of two apart: waves that walk
+// ranges of their own would all ask the same memory channel.)
+template <int TILES, int U>
+__device__ __forceinline__ void down_rounds(const _Float16* ap, const _Float16* const* xp, int K,
+                                            int first, int stride, f4* acc) {
+  const int h = (threadIdx.x & 63) >> 4;
+  const int rounds = (K + 127) / 128;
+  for (int q = first; q < rounds; q += U * stride) {
+    h8 av[U][4], xv[U][4][TILES];
 #pragma unroll
-  for (int i = 0; i < 4; i++)
-    xp[i] = p.x + (size_t)(base + list[min(i * 16 + l16, cnt - 1)]) * K + 8 * h;
-  f4 acc[4];
+    for (int u = 0; u < U; u++) {
 #pragma unroll
-  for (int i = 0; i < 4; i++) acc[i] = f4{0, 0, 0, 0};
-  for (int s = s0; s < s1; s++) {
-    const int k = s * 32;
-    const bool in = k + 8 * h < K;  // K is a multiple of 8
-    h8 av = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (in) av = *reinterpret_cast<const h8*>(ap + k);
+      for (int s = 0; s < 4; s++) {
+        const int k = (q + u * stride) * 128 + s * 32;
+        const bool in = k + 8 * h < K;  // K is a multiple of 8
+        av[u][s] = h8{0, 0, 0, 0, 0, 0, 0, 0};
+        if (in) av[u][s] = *reinterpret_cast<const h8*>(ap + k);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      if (i < tiles) {
-        h8 xv = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (in) xv = *reinterpret_cast<const h8*>(xp[i] + k);
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, xv, acc[i], 0, 0, 0);
+        for (int i = 0; i < TILES; i++) {
+          xv[u][s][i] = h8{0, 0, 0, 0, 0, 0, 0, 0};
+          if (in) xv[u][s][i] = *reinterpret_cast<const h8*>(xp[i] + k);
+        }
       }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < 4; i++)
-    if (i < tiles) part[wave][i][lane] = acc[i];
-  __syncthreads();
-  // wave i finishes row tile i
-  if (wave >= tiles) return;
-  f4 sum = part[0][wave][lane];
+    for (int u = 0; u < U; u++)
 #pragma unroll
-  for (int w = 1; w < 4; w++) sum += part[w][wave][lane];
-  const int j = wave * 16 + l16;
-  if (j < cnt) {
-    const size_t row = ((size_t)(blockIdx.z / blocks) * a.splits + sp) * a.M + base + list[j];
-    *reinterpret_cast<f4*>(a.ws + row * a.rank_ld + rt * 16 + 4 * h) = sum;
+      for (int s = 0; s < 4; s++)
+#pragma unroll
+        for (int i = 0; i < TILES; i++)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av[u][s], xv[u][s][i], acc[i], 0, 0, 0);
   }
 }
 
-// The group's rows times B: 256 outputs a workgroup, 64 a wave.
-__global__ void __launch_bounds__(256)
-k_lora_up(const LoraBatch bt, const LoraArgs a) {
-  constexpr int LD = LORA_MAX_RANK + 8;  // halves; rows start 16 bytes apart in bank order
+// t of one rank tile (16 A rows) for a group's rows, over one share of K, TB
+// tiles of 16 rows at a time.  The four waves' sums are added in wave order
+// through LDS.
+template <int TB>
+__global__ void __launch_bounds__(256, TB == 1 ? 4 : 3)
+k_lora_down(const LoraBatch bt, const LoraArgs a) {
   __shared__ unsigned char list[ROWS];
-  __shared__ __align__(16) _Float16 hi[ROWS][LD], lo[ROWS][LD];
-  __shared__ float back[ROWS];  // 2^e s_i
+  __shared__ f4 part[4][TB][64];
   const int blocks = (a.M + ROWS - 1) / ROWS;
-  const int pi = blockIdx.z / blocks;
+  const int pi = blockIdx.y / blocks;
   const LoraProblem& p = bt.p[pi];
-  const int base = (blockIdx.z % blocks) * ROWS;
+  const int base = (blockIdx.y % blocks) * ROWS;
+  const int rt = blockIdx.x / a.splits, sp = blockIdx.x % a.splits;
+  const Rows rows = load_rows(a, base);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15, h = lane >> 4;
+  for (int gi = blockIdx.z;; gi += gridDim.z) {
+    const Group g = find_group(a, rows, gi);
+    if (!g.rows) return;
+    if (rt * 16 >= g.r) continue;
+    const int cnt = list_rows(g.rows, list);
+    __syncthreads();
+    const int K = p.K;
+    // rows past the rank or the group repeat a valid one; their results are not stored
+    const _Float16* ap = p.a + (size_t)(g.off + min(rt * 16 + l16, g.r - 1)) * K + 8 * h;
+    for (int c0 = 0; c0 < cnt; c0 += 16 * TB) {
+      const int tiles = min((cnt - c0 + 15) / 16, TB);
+      const _Float16* xp[TB];
+#pragma unroll
+      for (int i = 0; i < TB; i++)
+        xp[i] = p.x + (size_t)(base + list[min(c0 + i * 16 + l16, cnt - 1)]) * K + 8 * h;
+      f4 acc[TB];
+#pragma unroll
+      for (int i = 0; i < TB; i++) acc[i] = f4{0, 0, 0, 0};
+      const int first = sp * 4 + wave, stride = 4 * a.splits;
+      if constexpr (TB == 1) {
+        down_rounds<1, 2>(ap, xp, K, first, stride, acc);
+      } else {
+        if (tiles == 1) down_rounds<1, 2>(ap, xp, K, first, stride, acc);
+        else if (tiles == 2) down_rounds<2, 1>(ap, xp, K, first, stride, acc);
+        else down_rounds<4, 1>(ap, xp, K, first, stride, acc);
+      }
+#pragma unroll
+      for (int i = 0; i < TB; i++)
+        if (i < tiles) part[wave][i][lane] = acc[i];
+      __syncthreads();
+      // wave i finishes row tile i
+      if (wave < tiles) {
+        f4 sum = part[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < 4; w++) sum += part[w][wave][lane];
+        const int j = c0 + wave * 16 + l16;
+        if (j < cnt) {
+          const size_t row = ((size_t)pi * a.splits + sp) * a.M + base + list[j];
+          *reinterpret_cast<f4*>(a.ws + row * a.rank_ld + rt * 16 + 4 * h) = sum;
+        }
+      }
+      __syncthreads();  // before the next sums, or the next group's list
+    }
+  }
+}
+
+// The group's rows times B: 256 outputs a workgroup, 32 of them a wave.  What
+// does not depend on t (the wave's B rows, y_in) is asked for before t is put
+// together.  A tile of 16 rows goes through LDS on its way out, so that a
+// wave reads and writes y in whole rows of 1 KiB: as the products lie in its
+// lanes, an access would take 64 bytes of each of 16 rows.
+constexpr int UP_WAVES = 8;
+constexpr int UP_TILES = 2;                       // tiles of 16 outputs a wave
+constexpr int UP_N = UP_WAVES * UP_TILES * 16;    // outputs of a workgroup: 4 a lane
+constexpr int UP_LD = UP_N + 4;                   // floats between rows of a tile
+constexpr int UP_ROWS = 16 / UP_WAVES;            // rows of a tile a wave takes out
+typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+
+template <int KS, int TB>  // k steps of 32: the rank is at most 32 KS
+struct UpShared {
+  static constexpr int LD = 32 * KS + 8;  // halves; rows start 16 bytes apart in bank order
+  float out[16 * UP_LD];
+  _Float16 hi[16 * TB * LD], lo[16 * TB * LD];
+  float back[16 * TB];  // 2^x s_i
+  unsigned char list[ROWS];
+};
+
+template <int KS, int TB>
+__device__ __forceinline__ void up_body(const LoraProblem& p, const LoraArgs& a, const Group& g,
+                                        int pi, int base, int n0, int cnt, UpShared<KS, TB>& sh) {
+  constexpr int LD = UpShared<KS, TB>::LD;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int l16 = lane & 15, h = lane >> 4;
+  const int N = p.N;
+  const int nw = n0 + wave * (UP_TILES * 16);
+  const _Float16* bblock = p.b + (size_t)g.off * N;  // [N][r]
+  h8 bv[UP_TILES][KS];
+#pragma unroll
+  for (int nt = 0; nt < UP_TILES; nt++) {
+    const _Float16* bp = bblock + (size_t)min(nw + nt * 16 + l16, N - 1) * g.r + 8 * h;
+#pragma unroll
+    for (int k = 0; k < KS; k++) {
+      bv[nt][k] = h8{0, 0, 0, 0, 0, 0, 0, 0};
+      if (32 * k + 8 * h < g.r) bv[nt][k] = *reinterpret_cast<const h8*>(bp + 32 * k);
+    }
+  }
+  const int n = n0 + 4 * lane;  // this lane's outputs of a whole row
+  for (int c0 = 0; c0 < cnt; c0 += 16 * TB) {
+    const int rows = min(cnt - c0, 16 * TB), tiles = (rows + 15) / 16;
+    // rows c0 + i * 16 + wave * UP_ROWS + q of the group
+    f4 y[TB][UP_ROWS];
+#pragma unroll
+    for (int i = 0; i < TB; i++) {
+#pragma unroll
+      for (int q = 0; q < UP_ROWS; q++) {
+        const int j = c0 + i * 16 + wave * UP_ROWS + q;
+        y[i][q] = f4{0, 0, 0, 0};
+        if (p.y_in && j < cnt) {
+          const float* src = p.y_in + (size_t)(base + sh.list[j]) * N + n;
+          if (n + 4 <= N) {
+            y[i][q] = *reinterpret_cast<const f4u*>(src);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 3; c++)
+              if (n + c < N) y[i][q][c] = src[c];
+          }
+        }
+      }
+    }
+    // t of all rows: LT lanes a row, four entries a lane
+    constexpr int LT = 8 * KS, PASS = 64 * UP_WAVES / LT, PASSES = (16 * TB + PASS - 1) / PASS;
+    const int e = 4 * (tid % LT);
+    f4 t[PASSES];
+    const float* src[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; i++) {
+      t[i] = f4{0, 0, 0, 0};
+      const int j = min(c0 + i * PASS + tid / LT, cnt - 1);
+      src[i] = a.ws + ((size_t)pi * a.splits * a.M + base + sh.list[j]) * a.rank_ld + e;
+    }
+    const size_t plane = (size_t)a.M * a.rank_ld;
+    if (e < g.r) {  // ranks are multiples of 8; the shares of K in a fixed order
+#pragma unroll 2
+      for (int s = 0; s < a.splits; s++)
+#pragma unroll
+        for (int i = 0; i < PASSES; i++)
+          if (i * PASS < rows) t[i] += *reinterpret_cast<const f4*>(src[i] + s * plane);
+    }
+    const float scale = a.scales ? a.scales[g.id] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < PASSES; i++) {
+      if (i * PASS >= rows) break;
+      float big = fmaxf(fmaxf(fabsf(t[i][0]), fabsf(t[i][1])), fmaxf(fabsf(t[i][2]), fabsf(t[i][3])));
+#pragma unroll
+      for (int d = LT / 2; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor(big, d, 64));
+      // 2^x with big / 2^x in [0.5, 1); 1 where big is zero or not finite
+      int x = 0;
+      if (big > 0.0f && big < __builtin_inff()) x = __builtin_amdgcn_frexp_expf(big);
+      const int j = i * PASS + tid / LT;
+      h4 vh, vl;
+#pragma unroll
+      for (int c = 0; c < 4; c++) {
+        const float u = ldexpf(t[i][c], 8 - x);  // [2^7, 2^8): lo stays a normal binary16 longer
+        vh[c] = (_Float16)u;
+        vl[c] = __builtin_isinf(u) ? (_Float16)0.0f : (_Float16)(u - (float)vh[c]);
+      }
+      if (j < rows) {  // past the rank t is zero
+        *reinterpret_cast<h4*>(&sh.hi[j * LD + e]) = vh;
+        *reinterpret_cast<h4*>(&sh.lo[j * LD + e]) = vl;
+        if (e == 0) sh.back[j] = ldexpf(scale, x - 8);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TB; i++) {
+      if (i >= tiles) break;
+      const int j = min(i * 16 + l16, rows - 1);
+      f4 acc[UP_TILES];
+#pragma unroll
+      for (int nt = 0; nt < UP_TILES; nt++) acc[nt] = f4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < KS; k++) {
+        const h8 tl = *reinterpret_cast<const h8*>(&sh.lo[j * LD + 32 * k + 8 * h]);
+        const h8 th = *reinterpret_cast<const h8*>(&sh.hi[j * LD + 32 * k + 8 * h]);
+#pragma unroll
+        for (int nt = 0; nt < UP_TILES; nt++) {
+          acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bv[nt][k], tl, acc[nt], 0, 0, 0);
+          acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bv[nt][k], th, acc[nt], 0, 0, 0);
+        }
+      }
+      const float f = sh.back[j];
+#pragma unroll
+      for (int nt = 0; nt < UP_TILES; nt++)
+        *reinterpret_cast<f4*>(&sh.out[l16 * UP_LD + wave * (UP_TILES * 16) + nt * 16 + 4 * h]) =
+            acc[nt] * f;
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < UP_ROWS; q++) {
+        const int jr = wave * UP_ROWS + q;
+        const f4 v = y[i][q] + *reinterpret_cast<const f4*>(&sh.out[jr * UP_LD + 4 * lane]);
+        if (i * 16 + jr < rows) {
+          float* dst = p.y + (size_t)(base + sh.list[c0 + i * 16 + jr]) * N + n;
+          if (n + 4 <= N) {
+            *reinterpret_cast<f4u*>(dst) = v;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 3; c++)
+              if (n + c < N) dst[c] = v[c];
+          }
+        }
+      }
+      if (i + 1 < tiles) __syncthreads();  // before the next tile is put in place
+    }
+    __syncthreads();  // before the next rows
+  }
+}
+
+template <int KS, int TB>  // KS: enough for the call's largest rank
+__global__ void __launch_bounds__(64 * UP_WAVES)
+k_lora_up(const LoraBatch bt, const LoraArgs a) {
+  __shared__ __align__(16) UpShared<KS, TB> sh;
+  const int blocks = (a.M + ROWS - 1) / ROWS;
+  const int pi = blockIdx.y / blocks;
+  const LoraProblem& p = bt.p[pi];
+  const int base = (blockIdx.y % blocks) * ROWS;
   const int N = p.N, n0 = blockIdx.x * UP_N;
   if (n0 >= N) return;  // problems of a call may differ in N
-  const Group g = find_group(a, base, blockIdx.y);
-  if (!g.rows) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int cnt = list_rows(g.rows, list);
-  __syncthreads();
-  if (g.r == 0) {  // no adapter: y = y_in
-    if (p.y_in == p.y) return;
-    const int nn = min(UP_N, N - n0);
-    for (int j = wave; j < cnt; j += 4) {
-      const size_t at = (size_t)(base + list[j]) * N + n0;
-      for (int n = lane; n < nn; n += 64) p.y[at + n] = p.y_in ? p.y_in[at + n] : 0.0f;
-    }
-    return;
-  }
-  const float scale = a.scales ? a.scales[g.id] : 1.0f;
-  const int rpad = (g.r + 31) / 32 * 32;  // the k steps of the MFMAs
-  // a wave per row: add the K ranges, find the row's power of two, split
-  for (int j = wave; j < cnt; j += 4) {
-    const float* t0 = a.ws + ((size_t)pi * a.splits * a.M + base + list[j]) * a.rank_ld;
-    float t[LORA_MAX_RANK / 64];
-    float big = 0.0f;
-#pragma unroll
-    for (int i = 0; i < LORA_MAX_RANK / 64; i++) {
-      const int e = i * 64 + lane;
-      float sum = 0.0f;
-      if (e < g.r)
-        for (int s = 0; s < a.splits; s++) sum += t0[(size_t)s * a.M * a.rank_ld + e];
-      t[i] = sum;
-      big = fmaxf(big, fabsf(sum));
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor(big, d, 64));
-    // 2^e with big / 2^e in [0.5, 1); 1 where big is zero or not finite
-    int e = 0;
-    if (big > 0.0f && big < __builtin_inff()) e = __builtin_amdgcn_frexp_expf(big);
-#pragma unroll
-    for (int i = 0; i < LORA_MAX_RANK / 64; i++) {
-      const int c = i * 64 + lane;
-      if (c < rpad) {
-        const float u = ldexpf(t[i], 8 - e);  // [2^7, 2^8): lo stays a normal binary16 longer
-        const _Float16 uh = (_Float16)u;
-        hi[j][c] = uh;
-        lo[j][c] = __builtin_isinf(u) ? (_Float16)0.0f : (_Float16)(u - (float)uh);
+  const Rows rows = load_rows(a, base);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int gi = blockIdx.z;; gi += gridDim.z) {
+    const Group g = find_group(a, rows, gi);
+    if (!g.rows) return;
+    const int cnt = list_rows(g.rows, sh.list);
+    __syncthreads();
+    if (g.r != 0) {
+      up_body<KS, TB>(p, a, g, pi, base, n0, cnt, sh);
+    } else if (p.y_in != p.y) {  // no adapter: y = y_in
+      const int nn = min(UP_N, N - n0);
+      for (int j = wave; j < cnt; j += UP_WAVES) {
+        const size_t at = (size_t)(base + sh.list[j]) * N + n0;
+        for (int n = lane; n < nn; n += 64) p.y[at + n] = p.y_in ? p.y_in[at + n] : 0.0f;
       }
     }
-    if (lane == 0) back[j] = ldexpf(scale, e - 8);
-  }
-  __syncthreads();
-  const int l16 = lane & 15, h = lane >> 4;
-  const int tiles = (cnt + 15) / 16;
-  const _Float16* bblock = p.b + (size_t)g.off * N;  // [N][r]
-  for (int nt = 0; nt < UP_N / 64; nt++) {
-    const int n16 = n0 + wave * (UP_N / 4) + nt * 16;
-    if (n16 >= N) break;
-    const _Float16* bp = bblock + (size_t)min(n16 + l16, N - 1) * g.r + 8 * h;
-    f4 acc[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) acc[i] = f4{0, 0, 0, 0};
-    for (int k = 0; k < g.r; k += 32) {
-      h8 bv = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (k + 8 * h < g.r) bv = *reinterpret_cast<const h8*>(bp + k);
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        if (i < tiles) {
-          const int j = min(i * 16 + l16, cnt - 1);
-          const h8 tl = *reinterpret_cast<const h8*>(&lo[j][k + 8 * h]);
-          const h8 th = *reinterpret_cast<const h8*>(&hi[j][k + 8 * h]);
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bv, tl, acc[i], 0, 0, 0);
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bv, th, acc[i], 0, 0, 0);
-        }
-      }
-    }
-    // lane: row i*16 + l16, outputs n16 + 4 h .. + 3
-    const int n = n16 + 4 * h;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int j = i * 16 + l16;
-      if (i < tiles && j < cnt && n < N) {
-        const size_t at = (size_t)(base + list[j]) * N + n;
-        const float f = back[j];
-        if (N % 4 == 0) {
-          f4 v = f4{0, 0, 0, 0};
-          if (p.y_in) v = *reinterpret_cast<const f4*>(p.y_in + at);
-#pragma unroll
-          for (int c = 0; c < 4; c++) v[c] += f * acc[i][c];
-          *reinterpret_cast<f4*>(p.y + at) = v;
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; c++)
-            if (n + c < N) p.y[at + c] = (p.y_in ? p.y_in[at + c] : 0.0f) + f * acc[i][c];
-        }
-      }
-    }
+    __syncthreads();  // before the next group's list and rows
   }
 }
 
 }  // namespace
 
-// K ranges over workgroups: about 512 workgroups in all, at least 256 columns
-// of K each (2 steps a wave).
+// Shares of K over workgroups: about LORA_WORKGROUPS workgroups in all, at
+// least one round of 128 columns for each of their four waves.
 int lora_splits(int count, int M, int K, int adapters, int max_rank) {
   const int rows = M < ROWS ? M : ROWS;
   const long long wgs = (long long)count * ((M + ROWS - 1) / ROWS) * ((max_rank + 15) / 16) *
                         (rows < adapters ? rows : adapters);
-  long long s = 512 / (wgs > 0 ? wgs : 1);
-  if (s > K / 256) s = K / 256;
+  long long s = LORA_WORKGROUPS / (wgs > 0 ? wgs : 1);
+  if (s > (K + 511) / 512) s = (K + 511) / 512;
   if (s > LORA_MAX_SPLITS) s = LORA_MAX_SPLITS;
   return s < 1 ? 1 : (int)s;
 }
@@ -263,14 +398,31 @@ hipError_t launch_lora(const LoraBatch& bt, const LoraArgs& a, hipStream_t s) {
   const int blocks = (a.M + ROWS - 1) / ROWS;
   int groups = a.M < ROWS ? a.M : ROWS;
   if (groups > a.adapters + 1) groups = a.adapters + 1;
+  // the more blocks of rows, the fewer workgroups for a block's groups: each
+  // then takes several, where there are several, instead of most finding none
+  // (prompts: a block's rows mostly share an adapter or two)
+  if (blocks > 1) groups = std::min(groups, std::max(2, 128 / blocks));
   int n = 0;
   for (int i = 0; i < bt.count; i++) n = bt.p[i].N > n ? bt.p[i].N : n;
-  hipLaunchKernelGGL(k_lora_down, dim3(a.splits * (a.rank_ld / 16), groups, bt.count * blocks),
-                     dim3(256), 0, s, bt, a);
-  hipError_t e = hipGetLastError();
+  // Groups are the slow index: where most blocks have one or two, the
+  // workgroups that find rows are neighbours and spread over all CUs.
+  const dim3 down(a.splits * (a.rank_ld / 16), bt.count * blocks, groups);
+  const dim3 up((n + UP_N - 1) / UP_N, bt.count * blocks, groups);
+  // Few rows an adapter (16 at a time, more workgroups per CU) or many (64).
+  const bool few = blocks == 1 && (a.M <= 16 || a.adapters * 8 >= a.M);
+#define RQ_LORA_UP(KS)                                                                       \
+  do {                                                                                       \
+    if (few) hipLaunchKernelGGL((k_lora_up<KS, 1>), up, dim3(64 * UP_WAVES), 0, s, bt, a);    \
+    else hipLaunchKernelGGL((k_lora_up<KS, 4>), up, dim3(64 * UP_WAVES), 0, s, bt, a);        \
+  } while (0)
+  if (few) hipLaunchKernelGGL(k_lora_down<1>, down, dim3(256), 0, s, bt, a);
+  else hipLaunchKernelGGL(k_lora_down<4>, down, dim3(256), 0, s, bt, a);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_lora_up, dim3((n + UP_N - 1) / UP_N, groups, bt.count * blocks), dim3(256),
-                     0, s, bt, a);
+  if (a.max_rank <= 32) RQ_LORA_UP(1);
+  else if (a.max_rank <= 64) RQ_LORA_UP(2);
+  else RQ_LORA_UP(4);
+#undef RQ_LORA_UP
   return hipGetLastError();
 }
 
