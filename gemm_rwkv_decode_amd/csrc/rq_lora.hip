@@ -199,70 +199,45 @@ k_lora_down(const LoraBatch bt, const LoraArgs a) {
   }
 }
 
-// The group's rows times B: 256 outputs a workgroup, 32 of them a wave.  What
-// does not depend on t (the wave's B rows, y_in) is asked for before t is put
-// together.  A tile of 16 rows goes through LDS on its way out, so that a
-// wave reads and writes y in whole rows of 1 KiB: as the products lie in its
-// lanes, an access would take 64 bytes of each of 16 rows.
+// The group's rows times B, TB tiles of 16 rows at a time; a wave has UT tiles
+// of 16 outputs, a workgroup eight times that.  A tile of rows goes through LDS
+// on its way out, so that a wave reads and writes y in whole rows of 1 KiB: as
+// the products lie in its lanes, an access would take 64 bytes of each of 16
+// rows.
 constexpr int UP_WAVES = 8;
-constexpr int UP_TILES = 2;                       // tiles of 16 outputs a wave
-constexpr int UP_N = UP_WAVES * UP_TILES * 16;    // outputs of a workgroup: 4 a lane
-constexpr int UP_LD = UP_N + 4;                   // floats between rows of a tile
-constexpr int UP_ROWS = 16 / UP_WAVES;            // rows of a tile a wave takes out
+constexpr int UP_ROWS = 16 / UP_WAVES;  // rows of a tile a wave takes out
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
 
-template <int KS, int TB>  // k steps of 32: the rank is at most 32 KS
+template <int UT>
+struct Up {
+  static constexpr int N = UP_WAVES * UT * 16;  // outputs of a workgroup
+  static constexpr int Q = N / 256;             // 16-byte accesses of a lane to a row
+  static constexpr int LD = N + 4;              // floats between rows of a tile in LDS
+};
+
+template <int KS, int TB, int UT>  // k steps of 32: the rank is at most 32 KS
 struct UpShared {
   static constexpr int LD = 32 * KS + 8;  // halves; rows start 16 bytes apart in bank order
-  float out[16 * UP_LD];
+  float out[16 * Up<UT>::LD];
   _Float16 hi[16 * TB * LD], lo[16 * TB * LD];
   float back[16 * TB];  // 2^x s_i
   unsigned char list[ROWS];
 };
 
-template <int KS, int TB>
+template <int KS, int TB, int UT>
 __device__ __forceinline__ void up_body(const LoraProblem& p, const LoraArgs& a, const Group& g,
-                                        int pi, int base, int n0, int cnt, UpShared<KS, TB>& sh) {
-  constexpr int LD = UpShared<KS, TB>::LD;
+                                        int pi, int base, int n0, int cnt, UpShared<KS, TB, UT>& sh) {
+  constexpr int LD = UpShared<KS, TB, UT>::LD, Q = Up<UT>::Q;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l16 = lane & 15, h = lane >> 4;
   const int N = p.N;
-  const int nw = n0 + wave * (UP_TILES * 16);
+  const int nw = n0 + wave * (UT * 16);
   const _Float16* bblock = p.b + (size_t)g.off * N;  // [N][r]
-  h8 bv[UP_TILES][KS];
-#pragma unroll
-  for (int nt = 0; nt < UP_TILES; nt++) {
-    const _Float16* bp = bblock + (size_t)min(nw + nt * 16 + l16, N - 1) * g.r + 8 * h;
-#pragma unroll
-    for (int k = 0; k < KS; k++) {
-      bv[nt][k] = h8{0, 0, 0, 0, 0, 0, 0, 0};
-      if (32 * k + 8 * h < g.r) bv[nt][k] = *reinterpret_cast<const h8*>(bp + 32 * k);
-    }
-  }
-  const int n = n0 + 4 * lane;  // this lane's outputs of a whole row
+  const int n = n0 + 4 * lane;  // this lane's outputs of a whole row, and 256 on
   for (int c0 = 0; c0 < cnt; c0 += 16 * TB) {
     const int rows = min(cnt - c0, 16 * TB), tiles = (rows + 15) / 16;
-    // rows c0 + i * 16 + wave * UP_ROWS + q of the group
-    f4 y[TB][UP_ROWS];
-#pragma unroll
-    for (int i = 0; i < TB; i++) {
-#pragma unroll
-      for (int q = 0; q < UP_ROWS; q++) {
-        const int j = c0 + i * 16 + wave * UP_ROWS + q;
-        y[i][q] = f4{0, 0, 0, 0};
-        if (p.y_in && j < cnt) {
-          const float* src = p.y_in + (size_t)(base + sh.list[j]) * N + n;
-          if (n + 4 <= N) {
-            y[i][q] = *reinterpret_cast<const f4u*>(src);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 3; c++)
-              if (n + c < N) y[i][q][c] = src[c];
-          }
-        }
-      }
-    }
-    // t of all rows: LT lanes a row, four entries a lane
+    // t of all rows, asked for first: loads come back in order, and t is needed
+    // before the others.  LT lanes a row, four entries a lane
     constexpr int LT = 8 * KS, PASS = 64 * UP_WAVES / LT, PASSES = (16 * TB + PASS - 1) / PASS;
     const int e = 4 * (tid % LT);
     f4 t[PASSES];
@@ -275,12 +250,58 @@ __device__ __forceinline__ void up_body(const LoraProblem& p, const LoraArgs& a,
     }
     const size_t plane = (size_t)a.M * a.rank_ld;
     if (e < g.r) {  // ranks are multiples of 8; the shares of K in a fixed order
-#pragma unroll 2
-      for (int s = 0; s < a.splits; s++)
+      constexpr int AHEAD = PASSES == 1 ? 4 : 2;  // shares asked for together
+      for (int s = 0; s < a.splits; s += AHEAD) {
+        f4 v[AHEAD][PASSES];
 #pragma unroll
-        for (int i = 0; i < PASSES; i++)
-          if (i * PASS < rows) t[i] += *reinterpret_cast<const f4*>(src[i] + s * plane);
+        for (int u = 0; u < AHEAD; u++)
+#pragma unroll
+          for (int i = 0; i < PASSES; i++) {
+            v[u][i] = f4{0, 0, 0, 0};
+            if (s + u < a.splits && i * PASS < rows)
+              v[u][i] = *reinterpret_cast<const f4*>(src[i] + (s + u) * plane);
+          }
+#pragma unroll
+        for (int u = 0; u < AHEAD; u++)
+#pragma unroll
+          for (int i = 0; i < PASSES; i++) t[i] += v[u][i];
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    h8 bv[UT][KS];
+#pragma unroll
+    for (int nt = 0; nt < UT; nt++) {
+      const _Float16* bp = bblock + (size_t)min(nw + nt * 16 + l16, N - 1) * g.r + 8 * h;
+#pragma unroll
+      for (int k = 0; k < KS; k++) {
+        bv[nt][k] = h8{0, 0, 0, 0, 0, 0, 0, 0};
+        if (32 * k + 8 * h < g.r) bv[nt][k] = *reinterpret_cast<const h8*>(bp + 32 * k);
+      }
+    }
+    // rows c0 + i * 16 + wave * UP_ROWS + q of the group
+    f4 y[TB][UP_ROWS][Q];
+#pragma unroll
+    for (int i = 0; i < TB; i++) {
+#pragma unroll
+      for (int q = 0; q < UP_ROWS; q++) {
+        const int j = c0 + i * 16 + wave * UP_ROWS + q;
+        const float* src = p.y_in + (size_t)(base + sh.list[min(j, cnt - 1)]) * N;
+#pragma unroll
+        for (int w = 0; w < Q; w++) {
+          const int nw = n + 256 * w;
+          y[i][q][w] = f4{0, 0, 0, 0};
+          if (!p.y_in || j >= cnt) continue;
+          if (nw + 4 <= N) {
+            y[i][q][w] = *reinterpret_cast<const f4u*>(src + nw);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 3; c++)
+              if (nw + c < N) y[i][q][w][c] = src[nw + c];
+          }
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
     const float scale = a.scales ? a.scales[g.id] : 1.0f;
 #pragma unroll
     for (int i = 0; i < PASSES; i++) {
@@ -310,37 +331,41 @@ __device__ __forceinline__ void up_body(const LoraProblem& p, const LoraArgs& a,
     for (int i = 0; i < TB; i++) {
       if (i >= tiles) break;
       const int j = min(i * 16 + l16, rows - 1);
-      f4 acc[UP_TILES];
+      f4 acc[UT];
 #pragma unroll
-      for (int nt = 0; nt < UP_TILES; nt++) acc[nt] = f4{0, 0, 0, 0};
+      for (int nt = 0; nt < UT; nt++) acc[nt] = f4{0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < KS; k++) {
         const h8 tl = *reinterpret_cast<const h8*>(&sh.lo[j * LD + 32 * k + 8 * h]);
         const h8 th = *reinterpret_cast<const h8*>(&sh.hi[j * LD + 32 * k + 8 * h]);
 #pragma unroll
-        for (int nt = 0; nt < UP_TILES; nt++) {
+        for (int nt = 0; nt < UT; nt++) {
           acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bv[nt][k], tl, acc[nt], 0, 0, 0);
           acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bv[nt][k], th, acc[nt], 0, 0, 0);
         }
       }
       const float f = sh.back[j];
 #pragma unroll
-      for (int nt = 0; nt < UP_TILES; nt++)
-        *reinterpret_cast<f4*>(&sh.out[l16 * UP_LD + wave * (UP_TILES * 16) + nt * 16 + 4 * h]) =
+      for (int nt = 0; nt < UT; nt++)
+        *reinterpret_cast<f4*>(&sh.out[l16 * Up<UT>::LD + wave * (UT * 16) + nt * 16 + 4 * h]) =
             acc[nt] * f;
       __syncthreads();
 #pragma unroll
       for (int q = 0; q < UP_ROWS; q++) {
         const int jr = wave * UP_ROWS + q;
-        const f4 v = y[i][q] + *reinterpret_cast<const f4*>(&sh.out[jr * UP_LD + 4 * lane]);
-        if (i * 16 + jr < rows) {
-          float* dst = p.y + (size_t)(base + sh.list[c0 + i * 16 + jr]) * N + n;
-          if (n + 4 <= N) {
-            *reinterpret_cast<f4u*>(dst) = v;
+        if (i * 16 + jr >= rows) continue;
+        float* dst = p.y + (size_t)(base + sh.list[c0 + i * 16 + jr]) * N;
+#pragma unroll
+        for (int w = 0; w < Q; w++) {
+          const int nw = n + 256 * w;
+          const f4 v = y[i][q][w] +
+                       *reinterpret_cast<const f4*>(&sh.out[jr * Up<UT>::LD + 256 * w + 4 * lane]);
+          if (nw + 4 <= N) {
+            *reinterpret_cast<f4u*>(dst + nw) = v;
           } else {
 #pragma unroll
             for (int c = 0; c < 3; c++)
-              if (n + c < N) dst[c] = v[c];
+              if (nw + c < N) dst[nw + c] = v[c];
           }
         }
       }
@@ -350,15 +375,15 @@ __device__ __forceinline__ void up_body(const LoraProblem& p, const LoraArgs& a,
   }
 }
 
-template <int KS, int TB>  // KS: enough for the call's largest rank
+template <int KS, int TB, int UT>  // KS: enough for the call's largest rank
 __global__ void __launch_bounds__(64 * UP_WAVES)
 k_lora_up(const LoraBatch bt, const LoraArgs a) {
-  __shared__ __align__(16) UpShared<KS, TB> sh;
+  __shared__ __align__(16) UpShared<KS, TB, UT> sh;
   const int blocks = (a.M + ROWS - 1) / ROWS;
   const int pi = blockIdx.y / blocks;
   const LoraProblem& p = bt.p[pi];
   const int base = (blockIdx.y % blocks) * ROWS;
-  const int N = p.N, n0 = blockIdx.x * UP_N;
+  const int N = p.N, n0 = blockIdx.x * Up<UT>::N;
   if (n0 >= N) return;  // problems of a call may differ in N
   const Rows rows = load_rows(a, base);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -368,9 +393,9 @@ k_lora_up(const LoraBatch bt, const LoraArgs a) {
     const int cnt = list_rows(g.rows, sh.list);
     __syncthreads();
     if (g.r != 0) {
-      up_body<KS, TB>(p, a, g, pi, base, n0, cnt, sh);
+      up_body<KS, TB, UT>(p, a, g, pi, base, n0, cnt, sh);
     } else if (p.y_in != p.y) {  // no adapter: y = y_in
-      const int nn = min(UP_N, N - n0);
+      const int nn = min(Up<UT>::N, N - n0);
       for (int j = wave; j < cnt; j += UP_WAVES) {
         const size_t at = (size_t)(base + sh.list[j]) * N + n0;
         for (int n = lane; n < nn; n += 64) p.y[at + n] = p.y_in ? p.y_in[at + n] : 0.0f;
@@ -382,14 +407,15 @@ k_lora_up(const LoraBatch bt, const LoraArgs a) {
 
 }  // namespace
 
-// Shares of K over workgroups: about LORA_WORKGROUPS workgroups in all, at
-// least one round of 128 columns for each of their four waves.
+// Shares of K over workgroups: about LORA_WORKGROUPS workgroups in all, with
+// two rounds of 128 columns for each of their four waves (one batch of loads;
+// smaller shares cost the second launch more than they save here).
 int lora_splits(int count, int M, int K, int adapters, int max_rank) {
   const int rows = M < ROWS ? M : ROWS;
   const long long wgs = (long long)count * ((M + ROWS - 1) / ROWS) * ((max_rank + 15) / 16) *
                         (rows < adapters ? rows : adapters);
   long long s = LORA_WORKGROUPS / (wgs > 0 ? wgs : 1);
-  if (s > (K + 511) / 512) s = (K + 511) / 512;
+  if (s > (K + 1023) / 1024) s = (K + 1023) / 1024;
   if (s > LORA_MAX_SPLITS) s = LORA_MAX_SPLITS;
   return s < 1 ? 1 : (int)s;
 }
@@ -407,13 +433,20 @@ hipError_t launch_lora(const LoraBatch& bt, const LoraArgs& a, hipStream_t s) {
   // Groups are the slow index: where most blocks have one or two, the
   // workgroups that find rows are neighbours and spread over all CUs.
   const dim3 down(a.splits * (a.rank_ld / 16), bt.count * blocks, groups);
-  const dim3 up((n + UP_N - 1) / UP_N, bt.count * blocks, groups);
   // Few rows an adapter (16 at a time, more workgroups per CU) or many (64).
+  // With few, a wave takes four tiles of 16 outputs for more of B in flight (64
+  // rows, 48 adapters of rank 32 or 16, 4096x4096: 22.1 -> 16.6 us), two where
+  // that would leave CUs without work (one row, 768x768: 7.2 against 7.7 us).
   const bool few = blocks == 1 && (a.M <= 16 || a.adapters * 8 >= a.M);
-#define RQ_LORA_UP(KS)                                                                       \
-  do {                                                                                       \
-    if (few) hipLaunchKernelGGL((k_lora_up<KS, 1>), up, dim3(64 * UP_WAVES), 0, s, bt, a);    \
-    else hipLaunchKernelGGL((k_lora_up<KS, 4>), up, dim3(64 * UP_WAVES), 0, s, bt, a);        \
+  const bool wide = few && (long long)n * bt.count * groups >= 256 * Up<4>::N;
+  const int per = wide ? Up<4>::N : Up<2>::N;
+  const dim3 up((n + per - 1) / per, bt.count * blocks, groups);
+#define RQ_LORA_UP(KS)                                                                          \
+  do {                                                                                          \
+    const dim3 th(64 * UP_WAVES);                                                               \
+    if (wide) hipLaunchKernelGGL((k_lora_up<KS, 1, 4>), up, th, 0, s, bt, a);                   \
+    else if (few) hipLaunchKernelGGL((k_lora_up<KS, 1, 2>), up, th, 0, s, bt, a);               \
+    else hipLaunchKernelGGL((k_lora_up<KS, 4, 2>), up, th, 0, s, bt, a);                        \
   } while (0)
   if (few) hipLaunchKernelGGL(k_lora_down<1>, down, dim3(256), 0, s, bt, a);
   else hipLaunchKernelGGL(k_lora_down<4>, down, dim3(256), 0, s, bt, a);
