@@ -101,56 +101,108 @@ k_wkv_seq(const WkvArgs a) {
 
 // ---------------------------------------------------------------------------
 // Sixteen tokens at a time.  With P_t = d_1 ... d_t (per key column, from the
-// chunk's start) and S0 the state before the chunk, the recurrence is
-//   u_t  = S0 (kappa_t o P_{t-1}) + sum_{s<t} (Mb[t][s] u_s + Mk[t][s] v_s)
-//   y_t  = S0 (r_t o P_t)         + sum_{s<=t} (Nb[t][s] u_s + Nk[t][s] v_s)
-//   S16  = S0 diag(P_16) + sum_s (u_s bc_s^T + v_s kc_s^T)
-// where u_t = S_{t-1} kappa_t, and with b_s = -(eta o kappa)_s / P_s, k^_s = k_s / P_s
-//   Mb[t][s] = (kappa_t o P_{t-1}) . b_s    Mk[t][s] = (kappa_t o P_{t-1}) . k^_s
-//   Nb[t][s] = (r_t o P_t) . b_s            Nk[t][s] = (r_t o P_t) . k^_s
-//   bc_s = b_s o P_16,  kc_s = k^_s o P_16.
+// chunk's start), Q = P_8 and S0 the state before the chunk, the recurrence is
+//   u_t = (S0 o Q) (kappa_t o P_{t-1} / Q) + sum_{s<t}  (Mb[t][s] u_s + Mk[t][s] v_s)
+//   y_t = (S0 o Q) (r_t o P_t / Q)         + sum_{s<=t} (Nb[t][s] u_s + Nk[t][s] v_s)
+//   S16 = S0 diag(P_16) + sum_s (u_s bc_s^T + v_s kc_s^T)
+// where u_t = S_{t-1} kappa_t and, with a_t = kappa_t o P_{t-1} / Q, q_t = r_t o
+// P_t / Q, b_s = -(eta o kappa)_s o Q / P_s, k_s standing for k_s o Q / P_s,
+//   Mb[t][s] = a_t . b_s   Mk[t][s] = a_t . k_s   Nb[t][s] = q_t . b_s   Nk[t][s] = q_t . k_s
+//   bc_s = b_s o P_16 / Q,   kc_s = k_s o P_16 / Q.
 // Mb is strictly lower triangular, so U = X (S0 part + Mk V), X = (I - Mb)^-1.
-// Everything is a product of small matrices on the binary32 matrix cores
-// (v_mfma_f32_16x16x4_f32): 80 of them per chunk and 16 state rows where the
-// token loop needs 36 vector instructions, and one dependent pass per 16
-// tokens.  Every decay is at least 0.545, so 1 / P stays below 2^14 and
-// nothing is lost to the factoring; a chunk is 16 tokens for that reason and
-// because it is the matrix instruction's tile.
+// Every decay is at least 0.545, so the factors P / Q lie between 2^-7 and
+// 2^7 whatever w is; a chunk is 16 tokens for that reason and because it is
+// the matrix instructions' tile.
+//
+// Products run on the binary16 matrix cores with binary32 sums, every operand
+// in two parts, x = hi + 2^-11 lo, both binary16: hi hi' goes to one sum, hi lo'
+// + lo hi' to a second that joins with 2^-11.  What is left out or rounded is
+// below 2^-22 of an operand (2^-36 in absolute terms for values under 2^-14),
+// so a product is as good as a binary32 one, at three binary16 MFMAs for eight
+// binary32 ones of twice the length.  The state itself, the decays, the
+// triangular inverse and everything added up stay binary32.
+// A chunk in which a value does not fit this (not finite, 2^15 or more, or
+// nothing as large as 2^-12 in k, r, or the state and v together) is done token
+// by token in binary32 instead.
 //
 // The contraction order is free, so operands are laid out for the accumulator:
 // a lane's accumulator f4 covers rows 4 (l / 16) .. + 3 of column l mod 16, and
-// as a right operand of four MFMAs it is the contraction index 4 (l / 16) + v.
-// The state S^T [keys][values], U and V are therefore used as they come, with
-// no exchange between lanes, and the state never leaves its registers.
+// as a right operand it is the contraction index 4 (l / 16) + v (of two tiles,
+// for the 32-deep instruction).  The state S^T [keys][values], U and V are
+// therefore used as they come, with no exchange between lanes, and the state
+// never leaves its registers.  The left operands Mk, Nb, Nk and X are made as
+// their transposes, whose accumulators are the operands; kc and bc are turned
+// by products with the identity.
 //
 // A workgroup has NR state waves, 16 value rows each, and three producer waves
 // that prepare what depends on the inputs alone (decays, the four 16x16
 // matrices, the triangular inverse), one chunk each, in three segments one
 // barrier apart; chunk c's operands go through LDS, two buffers in turn.
 // ---------------------------------------------------------------------------
-constexpr int CH = 16;      // tokens of a chunk
-constexpr int LDR = 68;     // floats between rows of a [16][64] operand (bank order)
-constexpr int LDT = 20;     // floats between rows of a [64][16] or [16][16] operand
+constexpr int CH = 16;  // tokens of a chunk
 constexpr int PRODUCERS = 3;
+constexpr float UP = 2048.0f, DOWN = 1.0f / 2048.0f;  // the low part's scale
+constexpr float TINY = 1.0f / 4096.0f, HUGE_ = 32768.0f;
 
-// What a chunk's state waves read.  With one state wave per workgroup the
-// producers also make the products with V, which leaves the state wave with
-// what depends on the state.
-template <int NR>
+// Two-part operands: 4 deep (one accumulator tile) and 8 deep (two).
+struct P4 {
+  h4 hi, lo;
+};
+struct P8 {
+  h8 hi, lo;
+};
+__device__ __forceinline__ P4 split(const f4& x) {
+  P4 p;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    // x as rounded to binary32: the compiler would else round the product
+    // behind x to binary16 in one step in one place and in two in another, and
+    // hi and lo would not belong together
+    float v = x[i];
+    asm("" : "+v"(v));
+    p.hi[i] = (_Float16)v;
+    p.lo[i] = (_Float16)__builtin_fmaf(-UP, (float)p.hi[i], UP * v);
+  }
+  return p;
+}
+__device__ __forceinline__ P8 join(const P4& a, const P4& b) {
+  return P8{__builtin_shufflevector(a.hi, b.hi, 0, 1, 2, 3, 4, 5, 6, 7),
+            __builtin_shufflevector(a.lo, b.lo, 0, 1, 2, 3, 4, 5, 6, 7)};
+}
+// A product's two sums.
+struct Sum {
+  f4 main, cross;
+  __device__ __forceinline__ f4 value() const {
+    f4 r;
+#pragma unroll
+    for (int i = 0; i < 4; i++) r[i] = __builtin_fmaf(DOWN, cross[i], main[i]);
+    return r;
+  }
+};
+__device__ __forceinline__ Sum none() { return Sum{f4{0, 0, 0, 0}, f4{0, 0, 0, 0}}; }
+__device__ __forceinline__ void mma(const P4& a, const P4& b, Sum& c) {
+  c.main = __builtin_amdgcn_mfma_f32_16x16x16f16(a.hi, b.hi, c.main, 0, 0, 0);
+  c.cross = __builtin_amdgcn_mfma_f32_16x16x16f16(a.hi, b.lo, c.cross, 0, 0, 0);
+  c.cross = __builtin_amdgcn_mfma_f32_16x16x16f16(a.lo, b.hi, c.cross, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(const P8& a, const P8& b, Sum& c) {
+  c.main = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.hi, c.main, 0, 0, 0);
+  c.cross = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.lo, c.cross, 0, 0, 0);
+  c.cross = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.lo, b.hi, c.cross, 0, 0, 0);
+}
+
+// What a chunk's state waves read: left operands by lane, decays by key.
 struct alignas(16) ChunkOps {
-  float ah[CH * LDR];   // kappa_t o P_{t-1}
-  float rh[CH * LDR];   // r_t o P_t
-  float bcT[HD * LDT];  // [key][token]
-  float x[CH * LDT];    // (I - Mb)^-1
-  float nb[CH * LDT];
-  float pc[HD];         // P_16
-  // NR > 1: kcT and the matrices that multiply V; NR = 1: the products
-  // themselves, as accumulators [j][lane] of kc^T V, then Mk V and Nk V
-  float v[NR == 1 ? 6 * 256 : HD * LDT + 2 * CH * LDT];
-  int bad;              // a value that is not finite: token by token
-  __device__ __forceinline__ float* kcT() { return v; }
-  __device__ __forceinline__ float* mk() { return v + HD * LDT; }
-  __device__ __forceinline__ float* nk() { return v + HD * LDT + CH * LDT; }
+  h8 a[2][2][64];   // [part][two key tiles][lane]: a_t
+  h8 q[2][2][64];   // q_t
+  h8 kb[2][4][64];  // [part][key tile][lane]: kc, then bc, of tokens 4 g + v
+  h4 x[2][64], nb[2][64], mk[2][64], nk[2][64];
+  int slow;         // token by token
+};
+// Q and P_16 of a chunk.  Written two steps before the other operands, so four
+// of them in turn.
+struct alignas(16) ChunkDecays {
+  float mid[HD], end[HD];
 };
 
 // product over the lanes of a row of 16 up to this one, for four values: a
@@ -174,12 +226,6 @@ __device__ __forceinline__ float left_or_one(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
                                        0x3f800000, __builtin_bit_cast(int, v), 0x111, 0xF, 0xF,
                                        false));
-}
-
-__device__ __forceinline__ f4 mma4(const f4& a, const f4& b, f4 c) {
-#pragma unroll
-  for (int v = 0; v < 4; v++) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[v], b[v], c, 0, 0, 0);
-  return c;
 }
 
 // Barrier that waits for this wave's LDS accesses only: loads of later chunks
@@ -225,36 +271,6 @@ struct ChunkIn {
   }
 };
 
-// z = kc^T V, from kcT [key][token] in LDS
-__device__ __forceinline__ void keys_times_v(const float* kcT, const f4& V, f4* z) {
-  const int lane = threadIdx.x & 63;
-  f4 k[4];
-#pragma unroll
-  for (int j = 0; j < 4; j++) {
-    k[j] = *reinterpret_cast<const f4*>(&kcT[(16 * j + (lane & 15)) * LDT + 4 * (lane >> 4)]);
-    z[j] = f4{0, 0, 0, 0};
-  }
-  // four independent sums, so no MFMA waits for the one before it
-#pragma unroll
-  for (int v = 0; v < 4; v++)
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-      z[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(k[j][v], V[v], z[j], 0, 0, 0);
-}
-// mv = Mk V, nv = Nk V
-__device__ __forceinline__ void tokens_times_v(const float* mk, const float* nk, const f4& V,
-                                               f4* mv, f4* nv) {
-  const int lane = threadIdx.x & 63, at = (lane & 15) * LDT + 4 * (lane >> 4);
-  const f4 m = *reinterpret_cast<const f4*>(&mk[at]);
-  const f4 n = *reinterpret_cast<const f4*>(&nk[at]);
-  *mv = *nv = f4{0, 0, 0, 0};
-#pragma unroll
-  for (int v = 0; v < 4; v++) {
-    *mv = __builtin_amdgcn_mfma_f32_16x16x4f32(m[v], V[v], *mv, 0, 0, 0);
-    *nv = __builtin_amdgcn_mfma_f32_16x16x4f32(n[v], V[v], *nv, 0, 0, 0);
-  }
-}
-
 // V of a chunk as a right operand: tokens 4 g + v of the lane's value row, as
 // loaded; tokens past the end repeat the last one until they are used.
 template <typename T>
@@ -284,42 +300,52 @@ __device__ __forceinline__ float row_of(float v) {
   const u32 r = b[G >> 1];
   return __builtin_bit_cast(float, r);
 }
-// Rows after S of x += column S of the strictly lower triangular m times row
-// S of x (accumulator layout: rows 4 g + v, columns lane mod 16), then the
-// rows after S + 1, and so on.
-template <int S>
+// X^T = I + Mb^T X^T by substitution from the last row: row T is final once the
+// rows after it have been taken off; it goes to all lanes, and every row s takes
+// Mb^T[s][T] of it (accumulator layout: rows 4 g + v, columns lane mod 16).
+template <int T>
 __device__ __forceinline__ void eliminate(const f4& m, f4& x) {
-  if constexpr (S < CH - 1) {
-    const float xs = row_of<S / 4>(x[S % 4]);
+  if constexpr (T > 0) {
+    const float xs = row_of<T / 4>(x[T % 4]);
 #pragma unroll
     for (int v = 0; v < 4; v++) {
       const float mv = m[v];
-      x[v] = __builtin_fmaf(dpp_mov<0x150 + S>(mv), xs, x[v]);  // lane S of the row
+      x[v] = __builtin_fmaf(dpp_mov<0x150 + T>(mv), xs, x[v]);  // lane T of the row
     }
-    eliminate<S + 1>(m, x);
+    eliminate<T - 1>(m, x);
   }
 }
 
-template <typename T, int NR>
-__device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, float* scratch,
-                                        int p, int lo, int hi, size_t base, size_t ld, int row) {
+__device__ __forceinline__ float larger(float m, const f4& x) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) m = fmaxf(m, fabsf(x[i]));
+  return m;
+}
+// Whether the wave's largest magnitude (m over the lanes) is too small for
+// two-part operands: under 2^-12 and not zero.
+__device__ __forceinline__ bool too_small(float m) {
+  return __ballot(m >= TINY) == 0 && __ballot(m > 0.0f) != 0;
+}
+
+template <typename T>
+__device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDecays* decays,
+                                        int p, int lo, int hi, size_t base, size_t ld) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int n = (hi - lo + CH - 1) / CH;
-  const T* vp = static_cast<const T*>(a.v) + base + row;
   ChunkIn<T> in;
-  ChunkV<T> vin;
   auto fetch = [&](int c) {
-    const int t0 = lo + c * CH;
-    in.load(a, (size_t)min(t0 + l16, hi - 1) * ld + base + 4 * g);
-    if constexpr (NR == 1) vin.load(vp, ld, t0, hi);
+    in.load(a, (size_t)min(lo + c * CH + l16, hi - 1) * ld + base + 4 * g);
   };
+  h4 identity;
+#pragma unroll
+  for (int v = 0; v < 4; v++) identity[v] = l16 == 4 * g + v ? (_Float16)1.0f : (_Float16)0.0f;
   if (p < n) fetch(p);
   int steps = p;
   for (int i = 0; i < p; i++) step_barrier();
   for (int c = p; c < n; c += PRODUCERS) {
     const int t0 = lo + c * CH;
     // segment 1: decays and the scaled operands
-    f4 ah[4], rh[4], bh[4], kh[4], pc[4], V = {0, 0, 0, 0};
+    f4 av[4], qv[4], bv[4], kv[4], rest[4];  // rest: P_16 / Q
     const bool live = t0 + l16 < hi;
     if (t0 + CH > hi && !live) {  // past the end: nothing decays, nothing is added
 #pragma unroll
@@ -328,118 +354,111 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, flo
         in.w[j] = T(-INFINITY);
       }
     }
+    float big_k = 0.0f, big_r = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      f4 P;
+      f4 P, mid, end;
 #pragma unroll
       for (int v = 0; v < 4; v++) P[v] = decay_of((float)in.w[j][v]);
       row_scan4(P);
 #pragma unroll
       for (int v = 0; v < 4; v++) {
-        const float kap = (float)in.kap[j][v];
+        const float kap = (float)in.kap[j][v], k = (float)in.k[j][v], r = (float)in.r[j][v];
         const float inv = __builtin_amdgcn_rcpf(P[v]);
-        pc[j][v] = dpp_mov<0x15F>(P[v]);  // lane 15 of the row
-        ah[j][v] = kap * left_or_one(P[v]);
-        rh[j][v] = (float)in.r[j][v] * P[v];
-        bh[j][v] = -((float)in.eta[j][v] * kap) * inv;
-        kh[j][v] = (float)in.k[j][v] * inv;
+        mid[v] = dpp_mov<0x157>(P[v]);           // lane 7 of the row: Q
+        const float over = dpp_mov<0x157>(inv);  // 1 / Q
+        end[v] = dpp_mov<0x15F>(P[v]);           // lane 15: P_16
+        rest[j][v] = end[v] * over;
+        const float up = inv * mid[v];
+        av[j][v] = kap * (left_or_one(P[v]) * over);
+        qv[j][v] = r * (P[v] * over);
+        bv[j][v] = -((float)in.eta[j][v] * kap) * up;
+        kv[j][v] = k * up;
+        big_k = fmaxf(big_k, fabsf(k));
+        big_r = fmaxf(big_r, fabsf(r));
+      }
+      if (l16 == 0) {
+        *reinterpret_cast<f4*>(&decays[c & 3].mid[16 * j + 4 * g]) = mid;
+        *reinterpret_cast<f4*>(&decays[c & 3].end[16 * j + 4 * g]) = end;
       }
     }
-    if constexpr (NR == 1) V = vin.get(t0, hi);
     if (c + PRODUCERS < n) fetch(c + PRODUCERS);  // two steps ahead of its use
-    float* const kcT = NR == 1 ? scratch : ops[c & 1].kcT();
-    f4 z[4];
-    if constexpr (NR == 1) {
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-#pragma unroll
-        for (int v = 0; v < 4; v++)
-          kcT[(16 * j + 4 * g + v) * LDT + l16] = kh[j][v] * pc[j][v];
-      // this wave's own writes, read back transposed (LDS keeps a wave's order)
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
-      keys_times_v(kcT, V, z);
-    }
+    bool slow = too_small(big_k) || too_small(big_r);
     step_barrier();
-    // segment 2: the four products, rows t = 4 g + v, columns s = lane mod 16
-    // (kept on this side of the barrier: the segments are of about one length)
+    // segment 2: the four products' transposes, rows s = 4 g + v, columns t =
+    // lane mod 16, and kc and bc turned from tokens x keys to keys x tokens by
+    // products with the identity, which are exact
+    P8 ap[2], qp[2], kb[4];
+    Sum mb = none(), mk = mb, nb = mb, nk = mb;
 #pragma unroll
-    for (int j = 0; j < 4; j++) asm volatile("" : "+v"(ah[j]), "+v"(rh[j]));
-    f4 mb = {0, 0, 0, 0}, mk = mb, nb = mb, nk = mb;
+    for (int q = 0; q < 2; q++) {
+      ap[q] = join(split(av[2 * q]), split(av[2 * q + 1]));
+      qp[q] = join(split(qv[2 * q]), split(qv[2 * q + 1]));
+      const P8 bp = join(split(bv[2 * q]), split(bv[2 * q + 1]));
+      const P8 kp = join(split(kv[2 * q]), split(kv[2 * q + 1]));
+      mma(bp, ap[q], mb);
+      mma(kp, ap[q], mk);
+      mma(bp, qp[q], nb);
+      mma(kp, qp[q], nk);
+    }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
+      const P4 kp = split(kv[j] * rest[j]), bp = split(bv[j] * rest[j]);
+      const f4 z = {0, 0, 0, 0};
+      const f4 kh = __builtin_amdgcn_mfma_f32_16x16x16f16(kp.hi, identity, z, 0, 0, 0);
+      const f4 bh = __builtin_amdgcn_mfma_f32_16x16x16f16(bp.hi, identity, z, 0, 0, 0);
+      const f4 kl = __builtin_amdgcn_mfma_f32_16x16x16f16(kp.lo, identity, z, 0, 0, 0);
+      const f4 bl = __builtin_amdgcn_mfma_f32_16x16x16f16(bp.lo, identity, z, 0, 0, 0);
 #pragma unroll
       for (int v = 0; v < 4; v++) {
-        mb = __builtin_amdgcn_mfma_f32_16x16x4f32(ah[j][v], bh[j][v], mb, 0, 0, 0);
-        mk = __builtin_amdgcn_mfma_f32_16x16x4f32(ah[j][v], kh[j][v], mk, 0, 0, 0);
-        nb = __builtin_amdgcn_mfma_f32_16x16x4f32(rh[j][v], bh[j][v], nb, 0, 0, 0);
-        nk = __builtin_amdgcn_mfma_f32_16x16x4f32(rh[j][v], kh[j][v], nk, 0, 0, 0);
+        kb[j].hi[v] = (_Float16)kh[v];
+        kb[j].hi[4 + v] = (_Float16)bh[v];
+        kb[j].lo[v] = (_Float16)kl[v];
+        kb[j].lo[4 + v] = (_Float16)bl[v];
       }
     }
-    // a value that is not finite leaves none of its row's or column's sums finite
+    f4 mbv = mb.value(), mkv = mk.value(), nbv = nb.value(), nkv = nk.value();
+    step_barrier();
+    // segment 3: the triangular inverse, and everything to the chunk's buffer
+    ChunkOps& o = ops[c & 1];
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+      o.a[0][q][lane] = ap[q].hi;
+      o.a[1][q][lane] = ap[q].lo;
+      o.q[0][q][lane] = qp[q].hi;
+      o.q[1][q][lane] = qp[q].lo;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      o.kb[0][j][lane] = kb[j].hi;
+      o.kb[1][j][lane] = kb[j].lo;
+    }
+    // a value that is not finite, or too large for an operand, leaves none of
+    // its row's or column's sums finite
     float zero = 0.0f;
-    float* const mks = kcT + HD * LDT;
-    float* const nks = mks + CH * LDT;
 #pragma unroll
     for (int v = 0; v < 4; v++) {
-      const int t = 4 * g + v;
-      zero = __builtin_fmaf(mb[v], 0.0f, __builtin_fmaf(mk[v], 0.0f, zero));
-      zero = __builtin_fmaf(nb[v], 0.0f, __builtin_fmaf(nk[v], 0.0f, zero));
-      if (l16 >= t) mb[v] = mk[v] = 0.0f;
-      if (l16 > t) nb[v] = nk[v] = 0.0f;
+      zero = __builtin_fmaf(mbv[v], 0.0f, __builtin_fmaf(mkv[v], 0.0f, zero));
+      zero = __builtin_fmaf(nbv[v], 0.0f, __builtin_fmaf(nkv[v], 0.0f, zero));
+      if (4 * g + v >= l16) mbv[v] = mkv[v] = 0.0f;
+      if (4 * g + v > l16) nbv[v] = nkv[v] = 0.0f;
     }
-    f4 mv, nv;
-    if constexpr (NR == 1) {
-#pragma unroll
-      for (int v = 0; v < 4; v++) {
-        mks[(4 * g + v) * LDT + l16] = mk[v];
-        nks[(4 * g + v) * LDT + l16] = nk[v];
-      }
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);  // as above
-      tokens_times_v(mks, nks, V, &mv, &nv);
-    }
-    step_barrier();
-    // segment 3: the rest, into the chunk's buffer
-    ChunkOps<NR>& o = ops[c & 1];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-#pragma unroll
-      for (int v = 0; v < 4; v++) {
-        const int key = 16 * j + 4 * g + v;
-        if constexpr (NR > 1) kcT[key * LDT + l16] = kh[j][v] * pc[j][v];
-        o.bcT[key * LDT + l16] = bh[j][v] * pc[j][v];
-      }
-      *reinterpret_cast<f4*>(&o.ah[l16 * LDR + 16 * j + 4 * g]) = ah[j];
-      *reinterpret_cast<f4*>(&o.rh[l16 * LDR + 16 * j + 4 * g]) = rh[j];
-      if (l16 == 0) *reinterpret_cast<f4*>(&o.pc[16 * j + 4 * g]) = pc[j];
-    }
-#pragma unroll
-    for (int v = 0; v < 4; v++) {
-      const int at = (4 * g + v) * LDT + l16;
-      if constexpr (NR > 1) {
-        mks[at] = mk[v];
-        nks[at] = nk[v];
-      }
-      o.nb[at] = nb[v];
-    }
-    if constexpr (NR == 1) {
-      f4* dst = reinterpret_cast<f4*>(o.v) + lane;
-#pragma unroll
-      for (int j = 0; j < 4; j++) dst[64 * j] = z[j];
-      dst[256] = mv;
-      dst[320] = nv;
-#pragma unroll
-      for (int v = 0; v < 4; v++) zero = __builtin_fmaf(z[0][v], 0.0f, zero);
-    }
-    // X by forward substitution: row s is final once the rows before it have
-    // been taken off; it goes to all lanes, and every row takes its share
     f4 x;
 #pragma unroll
     for (int v = 0; v < 4; v++) x[v] = l16 == 4 * g + v ? 1.0f : 0.0f;
-    eliminate<0>(mb, x);
-#pragma unroll
-    for (int v = 0; v < 4; v++) o.x[(4 * g + v) * LDT + l16] = x[v];
-    const bool bad = __ballot(!(zero == 0.0f)) != 0;
-    if (lane == 0) o.bad = bad;
+    eliminate<CH - 1>(mbv, x);
+    const float big = larger(larger(larger(larger(0.0f, x), mkv), nbv), nkv);
+    slow = slow || __ballot(!(zero == 0.0f) || !(big < HUGE_)) != 0;
+    const P4 xp = split(x), mkp = split(mkv), nbp = split(nbv), nkp = split(nkv);
+    o.x[0][lane] = xp.hi;
+    o.x[1][lane] = xp.lo;
+    o.mk[0][lane] = mkp.hi;
+    o.mk[1][lane] = mkp.lo;
+    o.nb[0][lane] = nbp.hi;
+    o.nb[1][lane] = nbp.lo;
+    o.nk[0][lane] = nkp.hi;
+    o.nk[1][lane] = nkp.lo;
+    if (lane == 0) o.slow = slow;
     step_barrier();
     steps += 3;
   }
@@ -449,24 +468,23 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps<NR>* ops, flo
 template <typename T, int NR>
 __global__ void __launch_bounds__(64 * (NR + PRODUCERS))
 k_wkv_chunk(const WkvArgs a) {
-  __shared__ __align__(16) ChunkOps<NR> ops[2];
-  // the producers' own copies of kcT, mk and nk
-  __shared__ __align__(16) float scratch[NR == 1 ? PRODUCERS : 1][NR == 1 ? (2 * CH + HD) * LDT : 1];
+  __shared__ ChunkOps ops[2];
+  __shared__ ChunkDecays decays[4];
   // heads are the fast index: a sequence's workgroups go to all XCDs
   constexpr int TILES = 4 / NR;
-  const int q = blockIdx.x / (a.H * TILES), h = blockIdx.x % (a.H * TILES) / TILES;
-  const int lo = max(a.offsets[q], 0), hi = min(a.offsets[q + 1], a.T);
+  const int sq = blockIdx.x / (a.H * TILES), h = blockIdx.x % (a.H * TILES) / TILES;
+  const int lo = max(a.offsets[sq], 0), hi = min(a.offsets[sq + 1], a.T);
   if (lo >= hi) return;
   const int n = (hi - lo + CH - 1) / CH;
   const size_t ld = (size_t)a.H * HD, base = (size_t)h * HD;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-  const int i = 16 * (blockIdx.x % TILES * NR + wave % NR) + l16;  // the lane's value row
   if (wave >= NR) {
-    produce<T, NR>(a, ops, scratch[NR == 1 ? wave - NR : 0], wave - NR, lo, hi, base, ld, i);
+    produce<T>(a, ops, decays, wave - NR, lo, hi, base, ld);
     return;
   }
-  const int slot = a.slots ? a.slots[q] : q;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  const int i = 16 * (blockIdx.x % TILES * NR + wave % NR) + l16;  // the lane's value row
+  const int slot = a.slots ? a.slots[sq] : sq;
   const bool stored = slot >= 0 && slot < a.nslots;
   float* st = a.state + (((size_t)(stored ? slot : 0) * a.H + h) * HD + i) * HD + 4 * g;
   f4 S[4];  // keys 16 j + 4 g + v
@@ -478,83 +496,79 @@ k_wkv_chunk(const WkvArgs a) {
   const T* vp = static_cast<const T*>(a.v) + base + i;
   float* yp = a.y + base + i;
   ChunkV<T> vin;
-  if constexpr (NR > 1) vin.load(vp, ld, lo, hi);
+  vin.load(vp, ld, lo, hi);
   for (int s = 0; s < 3; s++) step_barrier();
   // the state has arrived before the loop, so that no wait inside it stands
   // for these loads (and with them for the stores of y)
 #pragma unroll
   for (int j = 0; j < 4; j++) asm volatile("" : "+v"(S[j]));
   for (int c = 0; c < n; c++) {
-    ChunkOps<NR>& o = ops[c & 1];
+    const ChunkOps& o = ops[c & 1];
     const int t0 = lo + c * CH;
-    const int at = l16 * LDT + 4 * g;
-    f4 u, y, z[4], ah[4], rh[4], bc[4], pc[4];
-    // all of the chunk's operands are asked for at once
+    P8 ap[2], qp[2], kb[4];
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+      ap[q] = P8{o.a[0][q][lane], o.a[1][q][lane]};
+      qp[q] = P8{o.q[0][q][lane], o.q[1][q][lane]};
+    }
+    const P4 mk{o.mk[0][lane], o.mk[1][lane]}, nk{o.nk[0][lane], o.nk[1][lane]};
+    const P4 xp{o.x[0][lane], o.x[1][lane]}, nb{o.nb[0][lane], o.nb[1][lane]};
+#pragma unroll
+    for (int j = 0; j < 4; j++) kb[j] = P8{o.kb[0][j][lane], o.kb[1][j][lane]};
+    bool slow = o.slow;
+    const f4 V = vin.get(t0, hi);
+    if (c + 1 < n) vin.load(vp, ld, t0 + CH, hi);
+    f4 Sq[4];
+    float big = larger(0.0f, V);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      ah[j] = *reinterpret_cast<const f4*>(&o.ah[l16 * LDR + 16 * j + 4 * g]);
-      rh[j] = *reinterpret_cast<const f4*>(&o.rh[l16 * LDR + 16 * j + 4 * g]);
+      const f4 mid = *reinterpret_cast<const f4*>(&decays[c & 3].mid[16 * j + 4 * g]);
+#pragma unroll
+      for (int v = 0; v < 4; v++) Sq[j][v] = S[j][v] * mid[v];
+      big = larger(big, Sq[j]);
     }
-    const int bad = o.bad;
-    const f4 x = *reinterpret_cast<const f4*>(&o.x[at]);
-    const f4 nb = *reinterpret_cast<const f4*>(&o.nb[at]);
+    slow = slow || too_small(big);
+    const P4 vs = split(V);
+    Sum u = none(), y = u;
+    mma(mk, vs, u);
+    mma(nk, vs, y);
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      bc[j] = *reinterpret_cast<const f4*>(&o.bcT[16 * j * LDT + at]);
-      pc[j] = *reinterpret_cast<const f4*>(&o.pc[16 * j + 4 * g]);
+    for (int q = 0; q < 2; q++) {
+      const P8 sp = join(split(Sq[2 * q]), split(Sq[2 * q + 1]));
+      mma(ap[q], sp, u);
+      mma(qp[q], sp, y);
     }
-    float zero = 0.0f;  // NaN where a state is not finite
+    Sum us = none();
+    mma(xp, split(u.value()), us);
+    const f4 U = us.value();
+    // what is not finite, or too large for an operand, in V, S or U
+    slow = slow || __ballot(!(fabsf(U[0]) + fabsf(U[1]) + fabsf(U[2]) + fabsf(U[3]) < HUGE_)) != 0;
+    if (!slow) {
+      const P4 up = split(U);
+      const P8 vu = join(vs, up);
 #pragma unroll
-    for (int j = 0; j < 4; j++)
+      for (int j = 0; j < 4; j++) {
+        const f4 end = *reinterpret_cast<const f4*>(&decays[c & 3].end[16 * j + 4 * g]);
+        Sum s = none();
 #pragma unroll
-      for (int v = 0; v < 4; v++) zero = __builtin_fmaf(S[j][v], 0.0f, zero);
-    if constexpr (NR > 1) {
-      const f4 V = vin.get(t0, hi);
-      if (c + 1 < n) vin.load(vp, ld, t0 + CH, hi);
-#pragma unroll
-      for (int v = 0; v < 4; v++) zero = __builtin_fmaf(V[v], 0.0f, zero);
-      keys_times_v(o.kcT(), V, z);
-      tokens_times_v(o.mk(), o.nk(), V, &u, &y);
-    } else {
-      const f4* src = reinterpret_cast<const f4*>(o.v) + lane;
-#pragma unroll
-      for (int j = 0; j < 4; j++) z[j] = src[64 * j];
-      u = src[256];
-      y = src[320];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-#pragma unroll
-      for (int v = 0; v < 4; v++) {
-        u = __builtin_amdgcn_mfma_f32_16x16x4f32(ah[j][v], S[j][v], u, 0, 0, 0);
-        y = __builtin_amdgcn_mfma_f32_16x16x4f32(rh[j][v], S[j][v], y, 0, 0, 0);
+        for (int v = 0; v < 4; v++) s.main[v] = S[j][v] * end[v];
+        mma(kb[j], vu, s);
+        S[j] = s.value();
       }
-    }
-    if (!bad && __ballot(!(zero == 0.0f)) == 0) {
-      const f4 U = mma4(x, u, f4{0, 0, 0, 0});
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-#pragma unroll
-        for (int v = 0; v < 4; v++) S[j][v] = __builtin_fmaf(S[j][v], pc[j][v], z[j][v]);
-#pragma unroll
-      for (int v = 0; v < 4; v++) {
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-          S[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(bc[j][v], U[v], S[j], 0, 0, 0);
-        y = __builtin_amdgcn_mfma_f32_16x16x4f32(nb[v], U[v], y, 0, 0, 0);
-      }
+      mma(nb, up, y);
+      const f4 yv = y.value();
       float* yt = yp + (size_t)(t0 + 4 * g) * ld;
       if (t0 + CH <= hi) {
 #pragma unroll
-        for (int v = 0; v < 4; v++) yt[v * ld] = y[v];
+        for (int v = 0; v < 4; v++) yt[v * ld] = yv[v];
       } else {
 #pragma unroll
         for (int v = 0; v < 4; v++)
-          if (t0 + 4 * g + v < hi) yt[v * ld] = y[v];
+          if (t0 + 4 * g + v < hi) yt[v * ld] = yv[v];
       }
     } else {
-      // a value that is not finite must not reach earlier tokens through
-      // products with the zeros of the triangular matrices
+      // token by token (a value that is not finite must not reach earlier
+      // tokens through products with the zeros of the triangular matrices)
       for (int t = t0; t < min(t0 + CH, hi); t++) {
         const size_t at = (size_t)t * ld + base + 4 * g;
         const float vt = (float)vp[(size_t)t * ld];
