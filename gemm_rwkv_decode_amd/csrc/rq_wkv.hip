@@ -151,19 +151,22 @@ struct P4 {
 struct P8 {
   h8 hi, lo;
 };
+typedef float f2 __attribute__((ext_vector_type(2)));
+// Two values in two parts.  x as rounded to binary32 (the empty asm): the
+// compiler would else round the product behind x to binary16 in one step in one
+// place and in two in another, and hi and lo would not belong together.
+__device__ __forceinline__ void split2(float x, float y, h2* hi, h2* lo) {
+  asm("" : "+v"(x), "+v"(y));
+  *hi = __builtin_convertvector(f2{x, y}, h2);
+  const f2 back = __builtin_convertvector(*hi, f2);
+  *lo = __builtin_convertvector(
+      f2{__builtin_fmaf(-UP, back.x, UP * x), __builtin_fmaf(-UP, back.y, UP * y)}, h2);
+}
 __device__ __forceinline__ P4 split(const f4& x) {
-  P4 p;
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    // x as rounded to binary32: the compiler would else round the product
-    // behind x to binary16 in one step in one place and in two in another, and
-    // hi and lo would not belong together
-    float v = x[i];
-    asm("" : "+v"(v));
-    p.hi[i] = (_Float16)v;
-    p.lo[i] = (_Float16)__builtin_fmaf(-UP, (float)p.hi[i], UP * v);
-  }
-  return p;
+  h2 h0, h1, l0, l1;
+  split2(x[0], x[1], &h0, &l0);
+  split2(x[2], x[3], &h1, &l1);
+  return P4{__builtin_shufflevector(h0, h1, 0, 1, 2, 3), __builtin_shufflevector(l0, l1, 0, 1, 2, 3)};
 }
 __device__ __forceinline__ P8 join(const P4& a, const P4& b) {
   return P8{__builtin_shufflevector(a.hi, b.hi, 0, 1, 2, 3, 4, 5, 6, 7),
@@ -244,7 +247,9 @@ __device__ __forceinline__ void step_barrier() {
 
 // Inputs of one chunk as a producer lane holds them: token lane mod 16, keys
 // 16 jt + 4 (lane / 16) .. + 3.  They stay as they were loaded until they are
-// used: a conversion here would wait for them.
+// used: a conversion here would wait for them.  Tokens past the sequence's end
+// are read from a row of zeros: nothing is added.
+__device__ const float zero_row[HD] = {0};
 template <typename T>
 struct Vec4;
 template <>
@@ -259,15 +264,33 @@ template <typename T>
 struct ChunkIn {
   typedef typename Vec4<T>::type vec;
   vec w[4], k[4], kap[4], eta[4], r[4];
-  __device__ __forceinline__ void load(const WkvArgs& a, size_t at) {
+  __device__ __forceinline__ void load(const WkvArgs& a, size_t at, size_t key, bool live) {
+    // (global addresses said to be such: the choice between two arrays would
+    // else make flat loads, which the barriers' LDS waits would wait for)
+    typedef const __attribute__((address_space(1))) T* ptr;
+    typedef const __attribute__((address_space(1))) vec* vptr;
+    const ptr z = (ptr)reinterpret_cast<const T*>(zero_row) + key;
+    const auto row = [&](const void* x) { return (ptr) static_cast<const T*>(x) + at; };
+    const ptr pw = row(a.w);
+    const ptr pk = live ? row(a.k) : z, pkap = live ? row(a.kappa) : z;
+    const ptr peta = live ? row(a.eta) : z, pr = live ? row(a.r) : z;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      w[j] = *reinterpret_cast<const vec*>(static_cast<const T*>(a.w) + at + 16 * j);
-      k[j] = *reinterpret_cast<const vec*>(static_cast<const T*>(a.k) + at + 16 * j);
-      kap[j] = *reinterpret_cast<const vec*>(static_cast<const T*>(a.kappa) + at + 16 * j);
-      eta[j] = *reinterpret_cast<const vec*>(static_cast<const T*>(a.eta) + at + 16 * j);
-      r[j] = *reinterpret_cast<const vec*>(static_cast<const T*>(a.r) + at + 16 * j);
+      w[j] = *(vptr)(pw + 16 * j);
+      k[j] = *(vptr)(pk + 16 * j);
+      kap[j] = *(vptr)(pkap + 16 * j);
+      eta[j] = *(vptr)(peta + 16 * j);
+      r[j] = *(vptr)(pr + 16 * j);
     }
+  }
+  // P of key tile j: the decays' products up to the lane's token (a token past
+  // the end does not decay)
+  __device__ __forceinline__ f4 decays(int j, bool live) const {
+    f4 P;
+#pragma unroll
+    for (int v = 0; v < 4; v++) P[v] = live ? decay_of((float)w[j][v]) : 1.0f;
+    row_scan4(P);
+    return P;
   }
 };
 
@@ -290,30 +313,54 @@ struct ChunkV {
   }
 };
 
-// The value that lanes 16 G .. 16 G + 15 hold, in every row of 16 lanes.
-template <int G>
-__device__ __forceinline__ float row_of(float v) {
-  const u32 u = __builtin_bit_cast(u32, v);
-  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);  // rows 0 0 2 2, 1 1 3 3
-  const u32 w = a[G & 1];
-  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-  const u32 r = b[G >> 1];
-  return __builtin_bit_cast(float, r);
+// X = I + Mb X by forward substitution, with row t of X in lane t of every row
+// of 16 lanes (columns 4 g + v): row T is final once the rows before it have
+// been taken off, and one DPP multiply-add per column hands every later row its
+// share, mt[T] = Mb[t][T] of the lane's row t (zero for t <= T).  A register is
+// read by DPP three instructions after it was written, one more than it has to be.
+__device__ __forceinline__ void substitute(const float* mt, f4& x) {
+  float a = x[0], b = x[1], c = x[2], d = x[3];
+#define RQ_TAKE_OFF(T, m)                                                      \
+  "v_fmac_f32_dpp %0, %0, " m " row_newbcast:" #T " row_mask:0xf bank_mask:0xf\n" \
+  "v_fmac_f32_dpp %1, %1, " m " row_newbcast:" #T " row_mask:0xf bank_mask:0xf\n" \
+  "v_fmac_f32_dpp %2, %2, " m " row_newbcast:" #T " row_mask:0xf bank_mask:0xf\n" \
+  "v_fmac_f32_dpp %3, %3, " m " row_newbcast:" #T " row_mask:0xf bank_mask:0xf\n"
+  asm("s_nop 1\n" RQ_TAKE_OFF(0, "%4") RQ_TAKE_OFF(1, "%5") RQ_TAKE_OFF(2, "%6")
+      RQ_TAKE_OFF(3, "%7") RQ_TAKE_OFF(4, "%8") RQ_TAKE_OFF(5, "%9") RQ_TAKE_OFF(6, "%10")
+      RQ_TAKE_OFF(7, "%11") RQ_TAKE_OFF(8, "%12") RQ_TAKE_OFF(9, "%13") RQ_TAKE_OFF(10, "%14")
+      RQ_TAKE_OFF(11, "%15") RQ_TAKE_OFF(12, "%16") RQ_TAKE_OFF(13, "%17")
+      RQ_TAKE_OFF(14, "%18") "s_nop 1\n"
+      : "+v"(a), "+v"(b), "+v"(c), "+v"(d)
+      : "v"(mt[0]), "v"(mt[1]), "v"(mt[2]), "v"(mt[3]), "v"(mt[4]), "v"(mt[5]), "v"(mt[6]),
+        "v"(mt[7]), "v"(mt[8]), "v"(mt[9]), "v"(mt[10]), "v"(mt[11]), "v"(mt[12]), "v"(mt[13]),
+        "v"(mt[14]));
+#undef RQ_TAKE_OFF
+  x = f4{a, b, c, d};
 }
-// X^T = I + Mb^T X^T by substitution from the last row: row T is final once the
-// rows after it have been taken off; it goes to all lanes, and every row s takes
-// Mb^T[s][T] of it (accumulator layout: rows 4 g + v, columns lane mod 16).
-template <int T>
-__device__ __forceinline__ void eliminate(const f4& m, f4& x) {
-  if constexpr (T > 0) {
-    const float xs = row_of<T / 4>(x[T % 4]);
+// m: Mb transposed, as an accumulator (rows s = 4 g + v, columns t = lane mod
+// 16).  Returns X, row t in lane t, columns 4 g + v.
+__device__ __forceinline__ f4 inverse(const f4& m) {
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  float mt[CH];  // Mb[t][T] for all T: the other lane rows' values
 #pragma unroll
-    for (int v = 0; v < 4; v++) {
-      const float mv = m[v];
-      x[v] = __builtin_fmaf(dpp_mov<0x150 + T>(mv), xs, x[v]);  // lane T of the row
-    }
-    eliminate<T - 1>(m, x);
+  for (int v = 0; v < 4; v++) {
+    const float mv = m[v];
+    const u32 u = __builtin_bit_cast(u32, mv);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);  // rows 0 0 2 2, 1 1 3 3
+    const u32 a0 = a[0], a1 = a[1];
+    const auto b = __builtin_amdgcn_permlane32_swap(a0, a0, false, false);  // row 0, row 2
+    const auto c = __builtin_amdgcn_permlane32_swap(a1, a1, false, false);  // row 1, row 3
+    const u32 b0 = b[0], b1 = b[1], c0 = c[0], c1 = c[1];
+    mt[v] = __builtin_bit_cast(float, b0);
+    mt[4 + v] = __builtin_bit_cast(float, c0);
+    mt[8 + v] = __builtin_bit_cast(float, b1);
+    mt[12 + v] = __builtin_bit_cast(float, c1);
   }
+  f4 x;
+#pragma unroll
+  for (int v = 0; v < 4; v++) x[v] = l16 == 4 * g + v ? 1.0f : 0.0f;
+  substitute(mt, x);
+  return x;
 }
 
 __device__ __forceinline__ float larger(float m, const f4& x) {
@@ -333,45 +380,42 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int n = (hi - lo + CH - 1) / CH;
   ChunkIn<T> in;
-  auto fetch = [&](int c) {
-    in.load(a, (size_t)min(lo + c * CH + l16, hi - 1) * ld + base + 4 * g);
+  const auto live = [&](int c) { return lo + c * CH + l16 < hi; };
+  const auto fetch = [&](int c) {
+    in.load(a, (size_t)min(lo + c * CH + l16, hi - 1) * ld + base + 4 * g, 4 * g, live(c));
   };
   h4 identity;
 #pragma unroll
   for (int v = 0; v < 4; v++) identity[v] = l16 == 4 * g + v ? (_Float16)1.0f : (_Float16)0.0f;
-  if (p < n) fetch(p);
+  f4 P[4];
+  fetch(p);
+  P[0] = in.decays(0, live(p));
   int steps = p;
   for (int i = 0; i < p; i++) step_barrier();
   for (int c = p; c < n; c += PRODUCERS) {
-    const int t0 = lo + c * CH;
-    // segment 1: decays and the scaled operands
+    // segment 1: decays (a quarter of them was left to the last segment of the
+    // chunk before, so that the segments are of about one length) and the scaled
+    // operands
     f4 av[4], qv[4], bv[4], kv[4], rest[4];  // rest: P_16 / Q
-    const bool live = t0 + l16 < hi;
-    if (t0 + CH > hi && !live) {  // past the end: nothing decays, nothing is added
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        in.k[j] = in.kap[j] = in.eta[j] = in.r[j] = T(0);
-        in.w[j] = T(-INFINITY);
-      }
-    }
+    P[1] = in.decays(1, live(c));
+    P[2] = in.decays(2, live(c));
+    P[3] = in.decays(3, live(c));
     float big_k = 0.0f, big_r = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      f4 P, mid, end;
-#pragma unroll
-      for (int v = 0; v < 4; v++) P[v] = decay_of((float)in.w[j][v]);
-      row_scan4(P);
+      f4 mid, end;
 #pragma unroll
       for (int v = 0; v < 4; v++) {
         const float kap = (float)in.kap[j][v], k = (float)in.k[j][v], r = (float)in.r[j][v];
-        const float inv = __builtin_amdgcn_rcpf(P[v]);
-        mid[v] = dpp_mov<0x157>(P[v]);           // lane 7 of the row: Q
+        const float pv = P[j][v];
+        const float inv = __builtin_amdgcn_rcpf(pv);
+        mid[v] = dpp_mov<0x157>(pv);           // lane 7 of the row: Q
         const float over = dpp_mov<0x157>(inv);  // 1 / Q
-        end[v] = dpp_mov<0x15F>(P[v]);           // lane 15: P_16
+        end[v] = dpp_mov<0x15F>(pv);           // lane 15: P_16
         rest[j][v] = end[v] * over;
         const float up = inv * mid[v];
-        av[j][v] = kap * (left_or_one(P[v]) * over);
-        qv[j][v] = r * (P[v] * over);
+        av[j][v] = kap * (left_or_one(pv) * over);
+        qv[j][v] = r * (pv * over);
         bv[j][v] = -((float)in.eta[j][v] * kap) * up;
         kv[j][v] = k * up;
         big_k = fmaxf(big_k, fabsf(k));
@@ -382,7 +426,15 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
         *reinterpret_cast<f4*>(&decays[c & 3].end[16 * j + 4 * g]) = end;
       }
     }
-    if (c + PRODUCERS < n) fetch(c + PRODUCERS);  // two steps ahead of its use
+    // two steps ahead of their use, into the registers that are free by now
+    // (the operands are made before, not after; past the end rows of the
+    // sequence are read again, as a branch here would make the compiler wait for
+    // the loads to move them)
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      asm volatile("" : "+v"(av[j]), "+v"(qv[j]), "+v"(bv[j]), "+v"(kv[j]), "+v"(rest[j]));
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(c + PRODUCERS);
     bool slow = too_small(big_k) || too_small(big_r);
     step_barrier();
     // segment 2: the four products' transposes, rows s = 4 g + v, columns t =
@@ -443,10 +495,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       if (4 * g + v >= l16) mbv[v] = mkv[v] = 0.0f;
       if (4 * g + v > l16) nbv[v] = nkv[v] = 0.0f;
     }
-    f4 x;
-#pragma unroll
-    for (int v = 0; v < 4; v++) x[v] = l16 == 4 * g + v ? 1.0f : 0.0f;
-    eliminate<CH - 1>(mbv, x);
+    const f4 x = inverse(mbv);
     const float big = larger(larger(larger(larger(0.0f, x), mkv), nbv), nkv);
     slow = slow || __ballot(!(zero == 0.0f) || !(big < HUGE_)) != 0;
     const P4 xp = split(x), mkp = split(mkv), nbp = split(nbv), nkp = split(nkv);
@@ -459,6 +508,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     o.nk[0][lane] = nkp.hi;
     o.nk[1][lane] = nkp.lo;
     if (lane == 0) o.slow = slow;
+    P[0] = in.decays(0, live(c + PRODUCERS));
     step_barrier();
     steps += 3;
   }
@@ -495,36 +545,45 @@ k_wkv_chunk(const WkvArgs a) {
   }
   const T* vp = static_cast<const T*>(a.v) + base + i;
   float* yp = a.y + base + i;
-  ChunkV<T> vin;
-  vin.load(vp, ld, lo, hi);
+  // V of the even and the odd chunks, two chunks ahead
+  ChunkV<T> even, odd;
+  even.load(vp, ld, lo, hi);
+  odd.load(vp, ld, min(lo + CH, hi - 1), hi);
   for (int s = 0; s < 3; s++) step_barrier();
   // the state has arrived before the loop, so that no wait inside it stands
   // for these loads (and with them for the stores of y)
 #pragma unroll
   for (int j = 0; j < 4; j++) asm volatile("" : "+v"(S[j]));
-  for (int c = 0; c < n; c++) {
+  const auto chunk = [&](int c, ChunkV<T>& vin) {
     const ChunkOps& o = ops[c & 1];
     const int t0 = lo + c * CH;
+    // operands in the order of their use (LDS answers in order)
+    bool slow = o.slow;
+    f4 mid[4], end[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      mid[j] = *reinterpret_cast<const f4*>(&decays[c & 3].mid[16 * j + 4 * g]);
+    const P4 mk{o.mk[0][lane], o.mk[1][lane]}, nk{o.nk[0][lane], o.nk[1][lane]};
     P8 ap[2], qp[2], kb[4];
 #pragma unroll
     for (int q = 0; q < 2; q++) {
       ap[q] = P8{o.a[0][q][lane], o.a[1][q][lane]};
       qp[q] = P8{o.q[0][q][lane], o.q[1][q][lane]};
     }
-    const P4 mk{o.mk[0][lane], o.mk[1][lane]}, nk{o.nk[0][lane], o.nk[1][lane]};
-    const P4 xp{o.x[0][lane], o.x[1][lane]}, nb{o.nb[0][lane], o.nb[1][lane]};
+    const P4 xp{o.x[0][lane], o.x[1][lane]};
 #pragma unroll
-    for (int j = 0; j < 4; j++) kb[j] = P8{o.kb[0][j][lane], o.kb[1][j][lane]};
-    bool slow = o.slow;
+    for (int j = 0; j < 4; j++) {
+      end[j] = *reinterpret_cast<const f4*>(&decays[c & 3].end[16 * j + 4 * g]);
+      kb[j] = P8{o.kb[0][j][lane], o.kb[1][j][lane]};
+    }
+    const P4 nb{o.nb[0][lane], o.nb[1][lane]};
     const f4 V = vin.get(t0, hi);
-    if (c + 1 < n) vin.load(vp, ld, t0 + CH, hi);
+    vin.load(vp, ld, t0 + 2 * CH, hi);
     f4 Sq[4];
     float big = larger(0.0f, V);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      const f4 mid = *reinterpret_cast<const f4*>(&decays[c & 3].mid[16 * j + 4 * g]);
-#pragma unroll
-      for (int v = 0; v < 4; v++) Sq[j][v] = S[j][v] * mid[v];
+      Sq[j] = S[j] * mid[j];
       big = larger(big, Sq[j]);
     }
     slow = slow || too_small(big);
@@ -548,10 +607,7 @@ k_wkv_chunk(const WkvArgs a) {
       const P8 vu = join(vs, up);
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        const f4 end = *reinterpret_cast<const f4*>(&decays[c & 3].end[16 * j + 4 * g]);
-        Sum s = none();
-#pragma unroll
-        for (int v = 0; v < 4; v++) s.main[v] = S[j][v] * end[v];
+        Sum s{S[j] * end[j], f4{0, 0, 0, 0}};
         mma(kb[j], vu, s);
         S[j] = s.value();
       }
@@ -600,6 +656,12 @@ k_wkv_chunk(const WkvArgs a) {
       }
     }
     step_barrier();
+  };
+  for (int c = 0;;) {
+    chunk(c, even);
+    if (++c >= n) break;
+    chunk(c, odd);
+    if (++c >= n) break;
   }
   if (stored) {
 #pragma unroll
