@@ -118,8 +118,9 @@ k_wkv_seq(const WkvArgs a) {
 // in two parts, x = hi + 2^-11 lo, both binary16: hi hi' goes to one sum, hi lo'
 // + lo hi' to a second that joins with 2^-11.  What is left out or rounded is
 // below 2^-22 of an operand (2^-36 in absolute terms for values under 2^-14),
-// so a product is as good as a binary32 one, at three binary16 MFMAs for eight
-// binary32 ones of twice the length.  The state itself, the decays, the
+// so a product is about as good as a binary32 one, and three binary16
+// instructions stand for eight binary32 ones (over 32 terms; measured against
+// those: 64 heads of 4096 tokens in 16 sequences 241 -> 184 us).  The state itself, the decays, the
 // triangular inverse and everything added up stay binary32.
 // A chunk in which a value does not fit this (not finite, 2^15 or more, or
 // nothing as large as 2^-12 in k, r, or the state and v together) is done token
@@ -243,6 +244,13 @@ __device__ __forceinline__ void step_barrier() {
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// The value is made here: left alone, the compiler moves work over a barrier to
+// where its result is used, into another segment.
+template <typename V>
+__device__ __forceinline__ void pin(V& v) {
+  asm volatile("" : "+v"(v));
 }
 
 // Inputs of one chunk as a producer lane holds them: token lane mod 16, keys
@@ -390,19 +398,18 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
   f4 P[4];
   fetch(p);
   P[0] = in.decays(0, live(p));
+  P[1] = in.decays(1, live(p));
   int steps = p;
   for (int i = 0; i < p; i++) step_barrier();
   for (int c = p; c < n; c += PRODUCERS) {
-    // segment 1: decays (a quarter of them was left to the last segment of the
-    // chunk before, so that the segments are of about one length) and the scaled
+    // segment 1: decays (half of them were left to the last segment of the chunk
+    // before, so that the segments are of about one length) and the scaled
     // operands
     f4 av[4], qv[4], bv[4], kv[4], rest[4];  // rest: P_16 / Q
-    P[1] = in.decays(1, live(c));
     P[2] = in.decays(2, live(c));
     P[3] = in.decays(3, live(c));
     float big_k = 0.0f, big_r = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
+    const auto scale = [&](int j) {
       f4 mid, end;
 #pragma unroll
       for (int v = 0; v < 4; v++) {
@@ -425,21 +432,23 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
         *reinterpret_cast<f4*>(&decays[c & 3].mid[16 * j + 4 * g]) = mid;
         *reinterpret_cast<f4*>(&decays[c & 3].end[16 * j + 4 * g]) = end;
       }
+    };
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      scale(j);
+      pin(av[j]), pin(qv[j]), pin(bv[j]), pin(kv[j]), pin(rest[j]);
     }
     // two steps ahead of their use, into the registers that are free by now
     // (the operands are made before, not after; past the end rows of the
     // sequence are read again, as a branch here would make the compiler wait for
     // the loads to move them)
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-      asm volatile("" : "+v"(av[j]), "+v"(qv[j]), "+v"(bv[j]), "+v"(kv[j]), "+v"(rest[j]));
     __builtin_amdgcn_sched_barrier(0);
     fetch(c + PRODUCERS);
-    bool slow = too_small(big_k) || too_small(big_r);
     step_barrier();
     // segment 2: the four products' transposes, rows s = 4 g + v, columns t =
     // lane mod 16, and kc and bc turned from tokens x keys to keys x tokens by
     // products with the identity, which are exact
+    bool slow = too_small(big_k) || too_small(big_r);
     P8 ap[2], qp[2], kb[4];
     Sum mb = none(), mk = mb, nb = mb, nk = mb;
 #pragma unroll
@@ -470,6 +479,9 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       }
     }
     f4 mbv = mb.value(), mkv = mk.value(), nbv = nb.value(), nkv = nk.value();
+    pin(mbv), pin(mkv), pin(nbv), pin(nkv);
+#pragma unroll
+    for (int j = 0; j < 4; j++) pin(kb[j].hi), pin(kb[j].lo);
     step_barrier();
     // segment 3: the triangular inverse, and everything to the chunk's buffer
     ChunkOps& o = ops[c & 1];
@@ -508,7 +520,11 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     o.nk[0][lane] = nkp.hi;
     o.nk[1][lane] = nkp.lo;
     if (lane == 0) o.slow = slow;
-    P[0] = in.decays(0, live(c + PRODUCERS));
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      P[j] = in.decays(j, live(c + PRODUCERS));
+      pin(P[j]);
+    }
     step_barrier();
     steps += 3;
   }
@@ -553,7 +569,7 @@ k_wkv_chunk(const WkvArgs a) {
   // the state has arrived before the loop, so that no wait inside it stands
   // for these loads (and with them for the stores of y)
 #pragma unroll
-  for (int j = 0; j < 4; j++) asm volatile("" : "+v"(S[j]));
+  for (int j = 0; j < 4; j++) pin(S[j]);
   const auto chunk = [&](int c, ChunkV<T>& vin) {
     const ChunkOps& o = ops[c & 1];
     const int t0 = lo + c * CH;
@@ -675,14 +691,24 @@ void launch_chunks(const WkvArgs& a, unsigned heads, hipStream_t s) {
                      s, a);
 }
 
+// Token by token where less than 32 tokens are not their sequence's first: the
+// chunks would be mostly empty (64 requests of one token, 32 heads: 22 us).
+//
+// A workgroup of the chunk kernel takes 16, 32 or 64 of a head's value rows.
+// Fewer rows make a chunk's step shorter (a state wave then has a SIMD to
+// itself), but the producers' work is done again by each of a head's
+// workgroups, which pays while there is a compute unit for each of these 4 or 2
+// workgroups.  Binary32, 16 / 32 / 64 rows: 64 heads of 4096 tokens 328 / 379 /
+// 392 us; 96 heads, 1000 tokens in 3 sequences 54 / 46 / 49 us; 160 heads, 2000
+// tokens in 4 115 / 74 / 73 us; 1024 heads, 4096 tokens in 16 378 / 231 / 151 us.
 template <typename T>
 void launch(const WkvArgs& a, hipStream_t s) {
   const unsigned heads = (unsigned)a.sequences * a.H;
   if (a.T - a.sequences < 32)
     hipLaunchKernelGGL((k_wkv_seq<T>), dim3(heads), dim3(256), 0, s, a);
-  else if (heads <= 80)
+  else if (heads <= 64)
     launch_chunks<T, 1>(a, heads, s);
-  else if (heads < 256)
+  else if (heads <= 128)
     launch_chunks<T, 2>(a, heads, s);
   else
     launch_chunks<T, 4>(a, heads, s);
