@@ -153,21 +153,26 @@ struct P8 {
   h8 hi, lo;
 };
 typedef float f2 __attribute__((ext_vector_type(2)));
-// Two values in two parts.  x as rounded to binary32 (the empty asm): the
-// compiler would else round the product behind x to binary16 in one step in one
-// place and in two in another, and hi and lo would not belong together.
+// Two values in two parts.
 __device__ __forceinline__ void split2(float x, float y, h2* hi, h2* lo) {
-  asm("" : "+v"(x), "+v"(y));
   *hi = __builtin_convertvector(f2{x, y}, h2);
   const f2 back = __builtin_convertvector(*hi, f2);
   *lo = __builtin_convertvector(
       f2{__builtin_fmaf(-UP, back.x, UP * x), __builtin_fmaf(-UP, back.y, UP * y)}, h2);
 }
+// Of values that are no longer visible as products (pinned, or passed through
+// rounded()): the compiler would else round the product behind x to binary16 in
+// one step in one place and in two in another, and hi and lo would not belong
+// together.
 __device__ __forceinline__ P4 split(const f4& x) {
   h2 h0, h1, l0, l1;
   split2(x[0], x[1], &h0, &l0);
   split2(x[2], x[3], &h1, &l1);
   return P4{__builtin_shufflevector(h0, h1, 0, 1, 2, 3), __builtin_shufflevector(l0, l1, 0, 1, 2, 3)};
+}
+__device__ __forceinline__ f4 rounded(f4 x) {
+  asm("" : "+v"(x));
+  return x;
 }
 __device__ __forceinline__ P8 join(const P4& a, const P4& b) {
   return P8{__builtin_shufflevector(a.hi, b.hi, 0, 1, 2, 3, 4, 5, 6, 7),
@@ -399,14 +404,14 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
   fetch(p);
   P[0] = in.decays(0, live(p));
   P[1] = in.decays(1, live(p));
+  P[2] = in.decays(2, live(p));
   int steps = p;
   for (int i = 0; i < p; i++) step_barrier();
   for (int c = p; c < n; c += PRODUCERS) {
-    // segment 1: decays (half of them were left to the last segment of the chunk
-    // before, so that the segments are of about one length) and the scaled
+    // segment 1: decays (three quarters were made in the last segment of the
+    // chunk before, so that the segments are of about one length) and the scaled
     // operands
     f4 av[4], qv[4], bv[4], kv[4], rest[4];  // rest: P_16 / Q
-    P[2] = in.decays(2, live(c));
     P[3] = in.decays(3, live(c));
     float big_k = 0.0f, big_r = 0.0f;
     const auto scale = [&](int j) {
@@ -464,7 +469,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      const P4 kp = split(kv[j] * rest[j]), bp = split(bv[j] * rest[j]);
+      const P4 kp = split(rounded(kv[j] * rest[j])), bp = split(rounded(bv[j] * rest[j]));
       const f4 z = {0, 0, 0, 0};
       const f4 kh = __builtin_amdgcn_mfma_f32_16x16x16f16(kp.hi, identity, z, 0, 0, 0);
       const f4 bh = __builtin_amdgcn_mfma_f32_16x16x16f16(bp.hi, identity, z, 0, 0, 0);
@@ -500,17 +505,21 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     // a value that is not finite, or too large for an operand, leaves none of
     // its row's or column's sums finite
     float zero = 0.0f;
+    f4 mbt, mkt, nbt, nkt;
 #pragma unroll
     for (int v = 0; v < 4; v++) {
       zero = __builtin_fmaf(mbv[v], 0.0f, __builtin_fmaf(mkv[v], 0.0f, zero));
       zero = __builtin_fmaf(nbv[v], 0.0f, __builtin_fmaf(nkv[v], 0.0f, zero));
-      if (4 * g + v >= l16) mbv[v] = mkv[v] = 0.0f;
-      if (4 * g + v > l16) nbv[v] = nkv[v] = 0.0f;
+      const bool before = 4 * g + v < l16, upto = 4 * g + v <= l16;
+      mbt[v] = before ? mbv[v] : 0.0f;
+      mkt[v] = before ? mkv[v] : 0.0f;
+      nbt[v] = upto ? nbv[v] : 0.0f;
+      nkt[v] = upto ? nkv[v] : 0.0f;
     }
-    const f4 x = inverse(mbv);
-    const float big = larger(larger(larger(larger(0.0f, x), mkv), nbv), nkv);
+    const f4 x = inverse(mbt);
+    const float big = larger(larger(larger(larger(0.0f, x), mkt), nbt), nkt);
     slow = slow || __ballot(!(zero == 0.0f) || !(big < HUGE_)) != 0;
-    const P4 xp = split(x), mkp = split(mkv), nbp = split(nbv), nkp = split(nkv);
+    const P4 xp = split(x), mkp = split(mkt), nbp = split(nbt), nkp = split(nkt);
     o.x[0][lane] = xp.hi;
     o.x[1][lane] = xp.lo;
     o.mk[0][lane] = mkp.hi;
@@ -521,7 +530,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     o.nk[1][lane] = nkp.lo;
     if (lane == 0) o.slow = slow;
 #pragma unroll
-    for (int j = 0; j < 2; j++) {
+    for (int j = 0; j < 3; j++) {
       P[j] = in.decays(j, live(c + PRODUCERS));
       pin(P[j]);
     }
@@ -532,7 +541,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
 }
 
 template <typename T, int NR>
-__global__ void __launch_bounds__(64 * (NR + PRODUCERS))
+__global__ void __launch_bounds__(64 * (NR + PRODUCERS), 2)
 k_wkv_chunk(const WkvArgs a) {
   __shared__ ChunkOps ops[2];
   __shared__ ChunkDecays decays[4];
@@ -599,7 +608,7 @@ k_wkv_chunk(const WkvArgs a) {
     float big = larger(0.0f, V);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      Sq[j] = S[j] * mid[j];
+      Sq[j] = rounded(S[j] * mid[j]);
       big = larger(big, Sq[j]);
     }
     slow = slow || too_small(big);
@@ -614,8 +623,8 @@ k_wkv_chunk(const WkvArgs a) {
       mma(qp[q], sp, y);
     }
     Sum us = none();
-    mma(xp, split(u.value()), us);
-    const f4 U = us.value();
+    mma(xp, split(rounded(u.value())), us);
+    const f4 U = rounded(us.value());
     // what is not finite, or too large for an operand, in V, S or U
     slow = slow || __ballot(!(fabsf(U[0]) + fabsf(U[1]) + fabsf(U[2]) + fabsf(U[3]) < HUGE_)) != 0;
     if (!slow) {
