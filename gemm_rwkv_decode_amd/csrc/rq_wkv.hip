@@ -208,10 +208,10 @@ struct alignas(16) ChunkOps {
   h4 x[2][64], nb[2][64], mk[2][64], nk[2][64];
   int slow;         // token by token
 };
-// Q and P_16 of a chunk.  Written two steps before the other operands, so four
+// Q and then P_16 of a chunk.  Written two steps before the other operands, so four
 // of them in turn.
 struct alignas(16) ChunkDecays {
-  float mid[HD], end[HD];
+  float at[2][HD];
 };
 
 // product over the lanes of a row of 16 up to this one, for four values: a
@@ -230,11 +230,17 @@ __device__ __forceinline__ void row_scan4(f4& p) {
 #undef RQ_SCAN_STEP
   p = f4{a, b, c, d};
 }
-// the left neighbour's value, 1 in a row's first lane
-__device__ __forceinline__ float left_or_one(float v) {
+// the left neighbour's value, `first` in a row's first lane
+__device__ __forceinline__ float left_or(float v, float first) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
-                                       0x3f800000, __builtin_bit_cast(int, v), 0x111, 0xF, 0xF,
-                                       false));
+                                       __builtin_bit_cast(int, first), __builtin_bit_cast(int, v),
+                                       0x111, 0xF, 0xF, false));
+}
+// lane N of the row of 16
+template <int N>
+__device__ __forceinline__ float row_bcast(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x150 + N, 0xF, 0xF, true));
 }
 
 // Barrier that waits for this wave's LDS accesses only: loads of later chunks
@@ -415,28 +421,23 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     P[3] = in.decays(3, live(c));
     float big_k = 0.0f, big_r = 0.0f;
     const auto scale = [&](int j) {
-      f4 mid, end;
 #pragma unroll
       for (int v = 0; v < 4; v++) {
         const float kap = (float)in.kap[j][v], k = (float)in.k[j][v], r = (float)in.r[j][v];
         const float pv = P[j][v];
         const float inv = __builtin_amdgcn_rcpf(pv);
-        mid[v] = dpp_mov<0x157>(pv);           // lane 7 of the row: Q
-        const float over = dpp_mov<0x157>(inv);  // 1 / Q
-        end[v] = dpp_mov<0x15F>(pv);           // lane 15: P_16
-        rest[j][v] = end[v] * over;
-        const float up = inv * mid[v];
-        av[j][v] = kap * (left_or_one(pv) * over);
-        qv[j][v] = r * (pv * over);
+        const float over = row_bcast<7>(inv);  // 1 / Q
+        const float rel = pv * over, up = inv * row_bcast<7>(pv);
+        rest[j][v] = row_bcast<15>(rel);
+        av[j][v] = kap * left_or(rel, over);
+        qv[j][v] = r * rel;
         bv[j][v] = -((float)in.eta[j][v] * kap) * up;
         kv[j][v] = k * up;
         big_k = fmaxf(big_k, fabsf(k));
         big_r = fmaxf(big_r, fabsf(r));
       }
-      if (l16 == 0) {
-        *reinterpret_cast<f4*>(&decays[c & 3].mid[16 * j + 4 * g]) = mid;
-        *reinterpret_cast<f4*>(&decays[c & 3].end[16 * j + 4 * g]) = end;
-      }
+      // Q is token 7's P, P_16 token 15's
+      if ((l16 & 7) == 7) *reinterpret_cast<f4*>(&decays[c & 3].at[l16 >> 3][16 * j + 4 * g]) = P[j];
     };
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -545,9 +546,12 @@ __global__ void __launch_bounds__(64 * (NR + PRODUCERS), 2)
 k_wkv_chunk(const WkvArgs a) {
   __shared__ ChunkOps ops[2];
   __shared__ ChunkDecays decays[4];
-  // heads are the fast index: a sequence's workgroups go to all XCDs
+  // heads are the fast index: a sequence's workgroups go to all XCDs, a head's
+  // (they read the same inputs) to one
   constexpr int TILES = 4 / NR;
-  const int sq = blockIdx.x / (a.H * TILES), h = blockIdx.x % (a.H * TILES) / TILES;
+  const int b = blockIdx.x, hd = b / (8 * TILES) * 8 + b % 8, tile = b / 8 % TILES;
+  if (hd >= a.sequences * a.H) return;
+  const int sq = hd / a.H, h = hd % a.H;
   const int lo = max(a.offsets[sq], 0), hi = min(a.offsets[sq + 1], a.T);
   if (lo >= hi) return;
   const int n = (hi - lo + CH - 1) / CH;
@@ -558,7 +562,7 @@ k_wkv_chunk(const WkvArgs a) {
     return;
   }
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-  const int i = 16 * (blockIdx.x % TILES * NR + wave % NR) + l16;  // the lane's value row
+  const int i = 16 * (tile * NR + wave % NR) + l16;  // the lane's value row
   const int slot = a.slots ? a.slots[sq] : sq;
   const bool stored = slot >= 0 && slot < a.nslots;
   float* st = a.state + (((size_t)(stored ? slot : 0) * a.H + h) * HD + i) * HD + 4 * g;
@@ -587,7 +591,7 @@ k_wkv_chunk(const WkvArgs a) {
     f4 mid[4], end[4];
 #pragma unroll
     for (int j = 0; j < 4; j++)
-      mid[j] = *reinterpret_cast<const f4*>(&decays[c & 3].mid[16 * j + 4 * g]);
+      mid[j] = *reinterpret_cast<const f4*>(&decays[c & 3].at[0][16 * j + 4 * g]);
     const P4 mk{o.mk[0][lane], o.mk[1][lane]}, nk{o.nk[0][lane], o.nk[1][lane]};
     P8 ap[2], qp[2], kb[4];
 #pragma unroll
@@ -598,7 +602,7 @@ k_wkv_chunk(const WkvArgs a) {
     const P4 xp{o.x[0][lane], o.x[1][lane]};
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      end[j] = *reinterpret_cast<const f4*>(&decays[c & 3].end[16 * j + 4 * g]);
+      end[j] = *reinterpret_cast<const f4*>(&decays[c & 3].at[1][16 * j + 4 * g]);
       kb[j] = P8{o.kb[0][j][lane], o.kb[1][j][lane]};
     }
     const P4 nb{o.nb[0][lane], o.nb[1][lane]};
@@ -682,12 +686,14 @@ k_wkv_chunk(const WkvArgs a) {
     }
     step_barrier();
   };
-  for (int c = 0;;) {
+  // (no way out between the two: on it, the compiler would see the even chunk's
+  // loads as the newest ones at the loop's head, and wait for all)
+  int c = 0;
+  for (; c + 2 <= n; c += 2) {
     chunk(c, even);
-    if (++c >= n) break;
-    chunk(c, odd);
-    if (++c >= n) break;
+    chunk(c + 1, odd);
   }
+  if (c < n) chunk(c, even);
   if (stored) {
 #pragma unroll
     for (int j = 0; j < 4; j++) *reinterpret_cast<f4*>(st + 16 * j) = S[j];
@@ -696,7 +702,7 @@ k_wkv_chunk(const WkvArgs a) {
 
 template <typename T, int NR>
 void launch_chunks(const WkvArgs& a, unsigned heads, hipStream_t s) {
-  hipLaunchKernelGGL((k_wkv_chunk<T, NR>), dim3(heads * (4 / NR)), dim3(64 * (NR + PRODUCERS)), 0,
+  hipLaunchKernelGGL((k_wkv_chunk<T, NR>), dim3((heads + 7) / 8 * 8 * (4 / NR)), dim3(64 * (NR + PRODUCERS)), 0,
                      s, a);
 }
 
