@@ -410,14 +410,14 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
   fetch(p);
   P[0] = in.decays(0, live(p));
   P[1] = in.decays(1, live(p));
-  P[2] = in.decays(2, live(p));
   int steps = p;
   for (int i = 0; i < p; i++) step_barrier();
   for (int c = p; c < n; c += PRODUCERS) {
-    // segment 1: decays (three quarters were made in the last segment of the
+    // segment 1: decays (half of them were made in the last segment of the
     // chunk before, so that the segments are of about one length) and the scaled
     // operands
     f4 av[4], qv[4], bv[4], kv[4], rest[4];  // rest: P_16 / Q
+    P[2] = in.decays(2, live(c));
     P[3] = in.decays(3, live(c));
     float big_k = 0.0f, big_r = 0.0f;
     const auto scale = [&](int j) {
@@ -531,7 +531,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     o.nk[1][lane] = nkp.lo;
     if (lane == 0) o.slow = slow;
 #pragma unroll
-    for (int j = 0; j < 3; j++) {
+    for (int j = 0; j < 2; j++) {
       P[j] = in.decays(j, live(c + PRODUCERS));
       pin(P[j]);
     }
