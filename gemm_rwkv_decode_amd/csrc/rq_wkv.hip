@@ -617,9 +617,11 @@ k_wkv_chunk(const WkvArgs a) {
     }
     slow = slow || too_small(big);
     const P4 vs = split(V);
+    // (32 deep beside zeros: a 16-deep instruction's sum is not carried on by a
+    // 32-deep one, which, right behind it, took half of the sum for zero)
+    const h4 no = {0, 0, 0, 0};
     Sum u = none(), y = u;
-    mma(mk, vs, u);
-    mma(nk, vs, y);
+    mma(join(mk, P4{no, no}), join(vs, vs), u);
 #pragma unroll
     for (int q = 0; q < 2; q++) {
       const P8 sp = join(split(Sq[2 * q]), split(Sq[2 * q + 1]));
@@ -640,7 +642,7 @@ k_wkv_chunk(const WkvArgs a) {
         mma(kb[j], vu, s);
         S[j] = s.value();
       }
-      mma(nb, up, y);
+      mma(join(nk, nb), vu, y);
       const f4 yv = y.value();
       float* yt = yp + (size_t)(t0 + 4 * g) * ld;
       if (t0 + CH <= hi) {
@@ -702,8 +704,8 @@ k_wkv_chunk(const WkvArgs a) {
 
 template <typename T, int NR>
 void launch_chunks(const WkvArgs& a, unsigned heads, hipStream_t s) {
-  hipLaunchKernelGGL((k_wkv_chunk<T, NR>), dim3((heads + 7) / 8 * 8 * (4 / NR)), dim3(64 * (NR + PRODUCERS)), 0,
-                     s, a);
+  hipLaunchKernelGGL((k_wkv_chunk<T, NR>), dim3((heads + 7) / 8 * 8 * (4 / NR)),
+                     dim3(64 * (NR + PRODUCERS)), 0, s, a);
 }
 
 // Token by token where less than 32 tokens are not their sequence's first: the
@@ -713,9 +715,10 @@ void launch_chunks(const WkvArgs& a, unsigned heads, hipStream_t s) {
 // Fewer rows make a chunk's step shorter (a state wave then has a SIMD to
 // itself), but the producers' work is done again by each of a head's
 // workgroups, which pays while there is a compute unit for each of these 4 or 2
-// workgroups.  Binary32, 16 / 32 / 64 rows: 64 heads of 4096 tokens 328 / 379 /
-// 392 us; 96 heads, 1000 tokens in 3 sequences 54 / 46 / 49 us; 160 heads, 2000
-// tokens in 4 115 / 74 / 73 us; 1024 heads, 4096 tokens in 16 378 / 231 / 151 us.
+// workgroups.  Binary32, 16 / 32 / 64 rows: one prompt of 4096 tokens, 64 heads
+// 271 / 354 / 380 us; of 1000 tokens, 72 heads 107 / 92 / 97, 128 heads 109 /
+// 94 / 97, 160 heads 166 / 179 / 98; 4096 tokens in 16 sequences, 64 heads 250 /
+// 215 / 145 us.
 template <typename T>
 void launch(const WkvArgs& a, hipStream_t s) {
   const unsigned heads = (unsigned)a.sequences * a.H;
