@@ -8,13 +8,15 @@
 //
 // Bound by the logits' traffic (8 bytes a value) where rows are many, by the
 // chain of dependent loads and atomics (offsets, history, logits, maximum,
-// arrival) where they are few.  A workgroup takes slices of one row: it issues
-// the loads of a slice's logits, counts the history's tokens that fall into
-// the slice in LDS (integer atomics, whose order does not matter), and applies
-// all steps on the way out.  No table of counts goes through memory, and nothing
-// is sorted; the price is that every slice reads the row's whole history (from
-// L2).  An entry of the bias list is remembered the same way, by its place, so
-// that of several the last holds.
+// arrival) where they are few.  A workgroup takes a range of one row's tokens:
+// it asks for its first logits, counts the history's tokens that fall into the
+// range in LDS (integer atomics, whose order does not matter; 16 bits a token,
+// so that a row of 65536 is one range), and applies all steps as the logits
+// stream through.  No table of counts goes through memory, and nothing is
+// sorted; the price is that every range reads the row's whole history (from L2).
+// An entry of the bias list is remembered the same way, by its place, so that
+// of several the last holds.  200 x 65529 with histories of 9000 to 12000: 29 us,
+// 3.9 TB/s (in slices of 8192 tokens with 32-bit counts 47 us).
 //
 // The greatest: the values' order as an integer in the upper half, the
 // complement of the token's number in the lower half, so the maximum is the
@@ -22,6 +24,8 @@
 // workgroups join through one device-scope atomic maximum and an arrival
 // counter; the last one writes the token and leaves both zero.  No workgroup
 // waits for another.
+#include <type_traits>
+
 #include "rq_common.h"
 #include "rq_internal.h"
 
@@ -32,6 +36,8 @@ typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef unsigned long long u64;
 
 constexpr u32 SEEN = 0x80000000u;  // in the history at all; low bits: count generated
+constexpr u32 SEEN_HALF = 0x8000u;  // the same of a 16-bit count
+constexpr int MAX_HALF = 0x7FFF;
 
 struct Range {
   int lo, hi;
@@ -90,18 +96,41 @@ __device__ __forceinline__ void for_list(const int* list, int lo, int hi, int* t
   }
 }
 
-// A workgroup takes `per` slices of 4 Q NT tokens of one row, one after another.
-template <int NT, int Q>
+// Occurrences of a slice's tokens, 16 bits a token, or 32 where a row has more
+// generated tokens than 15 bits hold (`big`).
+__device__ __forceinline__ void count_token(u32* cnt, u32 t, bool generated, bool big) {
+  const int sh = big ? 0 : 16 * (t & 1);
+  const u32 seen = big ? SEEN : SEEN_HALF;
+  u32* const word = cnt + (big ? t : t / 2);
+  if (generated) atomicAdd(word, 1u << sh);
+  else atomicOr(word, seen << sh);
+}
+// of the four tokens from t on
+__device__ __forceinline__ u32x4 counts_of(const u32* cnt, u32 t, bool big) {
+  if (big) return *reinterpret_cast<const u32x4*>(cnt + t);
+  const u32x2 w = *reinterpret_cast<const u32x2*>(cnt + t / 2);
+  u32x4 c;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const u32 h = (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+    c[i] = (h & (u32)MAX_HALF) | ((h & SEEN_HALF) << 16);
+  }
+  return c;
+}
+
+// A workgroup takes `per` tokens of one row, in slices of `sl` tokens (half as
+// many where the counts need 32 bits), and a slice in steps of 4 NT.
+template <int NT>
 __global__ void __launch_bounds__(NT)
-k_logits(const LogitsArgs a, u64* records, int stride, int per) {
-  constexpr int SL = 4 * NT * Q;
-  extern __shared__ u32 lds[];  // counts [SL], then the bias entries [SL]
+k_logits(const LogitsArgs a, u64* records, int stride, int per, int sl) {
+  constexpr int STEP = 4 * NT;
+  extern __shared__ __attribute__((aligned(16))) u32 lds[];  // counts, then bias entries [sl]
   __shared__ u64 wave_best[NT / 64];
   u32* cnt = lds;
-  u32* ent = lds + (a.history ? SL : 0);
+  u32* ent = lds + (a.history ? sl / 2 : 0);
   const int tid = threadIdx.x;
   const int m = blockIdx.y;
-  const int first = blockIdx.x * per * SL, last = min(first + per * SL, a.V);
+  const int first = blockIdx.x * per, last = min(first + per, a.V);
   const float* x = a.logits + (size_t)m * a.V;
   float* out = a.out + (size_t)m * a.V;
   // what the loads below wait for, asked for together
@@ -112,37 +141,32 @@ k_logits(const LogitsArgs a, u64* records, int stride, int per) {
   const float rep = a.repetition ? a.repetition[m] : 1.0f;
   const float freq = a.frequency ? a.frequency[m] : 0.0f;
   const float pres = a.presence ? a.presence[m] : 0.0f;
-  const int own = hr.lo + max(given, 0);
+  const int own = hr.lo + min(max(given, 0), hr.hi - hr.lo);
+  const bool big = hr.hi - own > MAX_HALF;
+  const int span = big ? sl / 2 : sl;
   const bool masked = mid >= 0 && mid < a.nmasks;
   const u32* mrow = a.masks + (masked ? (size_t)mid * ((a.V + 31) / 32) : 0);
 
-  f4 next[Q];
-  u32 next_word[Q];
-  const auto fetch = [&](int v0) {
-#pragma unroll
-    for (int q = 0; q < Q; q++) {
-      const int e = v0 + (q * NT + tid) * 4;
-      next[q] = f4{0, 0, 0, 0};
-      next_word[q] = ~0u;
-      if (e + 4 <= last) {
-        next[q] = *reinterpret_cast<const f4u*>(x + e);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 3; c++)
-          if (e + c < last) next[q][c] = x[e + c];
-      }
-      if (masked && e < last) next_word[q] = mrow[e / 32];
-    }
+  f4 next;
+  u32 next_word = ~0u;
+  // Of the step at u0, which may pass the end of its slice and of the row: no
+  // load depends on a branch, or the compiler would wait for stores with them.
+  // What lies past the row's end is some other value of it.
+  const auto fetch = [&](int u0) {
+    if (a.V < 4) return;
+    const int e = u0 + tid * 4;
+    next = *reinterpret_cast<const f4u*>(x + min(e, a.V - 4));
+    if (masked) next_word = mrow[min(e, a.V - 1) / 32];
   };
   int ht[AHEAD], bt[AHEAD];
   fetch(first);
   list_batch<NT>(a.history, hr.lo + tid, hr.hi, ht);
   list_batch<NT>(a.bias_ids, br.lo + tid, br.hi, bt);
   u64 top = 0;
-  for (int v0 = first; v0 < last; v0 += SL) {
-    const int n = min(SL, last - v0);
+  for (int v0 = first; v0 < last; v0 += span) {
+    const int n = min(span, last - v0);
     if (a.history || a.bias_ids) {
-      const int words = (a.history ? SL : 0) + (a.bias_ids ? SL : 0);
+      const int words = (a.history ? sl / 2 : 0) + (a.bias_ids ? sl : 0);
       for (int i = tid * 4; i < words; i += NT * 4)
         *reinterpret_cast<u32x4*>(lds + i) = u32x4{0, 0, 0, 0};
       __syncthreads();
@@ -150,10 +174,7 @@ k_logits(const LogitsArgs a, u64* records, int stride, int per) {
         if (v0 > first) list_batch<NT>(a.history, hr.lo + tid, hr.hi, ht);
         for_list<NT>(a.history, hr.lo, hr.hi, ht, [&](int i, int token) {
           const u32 t = (u32)token - (u32)v0;
-          if (t < (u32)n) {
-            if (i < own) atomicOr(&cnt[t], SEEN);
-            else atomicAdd(&cnt[t], 1u);
-          }
+          if (t < (u32)n) count_token(cnt, t, i >= own, big);
         });
       }
       if (a.bias_ids) {
@@ -165,48 +186,55 @@ k_logits(const LogitsArgs a, u64* records, int stride, int per) {
       }
       __syncthreads();
     }
-    f4 z[Q];
-    u32 word[Q];
+    const auto step = [&](int u0, auto whole) {
+      f4 z = next;
+      u32 word = next_word;
+      fetch(u0 + STEP < n ? v0 + u0 + STEP : v0 + span);
+      const int e = u0 + tid * 4;
+      const bool all = whole() || e + 4 <= n;
+      if (!whole() && e >= n) return;
+      if (!all) {
 #pragma unroll
-    for (int q = 0; q < Q; q++) {
-      z[q] = next[q];
-      word[q] = next_word[q];
-    }
-    if (v0 + SL < last) fetch(v0 + SL);
-#pragma unroll
-    for (int q = 0; q < Q; q++) {
-      const int e = (q * NT + tid) * 4;
+        for (int c = 0; c < 3; c++)
+          if (e + c < n) z[c] = x[v0 + e + c];
+        if (masked) word = mrow[(v0 + e) / 32];
+      }
       if (a.history) {
-        const u32x4 c = *reinterpret_cast<const u32x4*>(cnt + e);
+        const u32x4 c = counts_of(cnt, e, big);
 #pragma unroll
-        for (int i = 0; i < 4; i++) z[q][i] = apply_one(z[q][i], c[i], rep, freq, pres);
+        for (int i = 0; i < 4; i++) z[i] = apply_one(z[i], c[i], rep, freq, pres);
       }
       if (a.bias_ids) {
         const u32x4 b = *reinterpret_cast<const u32x4*>(ent + e);
 #pragma unroll
         for (int i = 0; i < 4; i++)
-          if (b[i]) z[q][i] += a.bias[b[i] - 1];
+          if (b[i]) z[i] += a.bias[b[i] - 1];
       }
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        if (!((word[q] >> (e % 32 + i)) & 1u)) z[q][i] = -__builtin_inff();
+        if (!((word >> ((v0 + e) % 32 + i)) & 1u)) z[i] = -__builtin_inff();
       if (a.tokens) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          const u32 o = e + i < n ? order_of(z[q][i]) : 0u;
+          const u32 o = all || e + i < n ? order_of(z[i]) : 0u;
           const u64 key = o ? ((u64)o << 32) | (u32)~(u32)(v0 + e + i) : 0;
           top = key > top ? key : top;
         }
       }
-      if (e + 4 <= n) {
-        *reinterpret_cast<f4u*>(out + v0 + e) = z[q];
+      if (all) {
+        // (past the caches: logits and outputs of many rows are larger than they
+        // are; 256 x 65536 36 -> 30 us)
+        __builtin_nontemporal_store((f4u)z, reinterpret_cast<f4u*>(out + v0 + e));
       } else {
 #pragma unroll
         for (int c = 0; c < 3; c++)
-          if (e + c < n) out[v0 + e + c] = z[q][c];
+          if (e + c < n) out[v0 + e + c] = z[c];
       }
-    }
-    if ((a.history || a.bias_ids) && v0 + SL < last) __syncthreads();  // before the next clearing
+    };
+    int u0 = 0;
+    for (; u0 + STEP <= n; u0 += STEP) step(u0, std::true_type());
+    if (u0 < n) step(u0, std::false_type());
+    if ((a.history || a.bias_ids) && v0 + span < last) __syncthreads();  // before the clearing
   }
   if (!a.tokens) return;
 #pragma unroll
@@ -236,12 +264,30 @@ k_logits(const LogitsArgs a, u64* records, int stride, int per) {
   a.tokens[m] = top ? (int)~(u32)top : -1;
 }
 
-template <int NT, int Q>
-void launch_slices(const LogitsArgs& a, u64* records, int stride, int per, hipStream_t s) {
-  constexpr int SL = 4 * NT * Q;
-  const size_t lds = ((a.history ? SL : 0) + (a.bias_ids ? SL : 0)) * sizeof(u32);
-  hipLaunchKernelGGL((k_logits<NT, Q>), dim3((a.V + per * SL - 1) / (per * SL), a.M), dim3(NT), lds,
-                     s, a, records, stride, per);
+// `workgroups` of a row, each in as few slices as its LDS allows.
+constexpr size_t LOGITS_LDS = 152 << 10;
+template <int NT>
+hipError_t launch_slices(const LogitsArgs& a, u64* records, int stride, int workgroups,
+                         hipStream_t s) {
+  constexpr int STEP = 4 * NT;
+  const int steps = (a.V + STEP - 1) / STEP;
+  const int own = (steps + workgroups - 1) / workgroups;  // of a workgroup
+  const size_t token = (a.history ? 2 : 0) + (a.bias_ids ? 4 : 0);  // bytes
+  const int most = token ? (int)(LOGITS_LDS / (token * STEP)) : own;
+  const int slices = (own + most - 1) / most;
+  const int sl = (own + slices - 1) / slices * STEP;
+  const size_t lds = token * sl;
+  static bool raised = false;  // allow the full LDS once per instantiation
+  if (!raised) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_logits<NT>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             LOGITS_LDS);
+    if (e != hipSuccess) return e;
+    raised = true;
+  }
+  hipLaunchKernelGGL((k_logits<NT>), dim3((steps + own - 1) / own, a.M), dim3(NT), lds, s, a,
+                     records, stride, own * STEP, sl);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -253,19 +299,16 @@ hipError_t launch_logits(const LogitsArgs& a, void* ws, hipStream_t s) {
   // of 1024, records 16 bytes apart 41 us, 1 KiB apart 12.4 us)
   int stride = 2 * LOGITS_MAX_M;  // in 8 bytes
   for (int m = 1; m < a.M; m *= 2) stride /= 2;
-  // Up to 2^20 values: slices of 2048, a workgroup each, for the most
-  // workgroups (1 x 65536 5.3 us, slices of 8192 7.0 us; 16 x 65536 7.9 and
-  // 9.1 us).  Above: slices of 8192, so that the history is read by fewer of
-  // them, and one workgroup per CU that takes several with the next slice's
-  // loads in flight (64 x 65536 with histories of 1000 14.2 us, slices of 2048
-  // 23 us; 200 x 65529 with histories of 12000 45.6 and 86 us).
-  if ((long long)a.M * a.V <= 1 << 20) {
-    launch_slices<512, 1>(a, records, stride, 1, s);
-  } else {
-    const int slices = (a.V + 8191) / 8192, workgroups = a.M < 256 ? 256 / a.M : 1;  // of a row
-    launch_slices<1024, 2>(a, records, stride, (slices + workgroups - 1) / workgroups, s);
-  }
-  return hipGetLastError();
+  // Workgroups of 512 threads and 2048 tokens while that makes no more than one
+  // for each compute unit (1 x 65536 5.3 us, in slices of 8192 7.0; 8 x 65536 7.3
+  // and 8.3), or where a row has no more tokens (4000 x 2000 44 and 84 us).  Else
+  // 1024 threads, and as many workgroups as compute units or rows: the history
+  // is read by few (200 x 4096 7.6 and 9.1 us; 64 x 65536 with histories of 4000
+  // 12.8 and 27 us; 16 x 65536 8.1 and 8.0 us).
+  const int small = (a.V + 2047) / 2048;
+  if ((long long)a.M * small <= 256 || small == 1)
+    return launch_slices<512>(a, records, stride, small, s);
+  return launch_slices<1024>(a, records, stride, a.M < 256 ? 256 / a.M : 1, s);
 }
 
 }  // namespace rq

@@ -241,3 +241,31 @@ def test_more_rows_than_compute_units():
     z = np.random.default_rng(7).standard_normal((M, V)).astype(np.float32)
     out, tok = run(z)
     assert same_bits(out, z) and np.array_equal(tok.cpu().numpy(), z.argmax(1))
+
+
+@pytest.mark.parametrize("M,V,L,nb", [(20, 65529, 500, 30), (6, 150001, 800, 0), (260, 40001, 60, 4),
+                                      (300, 66003, 40, 0), (400, 1999, 50, 3), (70, 2, 9, 2)])
+def test_ranges_of_every_length(M, V, L, nb):
+    """Rows dealt out over one and several workgroups, ranges in one and several
+    slices."""
+    say(f"[logits] M {M} V {V}")
+    z, hist, pen, bias, bits, which = make(M, V, L, nb, 2, M + V)
+    bias = bias if nb else None
+    want, tok = R.logits_ref(z, hist, **pen, bias=bias, masks=(bits, which))
+    out, got = run(z, **device_args(hist, pen, bias, bits, which))
+    assert same_bits(out, want) and got.tolist() == tok.tolist()
+
+
+@pytest.mark.parametrize("M,V", [(3, 9001), (30, 65529)])
+@pytest.mark.parametrize("given", [0, 10, 40000 - 32768, 40000 - 32767, 40000])
+def test_counts_past_fifteen_bits(M, V, given):
+    """One row with more generated tokens than a 16-bit count holds, and at its
+    limit, most of them one token; the others short."""
+    say(f"[logits] M {M} V {V} given {given}")
+    z, hist, pen, bias, bits, which = make(M, V, 50, 3, 2, 9)
+    g = np.random.default_rng(8)
+    toks = np.where(g.random(40000) < 0.98, V - 1, g.integers(0, V, 40000))
+    hist[1] = (toks, given)
+    want, tok = R.logits_ref(z, hist, **pen, bias=bias, masks=(bits, which))
+    out, got = run(z, **device_args(hist, pen, bias, bits, which))
+    assert same_bits(out, want) and got.tolist() == tok.tolist()
