@@ -15,7 +15,8 @@
 #include "rq_internal.h"
 #include "rq_probe.h"
 
-static_assert(RQ_WKV_HEAD == rq::WKV_HEAD && RQ_LORA_MAX_RANK == rq::LORA_MAX_RANK &&
+static_assert(RQ_SHIFT_MAX_MIXES == rq::SHIFT_MAX_MIXES && RQ_WKV_HEAD == rq::WKV_HEAD &&
+              RQ_LORA_MAX_RANK == rq::LORA_MAX_RANK &&
               RQ_LORA_MAX_BATCH == rq::LORA_BATCH && RQ_LOGITS_MAX_M == rq::LOGITS_MAX_M &&
               RQ_LOGITS_MAX_M * 16 <= RQ_LOGITS_WORKSPACE_BYTES,
               "the interface's limits are the kernels'");

@@ -88,6 +88,8 @@ hipError_t launch_dequant(const void* qweight, const void* scales, const void* z
                           void* out, int N, int K, int group, int fmt, int out_kind,
                           hipStream_t s);
 
+constexpr int SHIFT_MAX_MIXES = 8;
+
 // Token shift (rq_shift.hip); pointers as in rq.h.
 struct ShiftArgs {
   const _Float16* x;   // [T][D]
