@@ -105,9 +105,9 @@ __device__ __forceinline__ int list_rows(u64 rows, unsigned char* list) {
 // share of K: rounds of 128 columns, every `stride`-th one.  MFMA: A operand =
 // adapter rows, B operand = activation rows, so a lane ends with four
 // consecutive rank entries of one row.  The 16-byte loads of U rounds are asked
-// for before their first product.  (Rounds are
-// dealt out in turn because rows are a power of two apart: waves that walk
-// ranges of their own would all ask the same memory channel.)
+// for before their first product.  (Rounds are dealt out in turn because rows are
+// a power of two apart: waves that walk ranges of their own would all ask the
+// same memory channel.)
 template <int TILES, int U>
 __device__ __forceinline__ void down_rounds(const _Float16* ap, const _Float16* const* xp, int K,
                                             int first, int stride, f4* acc) {
@@ -412,11 +412,14 @@ k_lora_up(const LoraBatch bt, const LoraArgs a) {
 
 // Shares of K over workgroups: about LORA_WORKGROUPS workgroups in all, with
 // two rounds of 128 columns for each of their four waves (one batch of loads;
-// smaller shares cost the second launch more than they save here).
+// smaller shares cost the second launch more than they save here).  Of several
+// blocks of rows, most are taken to have one adapter, as prompts do (1800 rows
+// of 24 adapters of rank 32, three projections 4096x4096: 69 us; as for a block
+// of requests, one adapter a row, 83 us).
 int lora_splits(int count, int M, int K, int adapters, int max_rank) {
-  const int rows = M < ROWS ? M : ROWS;
-  const long long wgs = (long long)count * ((M + ROWS - 1) / ROWS) * ((max_rank + 15) / 16) *
-                        (rows < adapters ? rows : adapters);
+  const int each = M > ROWS ? 1 : M < adapters ? M : adapters;  // adapters of a block
+  const long long wgs =
+      (long long)count * ((M + ROWS - 1) / ROWS) * ((max_rank + 15) / 16) * each;
   long long s = LORA_WORKGROUPS / (wgs > 0 ? wgs : 1);
   if (s > (K + 1023) / 1024) s = (K + 1023) / 1024;
   if (s > LORA_MAX_SPLITS) s = LORA_MAX_SPLITS;
