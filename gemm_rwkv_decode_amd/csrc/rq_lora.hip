@@ -20,7 +20,9 @@
 // t and cannot overflow for a large x.
 //
 // y goes past the caches both ways (2047 rows of 16384 outputs, rank 64: 83 ->
-// 76 us).
+// 75 us, 291 MB at 3.9 TB/s).  32 requests of 24 adapters of rank 64 on three
+// 4096x4096 projections: 25 us, 56 MB, 11 and 13 us of it in the two launches,
+// a third of each the chain ids, offsets, first loads.
 #include <algorithm>
 
 #include "rq_common.h"
