@@ -44,6 +44,7 @@ RQ_OUT_F32, RQ_OUT_CODES_I8 = 0, 1
 RQ_MAX_M = 64
 RQ_MAX_BATCH = 64
 RQ_MAX_SEQUENCES = 65536
+RQ_MAX_TOKENS = 1 << 24
 RQ_SHIFT_MAX_MIXES = 8
 RQ_WKV_HEAD = 64
 RQ_TYPE_F32, RQ_TYPE_F16 = 0, 1

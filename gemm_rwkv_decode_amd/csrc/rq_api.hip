@@ -307,11 +307,15 @@ rq_status check_apart(const Operand& w, const Operand* in, int n) {
   return RQ_OK;
 }
 
+// Sizes up to which the kernels' 32-bit indexes and grids do not overflow.
+constexpr int MAX_SIZE = 1 << 24, MAX_LENGTH = 1 << 30;
+
 // Sizes of a batch of sequences over stored states.
 rq_status check_batch(const void* state, const int* offsets, const int* slots, int T,
                       int sequences, int nslots) {
   if (!offsets) return RQ_ERR_NULL;
-  if (T < 1 || sequences < 1 || sequences > RQ_MAX_SEQUENCES || nslots < 0) return RQ_ERR_SHAPE;
+  if (T < 1 || T > RQ_MAX_TOKENS || sequences < 1 || sequences > RQ_MAX_SEQUENCES || nslots < 0)
+    return RQ_ERR_SHAPE;
   if (!slots && nslots < sequences) return RQ_ERR_SHAPE;
   if (nslots > 0 && !state) return RQ_ERR_NULL;
   return RQ_OK;
@@ -539,7 +543,7 @@ rq_status rq_shift(const void* x, const void* mu, void* state, void* out, const 
   if (!x || !mu || !out) return RQ_ERR_NULL;
   rq_status st = check_batch(state, offsets, slots, T, sequences, nslots);
   if (st != RQ_OK) return st;
-  if (D < 8 || D % 8 != 0 || n < 1 || n > RQ_SHIFT_MAX_MIXES) return RQ_ERR_SHAPE;
+  if (D < 8 || D > MAX_SIZE || D % 8 != 0 || n < 1 || n > RQ_SHIFT_MAX_MIXES) return RQ_ERR_SHAPE;
   const size_t row = (size_t)D * 2;
   const Operand o[] = {array(out, row * T * n), array(state, row * nslots), array(x, row * T),
                        array(mu, row * n), index_array(offsets, (size_t)sequences + 1),
@@ -564,7 +568,7 @@ rq_status rq_wkv7(const void* r, const void* w, const void* k, const void* v, co
   rq_status st = check_batch(state, offsets, slots, T, sequences, nslots);
   if (st != RQ_OK) return st;
   if (input_type != RQ_TYPE_F32 && input_type != RQ_TYPE_F16) return RQ_ERR_UNSUPPORTED;
-  if (H < 1 || H > 4096) return RQ_ERR_SHAPE;
+  if (H < 1 || H > 4096 || (long long)sequences * H > 1 << 22) return RQ_ERR_SHAPE;
   const size_t n = (size_t)T * H * RQ_WKV_HEAD, e = input_type == RQ_TYPE_F16 ? 2 : 4;
   const Operand o[] = {array(y, n * 4),
                        array(state, (size_t)nslots * H * RQ_WKV_HEAD * RQ_WKV_HEAD * 4),
@@ -593,8 +597,9 @@ static rq_status lora_plan(const rq_lora_problem* problems, int count, int M, in
   if (max_rank < 8 || max_rank > RQ_LORA_MAX_RANK || max_rank % 8 != 0) return RQ_ERR_SHAPE;
   int k_max = 0;
   for (int i = 0; i < count; i++) {
-    if (problems[i].N < 1 || problems[i].K < 8 || problems[i].K % 8 != 0) return RQ_ERR_SHAPE;
-    if (problems[i].K > k_max) k_max = problems[i].K;
+    const int N = problems[i].N, K = problems[i].K;
+    if (N < 1 || N > MAX_SIZE || K < 8 || K > MAX_SIZE || K % 8 != 0) return RQ_ERR_SHAPE;
+    if (K > k_max) k_max = K;
   }
   *splits = rq::lora_splits(count, M, k_max, adapters, max_rank);
   *bytes = (size_t)count * *splits * M * ((max_rank + 15) / 16 * 16) * sizeof(float);
@@ -666,12 +671,12 @@ rq_status rq_logits(const rq_logits_args* args, void* workspace, size_t workspac
                     void* stream) {
   if (!args || !args->logits || !args->out) return RQ_ERR_NULL;
   const rq_logits_args& g = *args;
-  if (g.M < 1 || g.M > RQ_LOGITS_MAX_M || g.V < 1) return RQ_ERR_SHAPE;
+  if (g.M < 1 || g.M > RQ_LOGITS_MAX_M || g.V < 1 || g.V > MAX_LENGTH) return RQ_ERR_SHAPE;
   if (g.history && !g.history_offsets) return RQ_ERR_NULL;
   if (g.bias_ids && (!g.bias || !g.bias_offsets)) return RQ_ERR_NULL;
   if (g.masks && !g.mask_ids) return RQ_ERR_NULL;
-  if ((g.history && g.history_len < 0) || (g.bias_ids && g.bias_len < 0) ||
-      (g.masks && g.nmasks < 1))
+  if ((g.history && (g.history_len < 0 || g.history_len > MAX_LENGTH)) ||
+      (g.bias_ids && (g.bias_len < 0 || g.bias_len > MAX_LENGTH)) || (g.masks && g.nmasks < 1))
     return RQ_ERR_SHAPE;
   const size_t zb = (size_t)g.M * g.V * 4, m = g.M;
   const size_t hl = g.history ? g.history_len : 0, bl = g.bias_ids ? g.bias_len : 0;

@@ -227,6 +227,8 @@ def generate(model, prompts, steps, adapters=None, ids=None, repetition=1.1, pre
     first single-token one are replays of a captured graph; the results are
     the same."""
     dev, n = model.device, len(prompts)
+    if not n or not all(prompts):
+        raise ValueError("a prompt has at least one token")
 
     def ints(v):
         return torch.tensor(v, dtype=torch.int32, device=dev)

@@ -282,6 +282,9 @@ rq_status rq_gemm_smallm_noalloc(const void* qweight, const void* scales, const 
 /* Largest number of sequences in a call of rq_shift or rq_wkv7. */
 #define RQ_MAX_SEQUENCES 65536
 
+/* Largest T of rq_shift and rq_wkv7. */
+#define RQ_MAX_TOKENS (1 << 24)
+
 /* Largest n of rq_shift. */
 #define RQ_SHIFT_MAX_MIXES 8
 
@@ -294,8 +297,8 @@ rq_status rq_gemm_smallm_noalloc(const void* qweight, const void* scales, const 
  *   x: binary16 [T][D].  mu: binary16 [n][D].  state: binary16 [nslots][D].
  *   out: binary16 [n][T][D], computed in binary32 and rounded once.
  * Rows of x that no sequence covers leave unspecified rows in out.
- * Shape rules: T >= 1, D >= 8, D % 8 == 0, 1 <= n <= RQ_SHIFT_MAX_MIXES,
- * 1 <= sequences <= RQ_MAX_SEQUENCES, nslots >= 0 (at least `sequences` when slots is NULL; state
+ * Shape rules: 1 <= T <= RQ_MAX_TOKENS, 8 <= D <= 1 << 24, D % 8 == 0, 1 <= n <=
+ * RQ_SHIFT_MAX_MIXES, 1 <= sequences <= RQ_MAX_SEQUENCES, nslots >= 0 (at least `sequences` when slots is NULL; state
  * may be NULL when nslots is 0, which needs slots).
  */
 rq_status rq_shift(const void* x, const void* mu, void* state, void* out, const int* offsets,
@@ -322,8 +325,8 @@ typedef enum { RQ_TYPE_F32 = 0, RQ_TYPE_F16 = 1 } rq_type;
  *   covers are not written.
  * All sums and the state are binary32.  Non-finite inputs reach the outputs of
  * their own token and later ones only.
- * Shape rules: T >= 1, 1 <= H <= 4096, sequences and nslots as for
- * rq_shift.
+ * Shape rules: T, sequences and nslots as for rq_shift, 1 <= H <= 4096,
+ * sequences * H <= 1 << 22.
  */
 rq_status rq_wkv7(const void* r, const void* w, const void* k, const void* v, const void* kappa,
                   const void* eta, int input_type, float* state, float* y, const int* offsets,
@@ -362,10 +365,11 @@ typedef struct {
  *   no clearing and holds nothing between calls.
  * Results do not depend on which other rows share the call's blocks of rows,
  * beyond the split of K, which follows the call's sizes.
- * Shape rules: 1 <= count <= RQ_LORA_MAX_BATCH, 1 <= M <= RQ_LORA_MAX_M, N >=
- * 1, K >= 8, K % 8 == 0, adapters >= 1, total_rank >= 0, 8 <= max_rank <=
- * RQ_LORA_MAX_RANK, max_rank % 8 == 0.  RQ_ERR_SCRATCH: the workspace is NULL
- * or too small.  `problems` is a host array the call reads before it returns.
+ * Shape rules: 1 <= count <= RQ_LORA_MAX_BATCH, 1 <= M <= RQ_LORA_MAX_M, 1 <=
+ * N <= 1 << 24, 8 <= K <= 1 << 24, K % 8 == 0, adapters >= 1, total_rank >= 0, 8
+ * <= max_rank <= RQ_LORA_MAX_RANK, max_rank % 8 == 0.  RQ_ERR_SCRATCH: the
+ * workspace is NULL or too small.  `problems` is a host array the call reads
+ * before it returns.
  */
 rq_status rq_lora(const rq_lora_problem* problems, int count, int M, const int* ids,
                   const int* offsets, const float* scales, int adapters, int total_rank,
@@ -425,8 +429,8 @@ typedef struct {
  *   use; every call leaves it zero (the first 64 KiB of a workspace of
  *   rq_gemm_smallm_ws will do).  Calls that share it must not overlap in time.
  *   RQ_ERR_SCRATCH: NULL or too small.
- * Shape rules: 1 <= M <= RQ_LOGITS_MAX_M, V >= 1, lengths >= 0, nmasks >= 1
- * with masks.
+ * Shape rules: 1 <= M <= RQ_LOGITS_MAX_M, 1 <= V <= 1 << 30, history_len and
+ * bias_len from 0 to 1 << 30, nmasks >= 1 with masks.
  */
 rq_status rq_logits(const rq_logits_args* args, void* workspace, size_t workspace_bytes,
                     void* stream);

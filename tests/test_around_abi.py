@@ -271,3 +271,34 @@ def test_the_binding_refuses_types_shapes_and_host_tensors():
             pytest.fail(f"call {k} was accepted")
     with pytest.raises(TypeError):
         rq.prepare("rq_gemv", 1, bias=None)
+
+
+# ------------------------------------------------- sizes the kernels' indexes allow
+def test_sizes_past_the_limits_are_refused(L):
+    src = open(os.path.join(ROOT, "include", "rq.h")).read()
+    assert re.search(r"#define RQ_MAX_TOKENS \(1 << 24\)", src) and rq.RQ_MAX_TOKENS == 1 << 24
+    big = 1 << 24
+    far = dict(out=A + 400 * G, state=None, nslots=0)
+    assert shift(L, T=big + 1, D=8, **far) == rq.RQ_ERR_SHAPE
+    assert shift(L, D=big + 8, T=1, **far) == rq.RQ_ERR_SHAPE
+    assert wkv(L, T=big + 1, y=A + 9000 * G, state=None, nslots=0) == rq.RQ_ERR_SHAPE
+    assert wkv(L, seqs=1025, H=4096, state=None, nslots=0) == rq.RQ_ERR_SHAPE
+    assert lora(L, (dict(N=big + 1),)) == rq.RQ_ERR_SHAPE
+    assert lora(L, (dict(K=big + 8),)) == rq.RQ_ERR_SHAPE
+    assert logits(L, V=G + 1) == rq.RQ_ERR_SHAPE
+    assert logits(L, history_len=G + 1) == rq.RQ_ERR_SHAPE
+    assert logits(L, bias_len=G + 1) == rq.RQ_ERR_SHAPE
+
+
+@no_gpu
+def test_sizes_at_the_limits_are_accepted(L):
+    big = 1 << 24
+    apart = {n: A + (i + 1) * 4096 * G for i, n in enumerate(("x", "mu", "out"))}
+    assert passes(shift(L, T=big, D=8, state=None, nslots=0, **apart))
+    assert passes(shift(L, T=1, D=big, state=None, nslots=0, **apart))
+    apart = {n: A + i * 65536 * G for i, n in enumerate(WKV) if n not in
+             ("type", "T", "H", "seqs", "nslots", "state")}
+    assert passes(wkv(L, T=big, H=1, state=None, nslots=0, **apart))
+    assert passes(wkv(L, T=1, H=4096, seqs=1024, state=None, nslots=0, **apart))
+    spread = dict(logits=A + 500 * G, out=A + 100 * G, history=A + 200 * G, masks=A + 300 * G)
+    assert passes(logits(L, M=1, V=G, history_len=G, bias_ids=None, bias=None, **spread))

@@ -168,6 +168,13 @@ def test_models_of_other_layouts_are_refused():
         V.Model(1, 256, 64, S.ASYM4_G32, device="cpu")
 
 
+def test_empty_prompts_are_refused():
+    model = V.Model(1, 64, 64, device="cpu")
+    for prompts in ([], [[1, 2], []]):
+        with pytest.raises(ValueError):
+            V.generate(model, prompts, 2)
+
+
 def test_histories_on_the_host():
     h = V.Histories([[5, 6, 7], [8]], 5, "cpu")
     h.append(torch.tensor([1, 2], dtype=torch.int32))
