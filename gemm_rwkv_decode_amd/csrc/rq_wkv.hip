@@ -272,42 +272,62 @@ __device__ __forceinline__ void pin(V& v) {
   asm volatile("" : "+v"(v));
 }
 
-// Inputs of one chunk as a producer lane holds them: token lane mod 16, keys
-// 16 jt + 4 (lane / 16) .. + 3.  They stay as they were loaded until they are
-// used: a conversion here would wait for them.  Tokens past the sequence's end
-// are read from a row of zeros: nothing is added.
-__device__ const float zero_row[HD] = {0};
+// A head's rows of a chunk from token t0 on, as a buffer that ends with the
+// sequence: reads past the end give zeros (nothing is added), writes there are
+// dropped, and the addresses are made on the scalar unit.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const void* x, size_t base, size_t ld,
+                                                             int t0, int hi) {
+  const int n = min(hi - t0, CH);
+  const T* p = static_cast<const T*>(x) + ((size_t)t0 * ld + base);
+  const size_t bytes = n > 0 ? ((n - 1) * ld + HD) * sizeof(T) : 0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, (u32)bytes, 0x00020000);
+}
 template <typename T>
 struct Vec4;
 template <>
 struct Vec4<float> {
   typedef f4 type;
+  static __device__ __forceinline__ f4 load(__amdgpu_buffer_rsrc_t r, u32 at) {
+    return __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+  }
+  static __device__ __forceinline__ float load1(__amdgpu_buffer_rsrc_t r, u32 at) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+  }
 };
 template <>
 struct Vec4<_Float16> {
   typedef h4 type;
+  static __device__ __forceinline__ h4 load(__amdgpu_buffer_rsrc_t r, u32 at) {
+    return __builtin_bit_cast(h4, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+  }
+  static __device__ __forceinline__ _Float16 load1(__amdgpu_buffer_rsrc_t r, u32 at) {
+    return __builtin_bit_cast(_Float16, __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0));
+  }
 };
+
+// Inputs of one chunk as a producer lane holds them: token lane mod 16, keys
+// 16 jt + 4 (lane / 16) .. + 3.  They stay as they were loaded until they are
+// used: a conversion here would wait for them.
 template <typename T>
 struct ChunkIn {
   typedef typename Vec4<T>::type vec;
   vec w[4], k[4], kap[4], eta[4], r[4];
-  __device__ __forceinline__ void load(const WkvArgs& a, size_t at, size_t key, bool live) {
-    // (global addresses said to be such: the choice between two arrays would
-    // else make flat loads, which the barriers' LDS waits would wait for)
-    typedef const __attribute__((address_space(1))) T* ptr;
-    typedef const __attribute__((address_space(1))) vec* vptr;
-    const ptr z = (ptr)reinterpret_cast<const T*>(zero_row) + key;
-    const auto row = [&](const void* x) { return (ptr) static_cast<const T*>(x) + at; };
-    const ptr pw = row(a.w);
-    const ptr pk = live ? row(a.k) : z, pkap = live ? row(a.kappa) : z;
-    const ptr peta = live ? row(a.eta) : z, pr = live ? row(a.r) : z;
+  __device__ __forceinline__ void load(const WkvArgs& a, size_t base, size_t ld, int t0, int hi,
+                                       u32 at) {
+    const __amdgpu_buffer_rsrc_t rw = chunk_rows<T>(a.w, base, ld, t0, hi);
+    const __amdgpu_buffer_rsrc_t rk = chunk_rows<T>(a.k, base, ld, t0, hi);
+    const __amdgpu_buffer_rsrc_t rkap = chunk_rows<T>(a.kappa, base, ld, t0, hi);
+    const __amdgpu_buffer_rsrc_t reta = chunk_rows<T>(a.eta, base, ld, t0, hi);
+    const __amdgpu_buffer_rsrc_t rr = chunk_rows<T>(a.r, base, ld, t0, hi);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      w[j] = *(vptr)(pw + 16 * j);
-      k[j] = *(vptr)(pk + 16 * j);
-      kap[j] = *(vptr)(pkap + 16 * j);
-      eta[j] = *(vptr)(peta + 16 * j);
-      r[j] = *(vptr)(pr + 16 * j);
+      const u32 to = at + 16 * j * (u32)sizeof(T);
+      w[j] = Vec4<T>::load(rw, to);
+      k[j] = Vec4<T>::load(rk, to);
+      kap[j] = Vec4<T>::load(rkap, to);
+      eta[j] = Vec4<T>::load(reta, to);
+      r[j] = Vec4<T>::load(rr, to);
     }
   }
   // P of key tile j: the decays' products up to the lane's token (a token past
@@ -322,20 +342,24 @@ struct ChunkIn {
 };
 
 // V of a chunk as a right operand: tokens 4 g + v of the lane's value row, as
-// loaded; tokens past the end repeat the last one until they are used.
+// loaded.
 template <typename T>
 struct ChunkV {
   T v[4];
-  __device__ __forceinline__ void load(const T* col, size_t ld, int t0, int hi) {
-    const int g = (threadIdx.x & 63) >> 4;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rows, const u32* at) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) v[i] = col[(size_t)min(t0 + 4 * g + i, hi - 1) * ld];
+    for (int i = 0; i < 4; i++) v[i] = Vec4<T>::load1(rows, at[i]);
   }
-  __device__ __forceinline__ f4 get(int t0, int hi) const {
-    const int g = (threadIdx.x & 63) >> 4;
+  // into registers of its own (a copy the compiler does not see through): the
+  // next load takes these, or it would move them at the loop's end, and wait
+  __device__ __forceinline__ f4 get() const {
     f4 r;
 #pragma unroll
-    for (int i = 0; i < 4; i++) r[i] = t0 + 4 * g + i < hi ? (float)v[i] : 0.0f;
+    for (int i = 0; i < 4; i++) {
+      float x = (float)v[i];
+      if constexpr (sizeof(T) == 4) asm volatile("v_mov_b32 %0, %1" : "=v"(x) : "v"(v[i]));
+      r[i] = x;
+    }
     return r;
   }
 };
@@ -408,9 +432,8 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
   const int n = (hi - lo + CH - 1) / CH;
   ChunkIn<T> in;
   const auto live = [&](int c) { return lo + c * CH + l16 < hi; };
-  const auto fetch = [&](int c) {
-    in.load(a, (size_t)min(lo + c * CH + l16, hi - 1) * ld + base + 4 * g, 4 * g, live(c));
-  };
+  const u32 at = (u32)((l16 * ld + 4 * g) * sizeof(T));
+  const auto fetch = [&](int c) { in.load(a, base, ld, lo + c * CH, hi, at); };
   h4 identity;
 #pragma unroll
   for (int v = 0; v < 4; v++) identity[v] = l16 == 4 * g + v ? (_Float16)1.0f : (_Float16)0.0f;
@@ -454,9 +477,8 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       pin(av[j]), pin(qv[j]), pin(bv[j]), pin(kv[j]), pin(rest[j]);
     }
     // two steps ahead of their use, into the registers that are free by now
-    // (the operands are made before, not after; past the end rows of the
-    // sequence are read again, as a branch here would make the compiler wait for
-    // the loads to move them)
+    // (the operands are made before, not after; past the end too, as a branch here
+    // would make the compiler wait for the loads to move them)
     __builtin_amdgcn_sched_barrier(0);
     fetch(c + PRODUCERS);
     step_barrier();
@@ -567,6 +589,9 @@ k_wkv_chunk(const WkvArgs a) {
   const size_t ld = (size_t)a.H * HD, base = (size_t)h * HD;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (wave >= NR) {
+    // where a producer shares a SIMD with a state wave, it is the later one (1531
+    // ragged tokens, 40 heads: 64 -> 60 us)
+    __builtin_amdgcn_s_setprio(1);
     produce<T>(a, ops, decays, wave - NR, lo, hi, base, ld);
     return;
   }
@@ -583,10 +608,16 @@ k_wkv_chunk(const WkvArgs a) {
   }
   const T* vp = static_cast<const T*>(a.v) + base + i;
   float* yp = a.y + base + i;
+  u32 vat[4], yat[4];  // of tokens 4 g + v in a chunk's rows
+#pragma unroll
+  for (int v = 0; v < 4; v++) {
+    vat[v] = (u32)(((4 * g + v) * ld + i) * sizeof(T));
+    yat[v] = (u32)(((4 * g + v) * ld + i) * sizeof(float));
+  }
   // V of the even and the odd chunks, two chunks ahead
   ChunkV<T> even, odd;
-  even.load(vp, ld, lo, hi);
-  odd.load(vp, ld, min(lo + CH, hi - 1), hi);
+  even.load(chunk_rows<T>(a.v, base, ld, lo, hi), vat);
+  odd.load(chunk_rows<T>(a.v, base, ld, lo + CH, hi), vat);
   for (int s = 0; s < 3; s++) step_barrier();
   // the state has arrived before the loop, so that no wait inside it stands
   // for these loads (and with them for the stores of y)
@@ -615,8 +646,8 @@ k_wkv_chunk(const WkvArgs a) {
       kb[j] = P8{o.kb[0][j][lane], o.kb[1][j][lane]};
     }
     const P4 nb{o.nb[0][lane], o.nb[1][lane]};
-    const f4 V = vin.get(t0, hi);
-    vin.load(vp, ld, t0 + 2 * CH, hi);
+    const f4 V = vin.get();
+    vin.load(chunk_rows<T>(a.v, base, ld, t0 + 2 * CH, hi), vat);
     f4 Sq[4];
     float big = larger(0.0f, V);
 #pragma unroll
@@ -653,14 +684,11 @@ k_wkv_chunk(const WkvArgs a) {
       }
       mma(join(nk, nb), vu, y);
       const f4 yv = y.value();
-      float* yt = yp + (size_t)(t0 + 4 * g) * ld;
-      if (t0 + CH <= hi) {
+      const __amdgpu_buffer_rsrc_t ry = chunk_rows<float>(a.y, base, ld, t0, hi);
 #pragma unroll
-        for (int v = 0; v < 4; v++) yt[v * ld] = yv[v];
-      } else {
-#pragma unroll
-        for (int v = 0; v < 4; v++)
-          if (t0 + 4 * g + v < hi) yt[v * ld] = yv[v];
+      for (int v = 0; v < 4; v++) {
+        const float yt = yv[v];
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(u32, yt), ry, yat[v], 0, 0);
       }
     } else {
       // token by token (a value that is not finite must not reach earlier
