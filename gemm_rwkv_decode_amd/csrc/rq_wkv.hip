@@ -139,16 +139,17 @@ k_wkv_seq(const WkvArgs a) {
 // A workgroup has NR state waves, 16 value rows each, and three producer waves
 // that prepare what depends on the inputs alone (decays, the four 16x16
 // matrices, the triangular inverse), one chunk each, in three segments one
-// barrier apart; chunk c's operands go through LDS, two buffers in turn.
+// barrier apart; chunk c's operands go through LDS, two buffers in turn.  Six
+// producers cut the segments in two.
 //
-// Bound by the chain of chunks: a step is as long as a producer's longest
-// segment (2250 cycles) or the state's chain of five dependent products (2100),
-// of which two thirds are instructions issued and the rest their latencies.
-// One prompt of 4096 tokens, 64 heads: 253 us, 2370 cycles a chunk, 472 MB at
-// 1.9 TB/s.
+// Bound by the chain of chunks where heads are few: a step is as long as a
+// producer's longest segment (2250 cycles) or the state's chain of five dependent
+// products (2100), of which two thirds are instructions issued and the rest
+// their latencies.  One prompt of 4096 tokens, 64 heads: 243 us, 2280 cycles a
+// chunk, 472 MB at 1.9 TB/s.  Bound by the SIMDs' instruction rate where heads
+// are many (4096 tokens in 16 sequences, 64 heads: 131 us).
 // ---------------------------------------------------------------------------
 constexpr int CH = 16;  // tokens of a chunk
-constexpr int PRODUCERS = 3;
 constexpr float UP = 2048.0f, DOWN = 1.0f / 2048.0f;  // the low part's scale
 constexpr float TINY = 1.0f / 4096.0f, HUGE_ = 32768.0f;
 
@@ -425,7 +426,7 @@ __device__ __forceinline__ bool too_small(float m) {
   return __ballot(m >= TINY) == 0 && __ballot(m > 0.0f) != 0;
 }
 
-template <typename T>
+template <typename T, int PRODUCERS>
 __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDecays* decays,
                                         int p, int lo, int hi, size_t base, size_t ld) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
@@ -437,6 +438,9 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
   h4 identity;
 #pragma unroll
   for (int v = 0; v < 4; v++) identity[v] = l16 == 4 * g + v ? (_Float16)1.0f : (_Float16)0.0f;
+  const auto half_barrier = [] {
+    if constexpr (PRODUCERS == 6) step_barrier();
+  };
   f4 P[4];
   fetch(p);
   P[0] = in.decays(0, live(p));
@@ -469,12 +473,13 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       }
       // Q is token 7's P, P_16 token 15's
       if ((l16 & 7) == 7)
-        *reinterpret_cast<f4*>(&decays[c & 3].at[l16 >> 3][16 * j + 4 * g]) = P[j];
+        *reinterpret_cast<f4*>(&decays[c & 7].at[l16 >> 3][16 * j + 4 * g]) = P[j];
     };
 #pragma unroll
     for (int j = 0; j < 4; j++) {
       scale(j);
       pin(av[j]), pin(qv[j]), pin(bv[j]), pin(kv[j]), pin(rest[j]);
+      if (j == 1) half_barrier();
     }
     // two steps ahead of their use, into the registers that are free by now
     // (the operands are made before, not after; past the end too, as a branch here
@@ -499,6 +504,9 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       mma(bp, qp[q], nb);
       mma(kp, qp[q], nk);
     }
+    f4 mbv = mb.value(), mkv = mk.value(), nbv = nb.value(), nkv = nk.value();
+    pin(mbv), pin(mkv), pin(nbv), pin(nkv);
+    half_barrier();
 #pragma unroll
     for (int j = 0; j < 4; j++) {
       const P4 kp = split(rounded(kv[j] * rest[j])), bp = split(rounded(bv[j] * rest[j]));
@@ -515,25 +523,26 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
         kb[j].lo[4 + v] = (_Float16)bl[v];
       }
     }
-    f4 mbv = mb.value(), mkv = mk.value(), nbv = nb.value(), nkv = nk.value();
-    pin(mbv), pin(mkv), pin(nbv), pin(nkv);
 #pragma unroll
     for (int j = 0; j < 4; j++) pin(kb[j].hi), pin(kb[j].lo);
     step_barrier();
     // segment 3: the triangular inverse, and everything to the chunk's buffer
     ChunkOps& o = ops[c & 1];
+    const auto put = [&] {
 #pragma unroll
-    for (int q = 0; q < 2; q++) {
-      o.a[0][q][lane] = ap[q].hi;
-      o.a[1][q][lane] = ap[q].lo;
-      o.q[0][q][lane] = qp[q].hi;
-      o.q[1][q][lane] = qp[q].lo;
-    }
+      for (int q = 0; q < 2; q++) {
+        o.a[0][q][lane] = ap[q].hi;
+        o.a[1][q][lane] = ap[q].lo;
+        o.q[0][q][lane] = qp[q].hi;
+        o.q[1][q][lane] = qp[q].lo;
+      }
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      o.kb[0][j][lane] = kb[j].hi;
-      o.kb[1][j][lane] = kb[j].lo;
-    }
+      for (int j = 0; j < 4; j++) {
+        o.kb[0][j][lane] = kb[j].hi;
+        o.kb[1][j][lane] = kb[j].lo;
+      }
+    };
+    if constexpr (PRODUCERS == 3) put();
     // a value that is not finite, or too large for an operand, leaves none of
     // its row's or column's sums finite
     float zero = 0.0f;
@@ -548,7 +557,12 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       nbt[v] = upto ? nbv[v] : 0.0f;
       nkt[v] = upto ? nkv[v] : 0.0f;
     }
-    const f4 x = inverse(mbt);
+    f4 x = inverse(mbt);
+    if constexpr (PRODUCERS == 6) {
+      pin(x), pin(mkt), pin(nbt), pin(nkt);
+      step_barrier();
+      put();
+    }
     const float big = larger(larger(larger(larger(0.0f, x), mkt), nbt), nkt);
     slow = slow || __ballot(!(zero == 0.0f) || !(big < HUGE_)) != 0;
     const P4 xp = split(x), mkp = split(mkt), nbp = split(nbt), nkp = split(nkt);
@@ -567,16 +581,16 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       pin(P[j]);
     }
     step_barrier();
-    steps += 3;
+    steps += PRODUCERS;
   }
-  for (; steps < n + 3; steps++) step_barrier();
+  for (; steps < n + PRODUCERS; steps++) step_barrier();
 }
 
-template <typename T, int NR>
+template <typename T, int NR, int PRODUCERS>
 __global__ void __launch_bounds__(64 * (NR + PRODUCERS), 2)
 k_wkv_chunk(const WkvArgs a) {
   __shared__ ChunkOps ops[2];
-  __shared__ ChunkDecays decays[4];
+  __shared__ ChunkDecays decays[8];
   // heads are the fast index: a sequence's workgroups go to all XCDs, a head's
   // (they read the same inputs) to one
   constexpr int TILES = 4 / NR;
@@ -587,14 +601,19 @@ k_wkv_chunk(const WkvArgs a) {
   if (lo >= hi) return;
   const int n = (hi - lo + CH - 1) / CH;
   const size_t ld = (size_t)a.H * HD, base = (size_t)h * HD;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (wave >= NR) {
+  // Waves go to the four SIMDs in turn.  Six producers take three of them, two
+  // waves each, the state waves the fourth.
+  const int nth = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool producer = PRODUCERS == 6 ? nth % 4 != 3 : nth >= NR;
+  if (producer) {
     // where a producer shares a SIMD with a state wave, it is the later one (1531
     // ragged tokens, 40 heads: 64 -> 60 us)
-    __builtin_amdgcn_s_setprio(1);
-    produce<T>(a, ops, decays, wave - NR, lo, hi, base, ld);
+    if (PRODUCERS == 3) __builtin_amdgcn_s_setprio(1);
+    produce<T, PRODUCERS>(a, ops, decays, PRODUCERS == 6 ? nth - nth / 4 : nth - NR, lo, hi, base,
+                          ld);
     return;
   }
+  const int wave = PRODUCERS == 6 ? nth / 4 : nth;
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int i = 16 * (tile * NR + wave % NR) + l16;  // the lane's value row
   const int slot = a.slots ? a.slots[sq] : sq;
@@ -618,7 +637,7 @@ k_wkv_chunk(const WkvArgs a) {
   ChunkV<T> even, odd;
   even.load(chunk_rows<T>(a.v, base, ld, lo, hi), vat);
   odd.load(chunk_rows<T>(a.v, base, ld, lo + CH, hi), vat);
-  for (int s = 0; s < 3; s++) step_barrier();
+  for (int s = 0; s < PRODUCERS; s++) step_barrier();
   // the state has arrived before the loop, so that no wait inside it stands
   // for these loads (and with them for the stores of y)
 #pragma unroll
@@ -631,7 +650,7 @@ k_wkv_chunk(const WkvArgs a) {
     f4 mid[4], end[4];
 #pragma unroll
     for (int j = 0; j < 4; j++)
-      mid[j] = *reinterpret_cast<const f4*>(&decays[c & 3].at[0][16 * j + 4 * g]);
+      mid[j] = *reinterpret_cast<const f4*>(&decays[c & 7].at[0][16 * j + 4 * g]);
     const P4 mk{o.mk[0][lane], o.mk[1][lane]}, nk{o.nk[0][lane], o.nk[1][lane]};
     P8 ap[2], qp[2], kb[4];
 #pragma unroll
@@ -642,7 +661,7 @@ k_wkv_chunk(const WkvArgs a) {
     const P4 xp{o.x[0][lane], o.x[1][lane]};
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      end[j] = *reinterpret_cast<const f4*>(&decays[c & 3].at[1][16 * j + 4 * g]);
+      end[j] = *reinterpret_cast<const f4*>(&decays[c & 7].at[1][16 * j + 4 * g]);
       kb[j] = P8{o.kb[0][j][lane], o.kb[1][j][lane]};
     }
     const P4 nb{o.nb[0][lane], o.nb[1][lane]};
@@ -739,9 +758,9 @@ k_wkv_chunk(const WkvArgs a) {
   }
 }
 
-template <typename T, int NR>
+template <typename T, int NR, int PRODUCERS>
 void launch_chunks(const WkvArgs& a, unsigned heads, hipStream_t s) {
-  hipLaunchKernelGGL((k_wkv_chunk<T, NR>), dim3((heads + 7) / 8 * 8 * (4 / NR)),
+  hipLaunchKernelGGL((k_wkv_chunk<T, NR, PRODUCERS>), dim3((heads + 7) / 8 * 8 * (4 / NR)),
                      dim3(64 * (NR + PRODUCERS)), 0, s, a);
 }
 
@@ -755,18 +774,22 @@ void launch_chunks(const WkvArgs& a, unsigned heads, hipStream_t s) {
 // workgroups.  Binary32, 16 / 32 / 64 rows: one prompt of 4096 tokens, 64 heads
 // 271 / 354 / 380 us; of 1000 tokens, 72 heads 107 / 92 / 97, 128 heads 109 /
 // 94 / 97, 160 heads 166 / 179 / 98; 4096 tokens in 16 sequences, 64 heads 250 /
-// 215 / 145 us.
+// 215 / 145 us (before a last step that took 5% off all three).
+//
+// Producers of binary16 inputs have more to do (conversions); at 16 rows, with
+// a SIMD's second wave free, six of them keep up with the state (4096 tokens, 64
+// heads 284 -> 252 us), which three do in binary32 (242 and 248 us).
 template <typename T>
 void launch(const WkvArgs& a, hipStream_t s) {
   const unsigned heads = (unsigned)a.sequences * a.H;
   if (a.T - a.sequences < 32)
     hipLaunchKernelGGL((k_wkv_seq<T>), dim3(heads), dim3(256), 0, s, a);
   else if (heads <= 64)
-    launch_chunks<T, 1>(a, heads, s);
+    launch_chunks<T, 1, sizeof(T) == 2 ? 6 : 3>(a, heads, s);
   else if (heads <= 128)
-    launch_chunks<T, 2>(a, heads, s);
+    launch_chunks<T, 2, 3>(a, heads, s);
   else
-    launch_chunks<T, 4>(a, heads, s);
+    launch_chunks<T, 4, 3>(a, heads, s);
 }
 
 }  // namespace
