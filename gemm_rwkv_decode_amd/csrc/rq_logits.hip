@@ -278,7 +278,7 @@ hipError_t launch_slices(const LogitsArgs& a, u64* records, int stride, int work
   const int sl = (own + slices - 1) / slices * STEP;
   const size_t lds = token * sl;
   static bool raised = false;  // allow the full LDS once per instantiation
-  if (!raised) {
+  if (lds > (64 << 10) && !raised) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_logits<NT>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize,
                                              LOGITS_LDS);

@@ -772,9 +772,9 @@ void launch_chunks(const WkvArgs& a, unsigned heads, hipStream_t s) {
 // itself), but the producers' work is done again by each of a head's
 // workgroups, which pays while there is a compute unit for each of these 4 or 2
 // workgroups.  Binary32, 16 / 32 / 64 rows: one prompt of 4096 tokens, 64 heads
-// 271 / 354 / 380 us; of 1000 tokens, 72 heads 107 / 92 / 97, 128 heads 109 /
-// 94 / 97, 160 heads 166 / 179 / 98; 4096 tokens in 16 sequences, 64 heads 250 /
-// 215 / 145 us (before a last step that took 5% off all three).
+// 264 / 324 / 350 us; of 1000 tokens, 72 heads 104 / 83 / 90, 128 heads 112 / 88 /
+// 91, 160 heads 164 / 163 / 95; 4096 tokens in 16 sequences, 64 heads 253 / 200 /
+// 137 us.
 //
 // Producers of binary16 inputs have more to do (conversions); at 16 rows, with
 // a SIMD's second wave free, six of them keep up with the state (4096 tokens, 64
