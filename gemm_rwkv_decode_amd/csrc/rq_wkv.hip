@@ -40,10 +40,10 @@ __device__ __forceinline__ f4 load4(const T* p) {
 // where they are long (4096 tokens, 64 heads: 3025 us, 1770 cycles a token).
 template <typename T>
 __global__ void __launch_bounds__(256)
-k_wkv_seq(const WkvArgs a) {
+k_wkv_seq(const WkvArgs a, int below) {
   const int q = blockIdx.x / a.H, h = blockIdx.x % a.H;
   const int lo = max(a.offsets[q], 0), hi = min(a.offsets[q + 1], a.T);
-  if (lo >= hi) return;
+  if (lo >= hi || hi - lo >= below) return;
   const int slot = a.slots ? a.slots[q] : q;
   const bool stored = slot >= 0 && slot < a.nslots;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -588,7 +588,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
 
 template <typename T, int NR, int PRODUCERS>
 __global__ void __launch_bounds__(64 * (NR + PRODUCERS), 2)
-k_wkv_chunk(const WkvArgs a) {
+k_wkv_chunk(const WkvArgs a, int from) {
   __shared__ ChunkOps ops[2];
   __shared__ ChunkDecays decays[8];
   // heads are the fast index: a sequence's workgroups go to all XCDs, a head's
@@ -598,7 +598,7 @@ k_wkv_chunk(const WkvArgs a) {
   if (hd >= a.sequences * a.H) return;
   const int sq = hd / a.H, h = hd % a.H;
   const int lo = max(a.offsets[sq], 0), hi = min(a.offsets[sq + 1], a.T);
-  if (lo >= hi) return;
+  if (lo >= hi || hi - lo < from) return;
   const int n = (hi - lo + CH - 1) / CH;
   const size_t ld = (size_t)a.H * HD, base = (size_t)h * HD;
   // Waves go to the four SIMDs in turn.  Six producers take three of them, two
@@ -759,13 +759,21 @@ k_wkv_chunk(const WkvArgs a) {
 }
 
 template <typename T, int NR, int PRODUCERS>
-void launch_chunks(const WkvArgs& a, unsigned heads, hipStream_t s) {
+void launch_chunks(const WkvArgs& a, unsigned heads, int from, hipStream_t s) {
   hipLaunchKernelGGL((k_wkv_chunk<T, NR, PRODUCERS>), dim3((heads + 7) / 8 * 8 * (4 / NR)),
-                     dim3(64 * (NR + PRODUCERS)), 0, s, a);
+                     dim3(64 * (NR + PRODUCERS)), 0, s, a, from);
 }
 
-// Token by token where less than 32 tokens are not their sequence's first: the
-// chunks would be mostly empty (64 requests of one token, 32 heads: 22 us).
+// Sequences go token by token below a length, in chunks from it on.  Few heads:
+// 8 tokens (token by token / chunks: 64 heads, one sequence of 4 tokens 4.8 / 6.4
+// us, 8 6.5 / 6.4, 16 10.2 / 6.5); many: 16 (1024 heads, sequences of 8 tokens
+// 15 / 24 us, 16 28 / 25; 2048 heads 29 / 47 and 48 / 47 us).
+//
+// The lengths are on the device.  Where sequences have on average more than 12
+// tokens beyond their first, all go in chunks; below that each kind has a launch
+// of its own, which passes over the other's sequences (chunks only / both: 64
+// heads, 31 single tokens beside one sequence of 48 49 / 22 us, of 500 56 / 61; 16
+// sequences of 8 24 / 18, of 16 25 / 27).
 //
 // A workgroup of the chunk kernel takes 16, 32 or 64 of a head's value rows.
 // Fewer rows make a chunk's step shorter (a state wave then has a SIMD to
@@ -782,14 +790,21 @@ void launch_chunks(const WkvArgs& a, unsigned heads, hipStream_t s) {
 template <typename T>
 void launch(const WkvArgs& a, hipStream_t s) {
   const unsigned heads = (unsigned)a.sequences * a.H;
-  if (a.T - a.sequences < 32)
-    hipLaunchKernelGGL((k_wkv_seq<T>), dim3(heads), dim3(256), 0, s, a);
-  else if (heads <= 64)
-    launch_chunks<T, 1, sizeof(T) == 2 ? 6 : 3>(a, heads, s);
+  const int from = heads <= 128 ? 8 : 16;
+  const int extra = a.T - a.sequences;
+  const bool all_short = extra + 1 < from;
+  const bool all_long = !all_short && (a.sequences == 1 || extra / 12 >= a.sequences);
+  if (!all_long)
+    hipLaunchKernelGGL((k_wkv_seq<T>), dim3(heads), dim3(256), 0, s, a,
+                       all_short ? a.T + 1 : from);
+  if (all_short) return;
+  const int least = all_long ? 0 : from;
+  if (heads <= 64)
+    launch_chunks<T, 1, sizeof(T) == 2 ? 6 : 3>(a, heads, least, s);
   else if (heads <= 128)
-    launch_chunks<T, 2, 3>(a, heads, s);
+    launch_chunks<T, 2, 3>(a, heads, least, s);
   else
-    launch_chunks<T, 4, 3>(a, heads, s);
+    launch_chunks<T, 4, 3>(a, heads, least, s);
 }
 
 }  // namespace

@@ -246,3 +246,13 @@ def test_graph_replays_and_other_streams(lens, H):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want_y[i]) and torch.equal(state, want_s[i])
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("lens,H", [
+    ([1] * 31 + [48], 3), ([7, 8, 9, 1, 0, 15, 16, 17], 2), ([7, 8, 9, 1, 0, 15, 16, 17], 20),
+    ([2] * 40 + [100], 2), ([8], 5), ([7], 5), ([13, 13, 13], 3), ([12, 12], 80), ([0, 0, 31, 0], 2)])
+def test_short_and_long_sequences_in_one_call(lens, H, half):
+    """Around the lengths from which sequences go in chunks, in batches of both
+    kinds and of one."""
+    test_against_the_recurrence(lens, H, half)
