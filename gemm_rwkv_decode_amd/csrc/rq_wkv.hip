@@ -118,14 +118,26 @@ k_wkv_seq(const WkvArgs a, int below) {
 // Products run on the binary16 matrix cores with binary32 sums, every operand
 // in two parts, x = hi + 2^-11 lo, both binary16: hi hi' goes to one sum, hi lo'
 // + lo hi' to a second that joins with 2^-11.  What is left out or rounded is
-// below 2^-22 of an operand (2^-36 in absolute terms for values under 2^-14),
-// so a product is about as good as a binary32 one, and three binary16
-// instructions stand for eight binary32 ones (over 32 terms; measured against
-// those: 64 heads of 4096 tokens in 16 sequences 241 -> 184 us).  The state itself, the decays, the
-// triangular inverse and everything added up stay binary32.
-// A chunk in which a value does not fit this (not finite, 2^15 or more, or
-// nothing as large as 2^-12 in k, r, or the state and v together) is done token
-// by token in binary32 instead.
+// below 2^-22 of an operand, or 2^-36 where the operand is under 2^-14, and three
+// binary16 instructions stand for eight binary32 ones (over 32 terms; measured
+// against those: 64 heads of 4096 tokens in 16 sequences 241 -> 184 us).  The
+// state itself, the decays, the triangular inverse and everything added up stay
+// binary32.
+//
+// So that 2^-36 is small beside what a result is made of, operands have powers of
+// two of their own: q_t and k_s per token, their largest key to [8, 16), and S, V
+// and U per value row (the recurrence is linear in a row; the k's power goes to V,
+// W_s = 2^e_s v_s, the q's and the row's to y).  A key of q_t or k_s counts to
+// 2^-39 of the token's largest, a state entry to 2^-28 of its row's largest or
+// better; a and b need none while b is at most 256, as what they add to the state
+// is a multiple of the state.  That leaves a value row whose state is small beside
+// its v's.  It is sound as long as the chunk's first v in the row is not (every y
+// and the state then contain it), or every W that is not zero is at least 2^-14.
+// A chunk with any other such row, a larger b, a value that is not finite or an
+// operand of 2^15 or more is done token by token in binary32, and the rows'
+// powers are set anew from the state.  (The powers cost 32 multiplications in a
+// producer and 8 in a state wave a chunk, with the checks 132 -> 136 us for 4096
+// tokens in 16 sequences, 64 heads.)
 //
 // The contraction order is free, so operands are laid out for the accumulator:
 // a lane's accumulator f4 covers rows 4 (l / 16) .. + 3 of column l mod 16, and
@@ -151,7 +163,9 @@ k_wkv_seq(const WkvArgs a, int below) {
 // ---------------------------------------------------------------------------
 constexpr int CH = 16;  // tokens of a chunk
 constexpr float UP = 2048.0f, DOWN = 1.0f / 2048.0f;  // the low part's scale
-constexpr float TINY = 1.0f / 4096.0f, HUGE_ = 32768.0f;
+constexpr float HUGE_ = 32768.0f, LARGE_B = 256.0f;
+// of a row's state (and first W), and of a W, from where on they are small
+constexpr float SMALL_ROW = 1.0f / 256.0f, SMALL_W = 1.0f / 16384.0f;
 
 // Two-part operands: 4 deep (one accumulator tile) and 8 deep (two).
 struct P4 {
@@ -161,6 +175,7 @@ struct P8 {
   h8 hi, lo;
 };
 typedef float f2 __attribute__((ext_vector_type(2)));
+typedef int i4 __attribute__((ext_vector_type(4)));
 // Two values in two parts.
 __device__ __forceinline__ void split2(float x, float y, h2* hi, h2* lo) {
   *hi = __builtin_convertvector(f2{x, y}, h2);
@@ -215,7 +230,8 @@ struct alignas(16) ChunkOps {
   h8 q[2][2][64];   // q_t
   h8 kb[2][4][64];  // [part][key tile][lane]: kc, then bc, of tokens 4 g + v
   h4 x[2][64], nb[2][64], mk[2][64], nk[2][64];
-  int slow;         // token by token
+  int exps[2 * CH];  // 2^exps[t] q_t and 2^exps[16 + s] k_s are meant
+  int slow;          // token by token
 };
 // Q and then P_16 of a chunk.  Written two steps before the other operands, so four
 // of them in turn.
@@ -351,15 +367,18 @@ struct ChunkV {
 #pragma unroll
     for (int i = 0; i < 4; i++) v[i] = Vec4<T>::load1(rows, at[i]);
   }
-  // into registers of its own (a copy the compiler does not see through): the
-  // next load takes these, or it would move them at the loop's end, and wait
-  __device__ __forceinline__ f4 get() const {
+  // v[i] 2^e[i], into registers of its own (an operation the compiler does not
+  // see through): the next load takes these, or it would move them at the loop's
+  // end, and wait
+  __device__ __forceinline__ f4 get(const i4& e) const {
     f4 r;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      float x = (float)v[i];
-      if constexpr (sizeof(T) == 4) asm volatile("v_mov_b32 %0, %1" : "=v"(x) : "v"(v[i]));
-      r[i] = x;
+      const float x = (float)v[i];
+      const int ei = e[i];
+      float y;
+      asm volatile("v_ldexp_f32 %0, %1, %2" : "=v"(y) : "v"(x), "v"(ei));
+      r[i] = y;
     }
     return r;
   }
@@ -420,10 +439,37 @@ __device__ __forceinline__ float larger(float m, const f4& x) {
   for (int i = 0; i < 4; i++) m = fmaxf(m, fabsf(x[i]));
   return m;
 }
-// Whether the wave's largest magnitude (m over the lanes) is too small for
-// two-part operands: under 2^-12 and not zero.
-__device__ __forceinline__ bool too_small(float m) {
-  return __ballot(m >= TINY) == 0 && __ballot(m > 0.0f) != 0;
+__device__ __forceinline__ float largest(const f4* x) {
+  return larger(larger(larger(larger(0.0f, x[0]), x[1]), x[2]), x[3]);
+}
+// The largest of the four lanes 16 apart, of values that are not negative (a
+// NaN is the largest).
+__device__ __forceinline__ float over_groups(float m) {
+  const u32 u = __builtin_bit_cast(u32, m);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const u32 a0 = a[0], a1 = a[1], b = max(a0, a1);
+  const auto c = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const u32 c0 = c[0], c1 = c[1];
+  return __builtin_bit_cast(float, max(c0, c1));
+}
+// What the lane's row of 16 lanes holds in the first one of the four.
+__device__ __forceinline__ float of_first_group(float m) {
+  const u32 u = __builtin_bit_cast(u32, m);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const u32 a0 = a[0];
+  const auto c = __builtin_amdgcn_permlane32_swap(a0, a0, false, false);
+  const u32 c0 = c[0];
+  return __builtin_bit_cast(float, c0);
+}
+// The exponent that brings a magnitude to [8, 16) (any for zero, infinities
+// and NaN).
+__device__ __forceinline__ int to_eight(float m) { return 4 - __builtin_amdgcn_frexp_expf(m); }
+__device__ __forceinline__ f4 scaled(const f4& x, int e) {
+  return f4{ldexpf(x[0], e), ldexpf(x[1], e), ldexpf(x[2], e), ldexpf(x[3], e)};
+}
+// Position of |x| in the order of the magnitudes that are not zero; zero is last.
+__device__ __forceinline__ u32 order_not_zero(float x) {
+  return (__builtin_bit_cast(u32, x) << 1) - 1u;
 }
 
 template <typename T, int PRODUCERS>
@@ -431,6 +477,10 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
                                         int p, int lo, int hi, size_t base, size_t ld) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int n = (hi - lo + CH - 1) / CH;
+  // Segment 1 is the longest of three with binary16 inputs (conversions): there
+  // the scaling of q and k goes to segment 2 (1531 ragged tokens, 40 heads 62.8 ->
+  // 59.6 us; in binary32 62.8 and 63.4).
+  constexpr bool SCALE_LATE = PRODUCERS == 3 && sizeof(T) == 2;
   ChunkIn<T> in;
   const auto live = [&](int c) { return lo + c * CH + l16 < hi; };
   const u32 at = (u32)((l16 * ld + 4 * g) * sizeof(T));
@@ -454,7 +504,6 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     f4 av[4], qv[4], bv[4], kv[4], rest[4];  // rest: P_16 / Q
     P[2] = in.decays(2, live(c));
     P[3] = in.decays(3, live(c));
-    float big_k = 0.0f, big_r = 0.0f;
     const auto scale = [&](int j) {
 #pragma unroll
       for (int v = 0; v < 4; v++) {
@@ -468,12 +517,24 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
         qv[j][v] = r * rel;
         bv[j][v] = -((float)in.eta[j][v] * kap) * up;
         kv[j][v] = k * up;
-        big_k = fmaxf(big_k, fabsf(k));
-        big_r = fmaxf(big_r, fabsf(r));
       }
       // Q is token 7's P, P_16 token 15's
       if ((l16 & 7) == 7)
         *reinterpret_cast<f4*>(&decays[c & 7].at[l16 >> 3][16 * j + 4 * g]) = P[j];
+    };
+    // a token's largest q and k to [8, 16)
+    int up_q, up_k;
+    bool slow;
+    const auto even_out = [&] {
+      up_q = to_eight(over_groups(largest(qv)));
+      up_k = to_eight(over_groups(largest(kv)));
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        qv[j] = scaled(qv[j], up_q);
+        kv[j] = scaled(kv[j], up_k);
+        pin(qv[j]), pin(kv[j]);
+      }
+      slow = __ballot(largest(bv) > LARGE_B) != 0;
     };
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -481,6 +542,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       pin(av[j]), pin(qv[j]), pin(bv[j]), pin(kv[j]), pin(rest[j]);
       if (j == 1) half_barrier();
     }
+    if constexpr (!SCALE_LATE) even_out();
     // two steps ahead of their use, into the registers that are free by now
     // (the operands are made before, not after; past the end too, as a branch here
     // would make the compiler wait for the loads to move them)
@@ -490,7 +552,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     // segment 2: the four products' transposes, rows s = 4 g + v, columns t =
     // lane mod 16, and kc and bc turned from tokens x keys to keys x tokens by
     // products with the identity, which are exact
-    bool slow = too_small(big_k) || too_small(big_r);
+    if constexpr (SCALE_LATE) even_out();
     P8 ap[2], qp[2], kb[4];
     Sum mb = none(), mk = mb, nb = mb, nk = mb;
 #pragma unroll
@@ -574,6 +636,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     o.nb[1][lane] = nbp.lo;
     o.nk[0][lane] = nkp.hi;
     o.nk[1][lane] = nkp.lo;
+    if (lane < 2 * CH) o.exps[lane] = g == 0 ? -up_q : -up_k;
     if (lane == 0) o.slow = slow;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
@@ -642,11 +705,24 @@ k_wkv_chunk(const WkvArgs a, int from) {
   // for these loads (and with them for the stores of y)
 #pragma unroll
   for (int j = 0; j < 4; j++) pin(S[j]);
+  // S, W and U of a value row are held times 2^lift, the row's own
+  int lift;
+  const auto center = [&](float m) {
+    lift = to_eight(over_groups(m));
+#pragma unroll
+    for (int j = 0; j < 4; j++) S[j] = scaled(S[j], lift);
+  };
+  {
+    const i4 ke = *reinterpret_cast<const i4*>(&ops[0].exps[CH + 4 * g]) + 4;
+    center(larger(largest(S), even.get(ke)));  // 16 W beside S: k's keys reach 16
+  }
   const auto chunk = [&](int c, ChunkV<T>& vin) {
     const ChunkOps& o = ops[c & 1];
     const int t0 = lo + c * CH;
     // operands in the order of their use (LDS answers in order)
     bool slow = o.slow;
+    const i4 re = *reinterpret_cast<const i4*>(&o.exps[4 * g]);
+    const i4 ke = *reinterpret_cast<const i4*>(&o.exps[CH + 4 * g]);
     f4 mid[4], end[4];
 #pragma unroll
     for (int j = 0; j < 4; j++)
@@ -665,17 +741,18 @@ k_wkv_chunk(const WkvArgs a, int from) {
       kb[j] = P8{o.kb[0][j][lane], o.kb[1][j][lane]};
     }
     const P4 nb{o.nb[0][lane], o.nb[1][lane]};
-    const f4 V = vin.get();
+    const f4 W = vin.get(ke + lift);
     vin.load(chunk_rows<T>(a.v, base, ld, t0 + 2 * CH, hi), vat);
     f4 Sq[4];
-    float big = larger(0.0f, V);
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      Sq[j] = rounded(S[j] * mid[j]);
-      big = larger(big, Sq[j]);
-    }
-    slow = slow || too_small(big);
-    const P4 vs = split(V);
+    for (int j = 0; j < 4; j++) Sq[j] = rounded(S[j] * mid[j]);
+    const float row = over_groups(largest(Sq)), lead = of_first_group(W[0]);
+    const u32 least = min(min(order_not_zero(W[0]), order_not_zero(W[1])),
+                          min(order_not_zero(W[2]), order_not_zero(W[3])));
+    const bool small = row < SMALL_ROW && fabsf(lead) < SMALL_ROW &&
+                       (row > 0.0f || least < order_not_zero(SMALL_W));
+    slow = slow || __ballot(small) != 0;
+    const P4 vs = split(W);
     // (32 deep beside zeros: a 16-deep instruction's sum is not carried on by a
     // 32-deep one, which, right behind it, took half of the sum for zero)
     const h4 no = {0, 0, 0, 0};
@@ -690,7 +767,7 @@ k_wkv_chunk(const WkvArgs a, int from) {
     Sum us = none();
     mma(xp, split(rounded(u.value())), us);
     const f4 U = rounded(us.value());
-    // what is not finite, or too large for an operand, in V, S or U
+    // what is not finite, or too large for an operand, in W, S or U
     slow = slow || __ballot(!(fabsf(U[0]) + fabsf(U[1]) + fabsf(U[2]) + fabsf(U[3]) < HUGE_)) != 0;
     if (!slow) {
       const P4 up = split(U);
@@ -706,12 +783,14 @@ k_wkv_chunk(const WkvArgs a, int from) {
       const __amdgpu_buffer_rsrc_t ry = chunk_rows<float>(a.y, base, ld, t0, hi);
 #pragma unroll
       for (int v = 0; v < 4; v++) {
-        const float yt = yv[v];
+        const float yt = ldexpf(yv[v], re[v] - lift);
         __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(u32, yt), ry, yat[v], 0, 0);
       }
     } else {
       // token by token (a value that is not finite must not reach earlier
       // tokens through products with the zeros of the triangular matrices)
+#pragma unroll
+      for (int j = 0; j < 4; j++) S[j] = scaled(S[j], -lift);
       for (int t = t0; t < min(t0 + CH, hi); t++) {
         const size_t at = (size_t)t * ld + base + 4 * g;
         const float vt = (float)vp[(size_t)t * ld];
@@ -741,6 +820,7 @@ k_wkv_chunk(const WkvArgs a, int from) {
         yt += __shfl_xor(yt, 32, 64);
         if (g == 0) yp[(size_t)t * ld] = yt;
       }
+      center(largest(S));
     }
     step_barrier();
   };
@@ -754,7 +834,7 @@ k_wkv_chunk(const WkvArgs a, int from) {
   if (c < n) chunk(c, even);
   if (stored) {
 #pragma unroll
-    for (int j = 0; j < 4; j++) *reinterpret_cast<f4*>(st + 16 * j) = S[j];
+    for (int j = 0; j < 4; j++) *reinterpret_cast<f4*>(st + 16 * j) = scaled(S[j], -lift);
   }
 }
 
@@ -784,9 +864,11 @@ void launch_chunks(const WkvArgs& a, unsigned heads, int from, hipStream_t s) {
 // 91, 160 heads 164 / 163 / 95; 4096 tokens in 16 sequences, 64 heads 253 / 200 /
 // 137 us.
 //
-// Producers of binary16 inputs have more to do (conversions); at 16 rows, with
-// a SIMD's second wave free, six of them keep up with the state (4096 tokens, 64
-// heads 284 -> 252 us), which three do in binary32 (242 and 248 us).
+// At 16 rows a SIMD's second wave is free, and six producers keep up with the
+// state better than three (4096 tokens, 64 heads, binary32 271 / 245 us with
+// three / six), but its chain starts three steps later: binary32 inputs take six
+// past 256 tokens (128 tokens 15.4 / 16.5 us, 256 23.6 / 23.8, 512 39.8 / 38.3).
+// With binary16 inputs three have conversions to do as well, and six always pay.
 template <typename T>
 void launch(const WkvArgs& a, hipStream_t s) {
   const unsigned heads = (unsigned)a.sequences * a.H;
@@ -799,8 +881,10 @@ void launch(const WkvArgs& a, hipStream_t s) {
                        all_short ? a.T + 1 : from);
   if (all_short) return;
   const int least = all_long ? 0 : from;
-  if (heads <= 64)
-    launch_chunks<T, 1, sizeof(T) == 2 ? 6 : 3>(a, heads, least, s);
+  if (heads <= 64 && (sizeof(T) == 2 || a.T > 256))
+    launch_chunks<T, 1, 6>(a, heads, least, s);
+  else if (heads <= 64)
+    launch_chunks<T, 1, 3>(a, heads, least, s);
   else if (heads <= 128)
     launch_chunks<T, 2, 3>(a, heads, least, s);
   else

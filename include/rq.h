@@ -323,8 +323,14 @@ typedef enum { RQ_TYPE_F32 = 0, RQ_TYPE_F16 = 1 } rq_type;
  *   state: float [nslots][H][64][64], read and overwritten for every
  *   sequence that has a token.  y: float [T][H*64]; rows that no sequence
  *   covers are not written.
- * All sums and the state are binary32.  Non-finite inputs reach the outputs of
- * their own token and later ones only.
+ * All sums and the state are binary32.  Tokens go one by one or, in longer
+ * sequences, sixteen at a time; then factors are held to 22 bits, and the error
+ * of y[t][i] is about 2^-20 or less beside |r_t| times the largest 2-norm that
+ * row i of the state had up to t, whatever the sizes at other tokens and rows.
+ * Which of the two forms a sequence takes follows from H and from the number and
+ * lengths of all sequences of the call, so the low bits of its results may change
+ * with the batch around it.  Non-finite inputs reach the outputs of their own
+ * token and later ones only.
  * Shape rules: T, sequences and nslots as for rq_shift, 1 <= H <= 4096,
  * sequences * H <= 1 << 22.
  */
