@@ -712,10 +712,33 @@ rq_status rq_logits(const rq_logits_args* args, void* workspace, size_t workspac
   int dev;
   st = check_device(&dev);
   if (st != RQ_OK) return st;
-  const rq::LogitsArgs a{g.logits, g.out, g.tokens, g.history, g.history_offsets, g.prompt,
-                         g.repetition, g.presence, g.frequency, g.bias_ids, g.bias,
-                         g.bias_offsets, g.masks, g.mask_ids, g.M, g.V, (int)hl, (int)bl,
-                         g.nmasks};
+  // a group that is left out takes its other pointers with it, unread
+  rq::LogitsArgs a{};
+  a.logits = g.logits;
+  a.out = g.out;
+  a.tokens = g.tokens;
+  a.M = g.M;
+  a.V = g.V;
+  if (g.history) {
+    a.history = g.history;
+    a.history_offsets = g.history_offsets;
+    a.prompt = g.prompt;
+    a.repetition = g.repetition;
+    a.presence = g.presence;
+    a.frequency = g.frequency;
+    a.history_len = g.history_len;
+  }
+  if (g.bias_ids) {
+    a.bias_ids = g.bias_ids;
+    a.bias = g.bias;
+    a.bias_offsets = g.bias_offsets;
+    a.bias_len = g.bias_len;
+  }
+  if (g.masks) {
+    a.masks = g.masks;
+    a.mask_ids = g.mask_ids;
+    a.nmasks = g.nmasks;
+  }
   return rq::launch_logits(a, workspace, static_cast<hipStream_t>(stream)) == hipSuccess
              ? RQ_OK
              : RQ_ERR_LAUNCH;

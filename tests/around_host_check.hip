@@ -1,0 +1,104 @@
+// Host-only check of what the calls around the products hand to their kernels
+// (built and run by tests/test_around_host.py; no GPU code is executed).
+//
+// The library's own host code is compiled here with the HIP runtime's queries
+// and launches replaced by recorders: the C entries are called with made-up
+// addresses and what would be launched is compared with what is expected.
+// One line is printed for each disagreement, and the exit status says whether
+// there was any.
+#include <hip/hip_runtime.h>
+
+#include <cstdio>
+#include <cstring>
+#include <vector>
+
+namespace fake {
+int device = 0;
+struct Launch {
+  dim3 grid, block;
+  size_t lds;
+};
+std::vector<Launch> launches;
+template <typename A>
+struct Args {
+  static A last;  // of the kernels that take an A first
+};
+template <typename A>
+A Args<A>::last{};
+
+hipError_t get_device(int* d) {
+  *d = device;
+  return hipSuccess;
+}
+hipError_t get_properties(hipDeviceProp_t* p, int) {
+  memset(p, 0, sizeof(*p));
+  strcpy(p->gcnArchName, "gfx950");
+  return hipSuccess;
+}
+hipError_t last_error() { return hipSuccess; }
+template <typename A, typename... More>
+void launch(dim3 grid, dim3 block, size_t lds, const A& a, const More&...) {
+  launches.push_back(Launch{grid, block, lds});
+  Args<A>::last = a;
+}
+}  // namespace fake
+
+#undef hipGetDeviceProperties
+#define hipGetDeviceProperties fake::get_properties
+#define hipGetDevice fake::get_device
+#define hipGetLastError fake::last_error
+#undef hipLaunchKernelGGL
+#define hipLaunchKernelGGL(kernel, grid, block, lds, stream, ...) \
+  fake::launch(grid, block, lds, __VA_ARGS__)
+
+#include "rq_api.hip"
+#include "rq_logits.hip"
+
+namespace {
+int bad = 0;
+void expect(bool ok, const char* what) {
+  if (!ok) printf("WRONG %s\n", what), bad++;
+}
+char* at(size_t i) { return reinterpret_cast<char*>((size_t)0x7F0000000000 + (i << 32)); }
+template <typename T>
+T* array_at(size_t i) {
+  return reinterpret_cast<T*>(at(i));
+}
+}  // namespace
+
+// A group whose first pointer is NULL is left out whole: its other pointers
+// are not read, whatever they are.
+static void logits_groups() {
+  rq_logits_args g{};
+  g.logits = array_at<const float>(0);
+  g.out = array_at<float>(1);
+  g.M = 4;
+  g.V = 1000;
+  g.history_offsets = array_at<const int>(2);
+  g.prompt = array_at<const int>(3);
+  g.repetition = array_at<const float>(4);
+  g.presence = array_at<const float>(5);
+  g.frequency = array_at<const float>(6);
+  g.bias = array_at<const float>(7);
+  g.bias_offsets = array_at<const int>(8);
+  g.mask_ids = array_at<const int>(9);
+  expect(rq_logits(&g, nullptr, 0, nullptr) == RQ_OK, "groups left out are accepted");
+  const rq::LogitsArgs& a = fake::Args<rq::LogitsArgs>::last;
+  expect(!a.history && !a.bias_ids && !a.masks, "groups left out");
+  expect(!a.history_offsets && !a.prompt, "history's lists without a history");
+  expect(!a.repetition && !a.presence && !a.frequency, "penalties without a history");
+  expect(!a.bias && !a.bias_offsets && !a.mask_ids, "lists of biases and masks left out");
+  g.history = array_at<const int>(10);
+  g.history_len = 100;
+  expect(rq_logits(&g, nullptr, 0, nullptr) == RQ_OK, "a history is accepted");
+  expect(a.history == g.history && a.history_offsets == g.history_offsets &&
+             a.prompt == g.prompt && a.repetition == g.repetition && a.presence == g.presence &&
+             a.frequency == g.frequency && a.history_len == 100,
+         "a history's lists reach the kernel");
+}
+
+int main() {
+  logits_groups();
+  printf("wrong=%d\n", bad);
+  return bad ? 1 : 0;
+}
