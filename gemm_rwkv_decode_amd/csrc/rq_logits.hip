@@ -277,8 +277,9 @@ hipError_t launch_slices(const LogitsArgs& a, u64* records, int stride, int work
   const int slices = (own + most - 1) / most;
   const int sl = (own + slices - 1) / slices * STEP;
   const size_t lds = token * sl;
+  constexpr size_t fixed = NT / 64 * sizeof(u64);  // wave_best
   static bool raised = false;  // allow the full LDS once per instantiation
-  if (lds > (64 << 10) && !raised) {
+  if (lds + fixed > (64 << 10) && !raised) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_logits<NT>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize,
                                              LOGITS_LDS);

@@ -36,6 +36,12 @@ hipError_t get_properties(hipDeviceProp_t* p, int) {
   return hipSuccess;
 }
 hipError_t last_error() { return hipSuccess; }
+int lds_limit = 64 << 10;  // of a launch's dynamic and static LDS
+hipError_t set_attribute(const void*, hipFuncAttribute what, int value) {
+  if (what != hipFuncAttributeMaxDynamicSharedMemorySize) return hipErrorInvalidValue;
+  lds_limit = value;
+  return hipSuccess;
+}
 template <typename A, typename... More>
 void launch(dim3 grid, dim3 block, size_t lds, const A& a, const More&...) {
   launches.push_back(Launch{grid, block, lds});
@@ -45,6 +51,7 @@ void launch(dim3 grid, dim3 block, size_t lds, const A& a, const More&...) {
 
 #undef hipGetDeviceProperties
 #define hipGetDeviceProperties fake::get_properties
+#define hipFuncSetAttribute fake::set_attribute
 #define hipGetDevice fake::get_device
 #define hipGetLastError fake::last_error
 #undef hipLaunchKernelGGL
@@ -97,8 +104,26 @@ static void logits_groups() {
          "a history's lists reach the kernel");
 }
 
+// A kernel's limit is raised where its dynamic and its static LDS (up to 128
+// bytes, one record for each wave) together pass 64 KiB.
+static void logits_lds() {
+  rq_logits_args g{};
+  g.logits = array_at<const float>(0);
+  g.out = array_at<float>(16);
+  g.history = array_at<const int>(32);
+  g.history_offsets = array_at<const int>(33);
+  const int sizes[][2] = {{128, 65536}, {256, 32768}, {256, 65536}, {1, 65536}, {64, 65536}};
+  for (const auto& mv : sizes) {
+    g.M = mv[0];
+    g.V = mv[1];
+    expect(rq_logits(&g, nullptr, 0, nullptr) == RQ_OK, "history only");
+    expect((int)fake::launches.back().lds + 128 <= fake::lds_limit, "LDS within its limit");
+  }
+}
+
 int main() {
   logits_groups();
+  logits_lds();
   printf("wrong=%d\n", bad);
   return bad ? 1 : 0;
 }

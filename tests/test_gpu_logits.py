@@ -269,3 +269,13 @@ def test_counts_past_fifteen_bits(M, V, given):
     want, tok = R.logits_ref(z, hist, **pen, bias=bias, masks=(bits, which))
     out, got = run(z, **device_args(hist, pen, bias, bits, which))
     assert same_bits(out, want) and got.tolist() == tok.tolist()
+
+
+@pytest.mark.parametrize("M,V", [(128, 65536), (256, 32768)])
+def test_ranges_of_64_kib_of_counts(M, V):
+    """A history alone, counted in exactly 64 KiB of LDS."""
+    say(f"[logits] M {M} V {V}")
+    z, hist, pen, _, _, _ = make(M, V, 20, 0, 0, M)
+    want, tok = R.logits_ref(z, hist, **pen)
+    out, got = run(z, **device_args(hist, pen))
+    assert same_bits(out, want) and got.tolist() == tok.tolist()
