@@ -4,7 +4,29 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
+
 namespace rq {
+
+// Allows a kernel that much dynamic LDS.  The limit belongs to a device, so it is
+// raised once on every device the kernel runs on; each kernel has its own LdsLimit.
+class LdsLimit {
+ public:
+  hipError_t raise(const void* kernel, size_t bytes) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);  // below 64: rq_api.hip takes no others
+    if (e != hipSuccess) return e;
+    const unsigned long long mine = 1ull << dev;
+    if (done_.load(std::memory_order_acquire) & mine) return hipSuccess;
+    // (threads that get here together set the same value)
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == hipSuccess) done_.fetch_or(mine, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<unsigned long long> done_{0};
+};
 
 // Launch-shape overrides for measurements and tests, read from the
 // environment once (RQ_GEMV_LPR, RQ_GEMV_CPL, RQ_GEMV_NPASS, RQ_GEMM_PLAN,

@@ -278,13 +278,10 @@ hipError_t launch_slices(const LogitsArgs& a, u64* records, int stride, int work
   const int sl = (own + slices - 1) / slices * STEP;
   const size_t lds = token * sl;
   constexpr size_t fixed = NT / 64 * sizeof(u64);  // wave_best
-  static bool raised = false;  // allow the full LDS once per instantiation
-  if (lds + fixed > (64 << 10) && !raised) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_logits<NT>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             LOGITS_LDS);
+  if (lds + fixed > (64 << 10)) {
+    static LdsLimit limit;
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_logits<NT>), LOGITS_LDS);
     if (e != hipSuccess) return e;
-    raised = true;
   }
   hipLaunchKernelGGL((k_logits<NT>), dim3((steps + own - 1) / own, a.M), dim3(NT), lds, s, a,
                      records, stride, own * STEP, sl);

@@ -350,13 +350,9 @@ static hipError_t launch_mv_t(const Problem* const* p, int count, int M, hipStre
   const int kr = ((K / ck + MV_WAVES - 1) / MV_WAVES) * ck;
   const int lds = mv_lds_bytes(kr, ME);
   if (lds > MV_LDS) return hipErrorInvalidValue;
-  static bool raised = false;  // allow the full LDS once per instantiation
-  if (!raised) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_mv<FMT, G, ME, B>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, MV_LDS);
-    if (e != hipSuccess) return e;
-    raised = true;
-  }
+  static LdsLimit limit;
+  const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_mv<FMT, G, ME, B>), MV_LDS);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_mv<FMT, G, ME, B>), dim3(blocks), dim3(64 * MV_WAVES), lds, s, bt, M, K,
                      mv_xstr(kr));
   return hipGetLastError();

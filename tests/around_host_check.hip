@@ -10,11 +10,15 @@
 
 #include <cstdio>
 #include <cstring>
+#include <map>
+#include <mutex>
+#include <utility>
 #include <vector>
 
 namespace fake {
 int device = 0;
 struct Launch {
+  const void* kernel;
   dim3 grid, block;
   size_t lds;
 };
@@ -36,15 +40,22 @@ hipError_t get_properties(hipDeviceProp_t* p, int) {
   return hipSuccess;
 }
 hipError_t last_error() { return hipSuccess; }
-int lds_limit = 64 << 10;  // of a launch's dynamic and static LDS
-hipError_t set_attribute(const void*, hipFuncAttribute what, int value) {
+// a kernel's limit of dynamic and static LDS, on each device
+std::map<std::pair<int, const void*>, int> lds_limits;
+std::mutex lds_mutex;
+hipError_t set_attribute(const void* kernel, hipFuncAttribute what, int value) {
   if (what != hipFuncAttributeMaxDynamicSharedMemorySize) return hipErrorInvalidValue;
-  lds_limit = value;
+  std::lock_guard<std::mutex> lk(lds_mutex);
+  lds_limits[{device, kernel}] = value;
   return hipSuccess;
 }
+int lds_limit(const void* kernel) {
+  const auto it = lds_limits.find({device, kernel});
+  return it == lds_limits.end() ? 64 << 10 : it->second;
+}
 template <typename A, typename... More>
-void launch(dim3 grid, dim3 block, size_t lds, const A& a, const More&...) {
-  launches.push_back(Launch{grid, block, lds});
+void launch(const void* kernel, dim3 grid, dim3 block, size_t lds, const A& a, const More&...) {
+  launches.push_back(Launch{kernel, grid, block, lds});
   Args<A>::last = a;
 }
 }  // namespace fake
@@ -56,10 +67,11 @@ void launch(dim3 grid, dim3 block, size_t lds, const A& a, const More&...) {
 #define hipGetLastError fake::last_error
 #undef hipLaunchKernelGGL
 #define hipLaunchKernelGGL(kernel, grid, block, lds, stream, ...) \
-  fake::launch(grid, block, lds, __VA_ARGS__)
+  fake::launch(reinterpret_cast<const void*>(kernel), grid, block, lds, __VA_ARGS__)
 
 #include "rq_api.hip"
 #include "rq_logits.hip"
+#include "rq_mv.hip"
 
 namespace {
 int bad = 0;
@@ -117,13 +129,39 @@ static void logits_lds() {
     g.M = mv[0];
     g.V = mv[1];
     expect(rq_logits(&g, nullptr, 0, nullptr) == RQ_OK, "history only");
-    expect((int)fake::launches.back().lds + 128 <= fake::lds_limit, "LDS within its limit");
+    const fake::Launch& l = fake::launches.back();
+    expect((int)l.lds + 128 <= fake::lds_limit(l.kernel), "LDS within its limit");
   }
+}
+
+// The limit is a device's: every device a kernel runs on has it raised.
+static void lds_on_every_device() {
+  rq_logits_args g{};
+  g.logits = array_at<const float>(0);
+  g.out = array_at<float>(16);
+  g.history = array_at<const int>(32);
+  g.history_offsets = array_at<const int>(33);
+  g.M = 200;
+  g.V = 65536;
+  rq::Problem p{array_at<const void>(0), array_at<const void>(1), nullptr, array_at<const void>(2),
+                array_at<float>(3), 4, 4096, 16384, 64, rq::FMT_S4};
+  const rq::Problem* const ps[] = {&p};
+  for (fake::device = 0; fake::device < 64; fake::device += 21) {
+    expect(rq_logits(&g, nullptr, 0, nullptr) == RQ_OK, "logits on another device");
+    const fake::Launch l = fake::launches.back();
+    expect((int)l.lds + 128 <= fake::lds_limit(l.kernel), "LDS of rq_logits on another device");
+    expect(rq::launch_mv_many(ps, 1, nullptr) == hipSuccess, "products on another device");
+    const fake::Launch m = fake::launches.back();
+    expect((int)m.lds > 64 << 10 && (int)m.lds <= fake::lds_limit(m.kernel),
+           "LDS of the decode kernel on another device");
+  }
+  fake::device = 0;
 }
 
 int main() {
   logits_groups();
   logits_lds();
+  lds_on_every_device();
   printf("wrong=%d\n", bad);
   return bad ? 1 : 0;
 }
