@@ -849,9 +849,13 @@ void launch_chunks(const WkvArgs& a, unsigned heads, int from, hipStream_t s) {
 // us, 8 6.5 / 6.4, 16 10.2 / 6.5); many: 16 (1024 heads, sequences of 8 tokens
 // 15 / 24 us, 16 28 / 25; 2048 heads 29 / 47 and 48 / 47 us).
 //
-// The lengths are on the device.  Where sequences have on average more than 12
-// tokens beyond their first, all go in chunks; below that each kind has a launch
-// of its own, which passes over the other's sequences (chunks only / both: 64
+// The lengths are on the device.  Where no sequence reaches that length, as all of
+// them have a token, or all together have not as many, all go token by token
+// (fewer tokens than sequences mean empty ones, and any of the others may be long:
+// 255 tokens in one of 256 slots, 64 heads 151 -> 43 us; a second launch for every batch
+// of single tokens would cost it 2 to 6 us).  Where sequences have on average more
+// than 12 tokens beyond their first, all go in chunks; between the two each kind
+// has a launch of its own, which passes over the other's sequences (chunks only / both: 64
 // heads, 31 single tokens beside one sequence of 48 49 / 22 us, of 500 56 / 61; 16
 // sequences of 8 24 / 18, of 16 25 / 27).
 //
@@ -874,7 +878,7 @@ void launch(const WkvArgs& a, hipStream_t s) {
   const unsigned heads = (unsigned)a.sequences * a.H;
   const int from = heads <= 128 ? 8 : 16;
   const int extra = a.T - a.sequences;
-  const bool all_short = extra + 1 < from;
+  const bool all_short = a.T < from || (extra >= 0 && extra + 1 < from);
   const bool all_long = !all_short && (a.sequences == 1 || extra / 12 >= a.sequences);
   if (!all_long)
     hipLaunchKernelGGL((k_wkv_seq<T>), dim3(heads), dim3(256), 0, s, a,

@@ -329,7 +329,9 @@ typedef enum { RQ_TYPE_F32 = 0, RQ_TYPE_F16 = 1 } rq_type;
  * row i of the state had up to t, whatever the sizes at other tokens and rows.
  * Which of the two forms a sequence takes follows from H and from the number and
  * lengths of all sequences of the call, so the low bits of its results may change
- * with the batch around it.  Non-finite inputs reach the outputs of their own
+ * with the batch around it.  (A call with as many tokens as sequences, or up to
+ * 14 more, is taken to have no empty sequence: a long one in it, which only empty
+ * ones make possible, goes token by token.)  Non-finite inputs reach the outputs of their own
  * token and later ones only.
  * Shape rules: T, sequences and nslots as for rq_shift, 1 <= H <= 4096,
  * sequences * H <= 1 << 22.

@@ -72,6 +72,7 @@ void launch(const void* kernel, dim3 grid, dim3 block, size_t lds, const A& a, c
 #include "rq_api.hip"
 #include "rq_logits.hip"
 #include "rq_mv.hip"
+#include "rq_wkv.hip"
 
 namespace {
 int bad = 0;
@@ -158,7 +159,30 @@ static void lds_on_every_device() {
   fake::device = 0;
 }
 
+// Launches of rq_wkv7: token by token, in chunks, or one of each.  Fewer tokens
+// than sequences say that some are empty, and then any of the others may be long.
+static size_t wkv_launches(int T, int sequences, int H) {
+  const size_t before = fake::launches.size();
+  expect(rq_wkv7(at(0), at(8), at(16), at(24), at(32), at(40), RQ_TYPE_F32, nullptr,
+                 array_at<float>(48), array_at<const int>(56), array_at<const int>(57), T, H,
+                 sequences, 0, nullptr) == RQ_OK,
+         "wkv7");
+  return fake::launches.size() - before;
+}
+static void wkv_empty_sequences() {
+  expect(wkv_launches(48, 64, 4) == 2, "48 tokens in 64 slots");
+  expect(wkv_launches(255, 256, 64) == 2, "255 tokens in 256 slots");
+  expect(wkv_launches(20, 4096, 1) == 2, "20 tokens in 4096 slots");
+  expect(wkv_launches(7, 64, 1) == 1, "7 tokens, none long");
+  expect(wkv_launches(15, 64, 4) == 1, "15 tokens of many heads, none long");
+  expect(wkv_launches(64, 64, 64) == 1, "a single token in every slot");
+  expect(wkv_launches(70, 64, 64) == 1, "few more tokens than sequences");
+  expect(wkv_launches(300, 64, 64) == 2, "both kinds");
+  expect(wkv_launches(4096, 1, 64) == 1, "one prompt");
+}
+
 int main() {
+  wkv_empty_sequences();
   logits_groups();
   logits_lds();
   lds_on_every_device();

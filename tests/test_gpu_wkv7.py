@@ -256,3 +256,11 @@ def test_short_and_long_sequences_in_one_call(lens, H, half):
     """Around the lengths from which sequences go in chunks, in batches of both
     kinds and of one."""
     test_against_the_recurrence(lens, H, half)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("lens,H", [([0] * 63 + [48], 2), ([0] * 40 + [39] + [0] * 23, 64),
+                                    ([0, 9] * 30 + [0] * 300, 3), ([0] * 20 + [7], 5)])
+def test_mostly_empty_sequences(lens, H, half):
+    """Fewer tokens than sequences."""
+    test_against_the_recurrence(lens, H, half)
