@@ -314,9 +314,10 @@ __device__ __forceinline__ void up_body(const LoraProblem& p, const LoraArgs& a,
       float big = fmaxf(fmaxf(fabsf(t[i][0]), fabsf(t[i][1])), fmaxf(fabsf(t[i][2]), fabsf(t[i][3])));
 #pragma unroll
       for (int d = LT / 2; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor(big, d, 64));
-      // 2^x with big / 2^x in [0.5, 1); 1 where big is zero or not finite
-      int x = 0;
-      if (big > 0.0f && big < __builtin_inff()) x = __builtin_amdgcn_frexp_expf(big);
+      // 2^x with big / 2^x in [0.5, 1); 1 where big is zero; beside an infinity no
+      // finite entry may become one (their difference would be NaN)
+      int x = 128;
+      if (big < __builtin_inff()) x = __builtin_amdgcn_frexp_expf(big);
       const int j = i * PASS + tid / LT;
       h4 vh, vl;
 #pragma unroll

@@ -366,7 +366,9 @@ typedef struct {
  * y_in is the shared projection's output, y usually the same array.  A row
  * whose id lies outside 0 .. adapters-1, or whose adapter has rank 0, gets
  * y[m] = y_in[m].  So does one whose rank is not a multiple of 8, exceeds
- * max_rank or leaves 0 .. total_rank.  A_i x is kept in binary32.
+ * max_rank or leaves 0 .. total_rank.  A_i x is kept in binary32 and meets B_i in
+ * 22 bits of its largest entry; infinities and NaN in A_i x reach y as in the
+ * formula, an infinite value of B_i as NaN.
  *   ids: [M].  offsets: [adapters + 1], multiples of 8.  scales: float
  *   [adapters], NULL for 1.  workspace: device memory of at least
  *   rq_lora_workspace_size bytes, 16-byte aligned, that overlaps nothing else; it needs

@@ -248,3 +248,24 @@ def test_a_workspace_of_the_queried_size():
     assert e.value.status == rq.RQ_ERR_SCRATCH
     torch.cuda.synchronize()
     assert bool((y == 2.0).all())
+
+
+@pytest.mark.parametrize("M,size", [(7, 1.0), (7, 3000.0), (70, 3000.0)])
+def test_an_infinite_entry_of_an_adapter_gives_what_the_formula_gives(M, size):
+    """Infinities of the formula's sign, beside large finite entries as well; NaN
+    where it multiplies a zero."""
+    N, K, rank = 200, 256, 16
+    a, b = pool(N, K, [rank], 1)
+    x, y_in = rows(M, N, K, 2, massive=False)
+    x = (x * size).clamp(-6e4, 6e4)
+    x[3, 5] = 0
+    a[2, 5] = float("inf")
+    b.view(N, rank)[11, 2] = 0
+    probs = [(a, b, x, y_in, N, K)]
+    scales = torch.tensor([-0.5])
+    got = run(probs, [0] * M, [0, rank], scales, rank)[0].cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        ref, _ = R.lora_ref((a.numpy(), b.numpy(), x.numpy(), y_in.numpy(), N, K), [0] * M,
+                            [0, rank], scales.numpy(), rank, rank)
+    assert np.isinf(ref).sum() == (M - 1) * (N - 1) and np.isnan(ref).sum() == M + N - 1
+    assert np.array_equal(got.astype(np.float64), ref, equal_nan=True)
