@@ -432,7 +432,7 @@ int lora_splits(int count, int M, int K, int adapters, int max_rank) {
 hipError_t launch_lora(const LoraBatch& bt, const LoraArgs& a, hipStream_t s) {
   const int blocks = (a.M + ROWS - 1) / ROWS;
   int groups = a.M < ROWS ? a.M : ROWS;
-  if (groups > a.adapters + 1) groups = a.adapters + 1;
+  if (groups - 1 > a.adapters) groups = a.adapters + 1;
   // the more blocks of rows, the fewer workgroups for a block's groups: each
   // then takes several, where there are several, instead of most finding none
   // (prompts: a block's rows mostly share an adapter or two)
@@ -446,7 +446,7 @@ hipError_t launch_lora(const LoraBatch& bt, const LoraArgs& a, hipStream_t s) {
   // With few, a wave takes four tiles of 16 outputs for more of B in flight (64
   // rows, 48 adapters of rank 32 or 16, 4096x4096: 22.1 -> 16.6 us), two where
   // that would leave CUs without work (one row, 768x768: 7.2 against 7.7 us).
-  const bool few = blocks == 1 && (a.M <= 16 || a.adapters * 8 >= a.M);
+  const bool few = blocks == 1 && (a.M <= 16 || a.adapters >= (a.M + 7) / 8);
   const bool wide = few && (long long)n * bt.count * groups >= 256 * Up<4>::N;
   const int per = wide ? Up<4>::N : Up<2>::N;
   const dim3 up((n + per - 1) / per, bt.count * blocks, groups);

@@ -71,6 +71,7 @@ void launch(const void* kernel, dim3 grid, dim3 block, size_t lds, const A& a, c
 
 #include "rq_api.hip"
 #include "rq_logits.hip"
+#include "rq_lora.hip"
 #include "rq_mv.hip"
 #include "rq_wkv.hip"
 
@@ -181,7 +182,34 @@ static void wkv_empty_sequences() {
   expect(wkv_launches(4096, 1, 64) == 1, "one prompt");
 }
 
+// Any number of adapters an int32 id can name: a block's groups are no more than
+// its rows, and few-row kernels are taken where rows mostly have their own.
+static void lora_many_adapters() {
+  for (int adapters : {1, 3, 100, 1 << 28, 2147483647}) {
+    for (int M : {1, 4, 64, 100}) {
+      rq_lora_problem p{at(0), at(8), at(16), nullptr, array_at<float>(24), 4096, 4096};
+      size_t need = 0;
+      expect(rq_lora_workspace_size(&p, 1, M, adapters, 16, &need) == RQ_OK, "workspace size");
+      expect(rq_lora(&p, 1, M, array_at<const int>(32), array_at<const int>(40), nullptr, adapters,
+                     48, 16, at(64), need, nullptr) == RQ_OK,
+             "lora");
+      const size_t n = fake::launches.size();
+      const int rows = M < 64 ? M : 64;
+      const int most = adapters < rows ? adapters + 1 : rows;
+      for (size_t i = n - 2; i < n; i++) {
+        const dim3 g = fake::launches[i].grid;
+        expect(g.z >= 1 && (int)g.z <= most && g.y == (M + 63u) / 64, "groups of a block of rows");
+      }
+      if (M == 64 && adapters >= 100) {  // the same kernel from 100 adapters on
+        static const void* const first = fake::launches[n - 1].kernel;
+        expect(fake::launches[n - 1].kernel == first, "few rows an adapter");
+      }
+    }
+  }
+}
+
 int main() {
+  lora_many_adapters();
   wkv_empty_sequences();
   logits_groups();
   logits_lds();
