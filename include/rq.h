@@ -296,7 +296,9 @@ rq_status rq_gemm_smallm_noalloc(const void* qweight, const void* scales, const 
  * two taps, n of them over one input (RWKV-7's time mix takes six).
  *   x: binary16 [T][D].  mu: binary16 [n][D].  state: binary16 [nslots][D].
  *   out: binary16 [n][T][D], computed in binary32 and rounded once.
- * Rows of x that no sequence covers leave unspecified rows in out.
+ * Rows of x that no sequence covers leave unspecified rows in out.  A sequence
+ * whose offsets leave 0 .. T does not begin: its slot is neither read nor written,
+ * and its rows are mixed with the row before them in x (row 0 with zeros).
  * Shape rules: 1 <= T <= RQ_MAX_TOKENS, 8 <= D <= 1 << 24, D % 8 == 0, 1 <= n <=
  * RQ_SHIFT_MAX_MIXES, 1 <= sequences <= RQ_MAX_SEQUENCES, nslots >= 0 (at least `sequences` when slots is NULL; state
  * may be NULL when nslots is 0, which needs slots).
@@ -322,7 +324,7 @@ typedef enum { RQ_TYPE_F32 = 0, RQ_TYPE_F16 = 1 } rq_type;
  *   before its two activations, kappa the removal key, eta its learning rate.
  *   state: float [nslots][H][64][64], read and overwritten for every
  *   sequence that has a token.  y: float [T][H*64]; rows that no sequence
- *   covers are not written.
+ *   covers are not written.  A sequence whose offsets leave 0 .. T is cut to it.
  * All sums and the state are binary32.  Tokens go one by one or, in longer
  * sequences, sixteen at a time; then factors are held to 22 bits, and the error
  * of y[t][i] is about 2^-20 or less beside |r_t| times the largest 2-norm that

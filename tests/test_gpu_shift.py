@@ -125,3 +125,18 @@ def test_replays_carry_the_state():
         check(out, ref, xn, [1] * B, before, range(B))
         assert np.array_equal(state.cpu().numpy(), after)
         before = torch.from_numpy(after)
+
+
+def test_rows_of_a_sequence_that_leaves_the_range():
+    """They are mixed with the row before them, the first with zeros."""
+    T, D = 20, 64
+    x, mu, state0 = tensors(T, D, 3, 3, 5)
+    out = torch.empty((3, T, D), dtype=torch.float16, device="cuda")
+    state = state0.cuda()
+    rq.rq_shift(x.cuda(), mu.cuda(), state, out, R.dev_ints([-5, 3, 8, T + 100]))
+    ref, _ = R.shift_ref(x.numpy(), mu.numpy(), state0.numpy(), [3, 5, 12], [-1, 1, -1])
+    before = x[7].double().numpy()  # of the third sequence's first row
+    ref[:, 8] = x[8].double().numpy() + (before - x[8].double().numpy()) * mu.double().numpy()
+    ref[:, 0] = x[0].double().numpy() * (1 - mu.double().numpy())
+    check(out, ref, x, [T], state0, [0])
+    assert torch.equal(state.cpu()[[0, 2]], state0[[0, 2]])
