@@ -221,7 +221,8 @@ def choose(logits, histories, repetition, presence, frequency, bias=None, masks=
 
 def generate(model, prompts, steps, adapters=None, ids=None, repetition=1.1, presence=0.2,
              frequency=0.1, bias=None, masks=None, on_step=None, graph=False):
-    """``steps`` greedy tokens after each prompt, int32 [requests][steps].
+    """``steps`` greedy tokens after each prompt, int32 [requests][steps]; -1
+    throughout for a request whose mask leaves no token.
     ids: one adapter per request.  on_step(i, logits) sees the head's logits
     before they are treated (i = 0: the prompts').  graph: the steps after the
     first single-token one are replays of a captured graph; the results are
@@ -229,6 +230,12 @@ def generate(model, prompts, steps, adapters=None, ids=None, repetition=1.1, pre
     dev, n = model.device, len(prompts)
     if not n or not all(prompts):
         raise ValueError("a prompt has at least one token")
+    if min(map(min, prompts)) < 0 or max(map(max, prompts)) >= model.vocab:
+        raise ValueError(f"tokens of 0 .. {model.vocab - 1} expected")
+    if steps < 1:
+        raise ValueError("at least one step expected")
+    if ids is not None and len(ids) != n:
+        raise ValueError(f"an adapter for each of {n} requests expected, got {len(ids)}")
 
     def ints(v):
         return torch.tensor(v, dtype=torch.int32, device=dev)

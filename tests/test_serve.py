@@ -256,3 +256,14 @@ def test_the_command(capsys, eager):
     lines = capsys.readouterr().out.splitlines()
     assert lines[0].startswith("6 requests") and "tokens/s" in lines[1]
     assert sum(line.startswith("request ") for line in lines) == 3
+
+
+@pytest.mark.parametrize("prompts,steps,ids", [
+    ([[1, 64]], 2, None), ([[1], [-1, 3]], 2, None), ([[1]], 0, None), ([[1]], -1, None),
+    ([[1], [2]], 2, [0]), ([[1]], 2, [0, 0])])
+def test_what_generate_refuses(prompts, steps, ids):
+    """On the host: a token outside the vocabulary would index past the embedding
+    on the GPU."""
+    model = V.Model(1, 64, 64, device="cpu")
+    with pytest.raises(ValueError):
+        V.generate(model, prompts, steps, ids=ids)
