@@ -233,11 +233,13 @@ struct alignas(16) ChunkOps {
   int exps[2 * CH];  // 2^exps[t] q_t and 2^exps[16 + s] k_s are meant
   int slow;          // token by token
 };
-// Q and then P_16 of a chunk.  Written two steps before the other operands, so four
-// of them in turn.
+// Q and then P_16 of a chunk.  Written in its first segment, as many steps before
+// they are read as there are producers, while that many later chunks write theirs:
+// a ring of more places than that.
 struct alignas(16) ChunkDecays {
   float at[2][HD];
 };
+constexpr int RING = 8;
 
 // product over the lanes of a row of 16 up to this one, for four values: a
 // lane without a left neighbour at the distance keeps its value (a DPP read
@@ -520,7 +522,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       }
       // Q is token 7's P, P_16 token 15's
       if ((l16 & 7) == 7)
-        *reinterpret_cast<f4*>(&decays[c & 7].at[l16 >> 3][16 * j + 4 * g]) = P[j];
+        *reinterpret_cast<f4*>(&decays[c & (RING - 1)].at[l16 >> 3][16 * j + 4 * g]) = P[j];
     };
     // a token's largest q and k to [8, 16)
     int up_q, up_k;
@@ -653,7 +655,8 @@ template <typename T, int NR, int PRODUCERS>
 __global__ void __launch_bounds__(64 * (NR + PRODUCERS), 2)
 k_wkv_chunk(const WkvArgs a, int from) {
   __shared__ ChunkOps ops[2];
-  __shared__ ChunkDecays decays[8];
+  __shared__ ChunkDecays decays[RING];
+  static_assert(RING > PRODUCERS && (RING & (RING - 1)) == 0, "chunks c % RING in turn");
   // heads are the fast index: a sequence's workgroups go to all XCDs, a head's
   // (they read the same inputs) to one
   constexpr int TILES = 4 / NR;
@@ -726,7 +729,7 @@ k_wkv_chunk(const WkvArgs a, int from) {
     f4 mid[4], end[4];
 #pragma unroll
     for (int j = 0; j < 4; j++)
-      mid[j] = *reinterpret_cast<const f4*>(&decays[c & 7].at[0][16 * j + 4 * g]);
+      mid[j] = *reinterpret_cast<const f4*>(&decays[c & (RING - 1)].at[0][16 * j + 4 * g]);
     const P4 mk{o.mk[0][lane], o.mk[1][lane]}, nk{o.nk[0][lane], o.nk[1][lane]};
     P8 ap[2], qp[2], kb[4];
 #pragma unroll
@@ -737,7 +740,7 @@ k_wkv_chunk(const WkvArgs a, int from) {
     const P4 xp{o.x[0][lane], o.x[1][lane]};
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      end[j] = *reinterpret_cast<const f4*>(&decays[c & 7].at[1][16 * j + 4 * g]);
+      end[j] = *reinterpret_cast<const f4*>(&decays[c & (RING - 1)].at[1][16 * j + 4 * g]);
       kb[j] = P8{o.kb[0][j][lane], o.kb[1][j][lane]};
     }
     const P4 nb{o.nb[0][lane], o.nb[1][lane]};
