@@ -8,10 +8,12 @@
 // A thread owns 8 channels (16 bytes) of TB = 2 consecutive tokens: a row of x is
 // read once or twice (the second time from L2), a mix vector once per two
 // tokens, however many mixes are made from them, and all of a thread's loads
-// are asked for together.  The outputs, n times the input, go past the caches.
-// 4001 tokens of width 2560, six mixes: 26 us, 5.5 TB/s (four tokens a thread,
-// mix vectors one after another, stored through the caches 31.5 us; 64 tokens of
-// width 4096 4.9 and 8.2 us).
+// are asked for together.  The outputs stay in the caches for the products that
+// read them next: stored past them, a call whose batches take turns in more memory
+// than the last-level cache is faster by itself (4001 tokens of width 2560, six
+// mixes, three batches in turn 25.8 against 31.6 us; one batch 25.0 against 23.8),
+// but with the receptance, key and value products behind it the chain is slower
+// (1308 against 1126 us; 512 tokens of width 4096 146 against 141 us).
 //
 // Which tokens begin a sequence is found by all threads together: each looks
 // at some sequences and, where one begins inside this workgroup's tokens,
@@ -102,7 +104,7 @@ k_shift(const ShiftArgs a) {
           const float xe = (float)x[j].h[e];
           o.h[e] = (_Float16)(xe + ((float)before[j].h[e] - xe) * (float)mu.h[e]);
         }
-        __builtin_nontemporal_store(o.v, reinterpret_cast<u32x4*>(op + i * plane + j * D));
+        *reinterpret_cast<u32x4*>(op + i * plane + j * D) = o.v;
       }
     }
   }
