@@ -120,7 +120,7 @@ __device__ __forceinline__ u32x4 counts_of(const u32* cnt, u32 t, bool big) {
 
 // A workgroup takes `per` tokens of one row, in slices of `sl` tokens (half as
 // many where the counts need 32 bits), and a slice in steps of 4 NT.
-template <int NT>
+template <int NT, bool TOKENS>
 __global__ void __launch_bounds__(NT)
 k_logits(const LogitsArgs a, u64* records, int stride, int per, int sl) {
   constexpr int STEP = 4 * NT;
@@ -213,7 +213,7 @@ k_logits(const LogitsArgs a, u64* records, int stride, int per, int sl) {
 #pragma unroll
       for (int i = 0; i < 4; i++)
         if (!((word >> ((v0 + e) % 32 + i)) & 1u)) z[i] = -__builtin_inff();
-      if (a.tokens) {
+      if constexpr (TOKENS) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
           const u32 o = all || e + i < n ? order_of(z[i]) : 0u;
@@ -222,9 +222,15 @@ k_logits(const LogitsArgs a, u64* records, int stride, int per, int sl) {
         }
       }
       if (all) {
-        // (past the caches: logits and outputs of many rows are larger than they
-        // are; 256 x 65536 36 -> 30 us)
-        __builtin_nontemporal_store((f4u)z, reinterpret_cast<f4u*>(out + v0 + e));
+        // Past the caches where the tokens are chosen here, as nobody has to read the
+        // outputs then (200 x 65529 with histories of 12000, batches in turn 32.0 ->
+        // 28.5 us, 64 x 65536 13.8 -> 13.2).  Without tokens the caller reads them
+        // next: with a softmax behind the call 64 x 65536 take 34.8 us through the
+        // caches, 42.5 past them.
+        if constexpr (TOKENS)
+          __builtin_nontemporal_store((f4u)z, reinterpret_cast<f4u*>(out + v0 + e));
+        else
+          *reinterpret_cast<f4u*>(out + v0 + e) = (f4u)z;
       } else {
 #pragma unroll
         for (int c = 0; c < 3; c++)
@@ -236,7 +242,7 @@ k_logits(const LogitsArgs a, u64* records, int stride, int per, int sl) {
     if (u0 < n) step(u0, std::false_type());
     if ((a.history || a.bias_ids) && v0 + span < last) __syncthreads();  // before the clearing
   }
-  if (!a.tokens) return;
+  if constexpr (!TOKENS) return;
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) {
     const u64 o = __shfl_xor(top, d, 64);
@@ -266,7 +272,7 @@ k_logits(const LogitsArgs a, u64* records, int stride, int per, int sl) {
 
 // `workgroups` of a row, each in as few slices as its LDS allows.
 constexpr size_t LOGITS_LDS = 152 << 10;
-template <int NT>
+template <int NT, bool TOKENS>
 hipError_t launch_slices(const LogitsArgs& a, u64* records, int stride, int workgroups,
                          hipStream_t s) {
   constexpr int STEP = 4 * NT;
@@ -280,10 +286,10 @@ hipError_t launch_slices(const LogitsArgs& a, u64* records, int stride, int work
   constexpr size_t fixed = NT / 64 * sizeof(u64);  // wave_best
   if (lds + fixed > (64 << 10)) {
     static LdsLimit limit;
-    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_logits<NT>), LOGITS_LDS);
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_logits<NT, TOKENS>), LOGITS_LDS);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((k_logits<NT>), dim3((steps + own - 1) / own, a.M), dim3(NT), lds, s, a,
+  hipLaunchKernelGGL((k_logits<NT, TOKENS>), dim3((steps + own - 1) / own, a.M), dim3(NT), lds, s, a,
                      records, stride, own * STEP, sl);
   return hipGetLastError();
 }
@@ -304,9 +310,13 @@ hipError_t launch_logits(const LogitsArgs& a, void* ws, hipStream_t s) {
   // is read by few (200 x 4096 7.6 and 9.1 us; 64 x 65536 with histories of 4000
   // 12.8 and 27 us; 16 x 65536 8.1 and 8.0 us).
   const int small = (a.V + 2047) / 2048;
-  if ((long long)a.M * small <= 256 || small == 1)
-    return launch_slices<512>(a, records, stride, small, s);
-  return launch_slices<1024>(a, records, stride, a.M < 256 ? 256 / a.M : 1, s);
+  const bool few = (long long)a.M * small <= 256 || small == 1;
+  const int workgroups = few ? small : a.M < 256 ? 256 / a.M : 1;
+  if (a.tokens)
+    return few ? launch_slices<512, true>(a, records, stride, workgroups, s)
+               : launch_slices<1024, true>(a, records, stride, workgroups, s);
+  return few ? launch_slices<512, false>(a, records, stride, workgroups, s)
+             : launch_slices<1024, false>(a, records, stride, workgroups, s);
 }
 
 }  // namespace rq
