@@ -19,8 +19,9 @@
 // row's own power of two, so B t loses nothing above 2^-22 of the row's largest
 // t and cannot overflow for a large x.
 //
-// y goes past the caches both ways (2047 rows of 16384 outputs, rank 64: 83 ->
-// 75 us, 291 MB at 3.9 TB/s).  32 requests of 24 adapters of rank 64 on three
+// A y of many rows goes past the caches both ways, a smaller one stays there for
+// its reader (below).  2047 rows of 16384 outputs, rank 64: 75 us, 291 MB at 3.9
+// TB/s.  32 requests of 24 adapters of rank 64 on three
 // 4096x4096 projections: 25 us, 56 MB, 11 and 13 us of it in the two launches,
 // a third of each the chain ids, offsets, first loads.
 #include <algorithm>
@@ -229,7 +230,7 @@ struct UpShared {
   unsigned char list[ROWS];
 };
 
-template <int KS, int TB, int UT>
+template <int KS, int TB, int UT, bool PAST>  // PAST: y goes past the caches
 __device__ __forceinline__ void up_body(const LoraProblem& p, const LoraArgs& a, const Group& g,
                                         int pi, int base, int n0, int cnt, UpShared<KS, TB, UT>& sh) {
   constexpr int LD = UpShared<KS, TB, UT>::LD, Q = Up<UT>::Q;
@@ -297,7 +298,9 @@ __device__ __forceinline__ void up_body(const LoraProblem& p, const LoraArgs& a,
           y[i][q][w] = f4{0, 0, 0, 0};
           if (!p.y_in || j >= cnt) continue;
           if (nw + 4 <= N) {
-            y[i][q][w] = __builtin_nontemporal_load(reinterpret_cast<const f4u*>(src + nw));
+            const f4u* const at = reinterpret_cast<const f4u*>(src + nw);
+            if constexpr (PAST) y[i][q][w] = __builtin_nontemporal_load(at);
+            else y[i][q][w] = *at;
           } else {
 #pragma unroll
             for (int c = 0; c < 3; c++)
@@ -367,7 +370,9 @@ __device__ __forceinline__ void up_body(const LoraProblem& p, const LoraArgs& a,
           const f4 v = y[i][q][w] +
                        *reinterpret_cast<const f4*>(&sh.out[jr * Up<UT>::LD + 256 * w + 4 * lane]);
           if (nw + 4 <= N) {
-            __builtin_nontemporal_store((f4u)v, reinterpret_cast<f4u*>(dst + nw));
+            f4u* const at = reinterpret_cast<f4u*>(dst + nw);
+            if constexpr (PAST) __builtin_nontemporal_store((f4u)v, at);
+            else *at = (f4u)v;
           } else {
 #pragma unroll
             for (int c = 0; c < 3; c++)
@@ -381,7 +386,7 @@ __device__ __forceinline__ void up_body(const LoraProblem& p, const LoraArgs& a,
   }
 }
 
-template <int KS, int TB, int UT>  // KS: enough for the call's largest rank
+template <int KS, int TB, int UT, bool PAST>  // KS: enough for the call's largest rank
 __global__ void __launch_bounds__(64 * UP_WAVES)
 k_lora_up(const LoraBatch bt, const LoraArgs a) {
   __shared__ __align__(16) UpShared<KS, TB, UT> sh;
@@ -399,7 +404,7 @@ k_lora_up(const LoraBatch bt, const LoraArgs a) {
     const int cnt = list_rows(g.rows, sh.list);
     __syncthreads();
     if (g.r != 0) {
-      up_body<KS, TB, UT>(p, a, g, pi, base, n0, cnt, sh);
+      up_body<KS, TB, UT, PAST>(p, a, g, pi, base, n0, cnt, sh);
     } else if (p.y_in != p.y) {  // no adapter: y = y_in
       const int nn = min(Up<UT>::N, N - n0);
       for (int j = wave; j < cnt; j += UP_WAVES) {
@@ -450,12 +455,21 @@ hipError_t launch_lora(const LoraBatch& bt, const LoraArgs& a, hipStream_t s) {
   const bool wide = few && (long long)n * bt.count * groups >= 256 * Up<4>::N;
   const int per = wide ? Up<4>::N : Up<2>::N;
   const dim3 up((n + per - 1) / per, bt.count * blocks, groups);
+  // The next call reads y, so it stays in the caches unless it is much of the
+  // last level's 256 MB (past the caches / through them, 32 requests on r/k/v with
+  // rq_wkv7 as y's reader 39.7 / 37.4 us, 64 52.2 / 48.2; 16384 outputs with a
+  // squared ReLU as the reader: 128 rows 30.3 / 28.9 us, 512 57.6 / 56.5, 1024 94.6
+  // / 95.4, 1400 129 / 133, 2047 190 / 198).
+  size_t y_bytes = 0;
+  for (int i = 0; i < bt.count; i++) y_bytes += (size_t)a.M * bt.p[i].N * sizeof(float);
+  const bool past = y_bytes > (64u << 20);
 #define RQ_LORA_UP(KS)                                                                          \
   do {                                                                                          \
     const dim3 th(64 * UP_WAVES);                                                               \
-    if (wide) hipLaunchKernelGGL((k_lora_up<KS, 1, 4>), up, th, 0, s, bt, a);                   \
-    else if (few) hipLaunchKernelGGL((k_lora_up<KS, 1, 2>), up, th, 0, s, bt, a);               \
-    else hipLaunchKernelGGL((k_lora_up<KS, 4, 2>), up, th, 0, s, bt, a);                        \
+    if (wide) hipLaunchKernelGGL((k_lora_up<KS, 1, 4, false>), up, th, 0, s, bt, a);            \
+    else if (few) hipLaunchKernelGGL((k_lora_up<KS, 1, 2, false>), up, th, 0, s, bt, a);        \
+    else if (past) hipLaunchKernelGGL((k_lora_up<KS, 4, 2, true>), up, th, 0, s, bt, a);        \
+    else hipLaunchKernelGGL((k_lora_up<KS, 4, 2, false>), up, th, 0, s, bt, a);                 \
   } while (0)
   if (few) hipLaunchKernelGGL(k_lora_down<1>, down, dim3(256), 0, s, bt, a);
   else hipLaunchKernelGGL(k_lora_down<4>, down, dim3(256), 0, s, bt, a);
