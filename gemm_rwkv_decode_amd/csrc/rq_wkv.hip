@@ -125,19 +125,21 @@ k_wkv_seq(const WkvArgs a, int below) {
 // binary32.
 //
 // So that 2^-36 is small beside what a result is made of, operands have powers of
-// two of their own: q_t and k_s per token, their largest key to [8, 16), and S, V
-// and U per value row (the recurrence is linear in a row; the k's power goes to V,
-// W_s = 2^e_s v_s, the q's and the row's to y).  A key of q_t or k_s counts to
-// 2^-39 of the token's largest, a state entry to 2^-28 of its row's largest or
-// better; a and b need none while b is at most 256, as what they add to the state
-// is a multiple of the state.  That leaves a value row whose state is small beside
-// its v's.  It is sound as long as the chunk's first v in the row is not (every y
-// and the state then contain it), or every W that is not zero is at least 2^-14.
+// two of their own: r and k per token, their largest key to [8, 16) (before the
+// decays: W below is then as even over the tokens as v and k are, and the products
+// of a q and an earlier k stay within 2^14), and S, W and U per value row (the
+// recurrence is linear in a row; the k's power goes to v, W_s = 2^e_s v_s, the r's
+// and the row's to y).  A key of r or k counts to 2^-32 of the token's largest, a
+// state entry to 2^-26 of its row's largest or better; a and b need none while b is at most 256, as what they add to the
+// state is a multiple of the state.  That leaves a value row whose state is small
+// beside its W.  It is sound as long as the chunk's first W in the row is not (every
+// y and the state then contain it), or every W that is not zero is at least 2^-14.
 // A chunk with any other such row, a larger b, a value that is not finite or an
 // operand of 2^15 or more is done token by token in binary32, and the rows'
-// powers are set anew from the state.  (The powers cost 32 multiplications in a
-// producer and 8 in a state wave a chunk, with the checks 132 -> 136 us for 4096
-// tokens in 16 sequences, 64 heads.)
+// powers are set anew from the state: its largest to [2^7, 2^8), so that it may
+// grow 2^7 and shrink 2^17 times until the next chunk of this kind (12 us).  (The
+// powers cost 32 multiplications in a producer and 8 in a state wave a chunk, with
+// the checks 132 -> 136 us for 4096 tokens in 16 sequences, 64 heads.)
 //
 // The contraction order is free, so operands are laid out for the accumulator:
 // a lane's accumulator f4 covers rows 4 (l / 16) .. + 3 of column l mod 16, and
@@ -164,8 +166,8 @@ k_wkv_seq(const WkvArgs a, int below) {
 constexpr int CH = 16;  // tokens of a chunk
 constexpr float UP = 2048.0f, DOWN = 1.0f / 2048.0f;  // the low part's scale
 constexpr float HUGE_ = 32768.0f, LARGE_B = 256.0f;
-// of a row's state (and first W), and of a W, from where on they are small
-constexpr float SMALL_ROW = 1.0f / 256.0f, SMALL_W = 1.0f / 16384.0f;
+// a row's state and a W are small below these
+constexpr float SMALL_ROW = 1.0f / 1024.0f, SMALL_W = 1.0f / 16384.0f;
 
 // Two-part operands: 4 deep (one accumulator tile) and 8 deep (two).
 struct P4 {
@@ -463,9 +465,15 @@ __device__ __forceinline__ float of_first_group(float m) {
   const u32 c0 = c[0];
   return __builtin_bit_cast(float, c0);
 }
-// The exponent that brings a magnitude to [8, 16) (any for zero, infinities
-// and NaN).
-__device__ __forceinline__ int to_eight(float m) { return 4 - __builtin_amdgcn_frexp_expf(m); }
+// m = max(m, |x|, |y|), of values as loaded (which fmaxf would quieten first)
+__device__ __forceinline__ void take_larger(float& m, float x, float y) {
+  asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(x), "v"(y));
+}
+// The exponent that brings a magnitude to [2^(e-1), 2^e) (any for zero,
+// infinities and NaN).
+__device__ __forceinline__ int exponent_to(int e, float m) {
+  return e - __builtin_amdgcn_frexp_expf(m);
+}
 __device__ __forceinline__ f4 scaled(const f4& x, int e) {
   return f4{ldexpf(x[0], e), ldexpf(x[1], e), ldexpf(x[2], e), ldexpf(x[3], e)};
 }
@@ -506,7 +514,12 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     f4 av[4], qv[4], bv[4], kv[4], rest[4];  // rest: P_16 / Q
     P[2] = in.decays(2, live(c));
     P[3] = in.decays(3, live(c));
+    float big_r = 0.0f, big_k = 0.0f;
     const auto scale = [&](int j) {
+      take_larger(big_r, (float)in.r[j][0], (float)in.r[j][1]);
+      take_larger(big_r, (float)in.r[j][2], (float)in.r[j][3]);
+      take_larger(big_k, (float)in.k[j][0], (float)in.k[j][1]);
+      take_larger(big_k, (float)in.k[j][2], (float)in.k[j][3]);
 #pragma unroll
       for (int v = 0; v < 4; v++) {
         const float kap = (float)in.kap[j][v], k = (float)in.k[j][v], r = (float)in.r[j][v];
@@ -524,15 +537,13 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       if ((l16 & 7) == 7)
         *reinterpret_cast<f4*>(&decays[c & (RING - 1)].at[l16 >> 3][16 * j + 4 * g]) = P[j];
     };
-    // a token's largest q and k to [8, 16)
-    int up_q, up_k;
+    // a token's largest r and k to [8, 16)
+    int up_r, up_k;
     bool slow;
     const auto even_out = [&] {
-      up_q = to_eight(over_groups(largest(qv)));
-      up_k = to_eight(over_groups(largest(kv)));
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        qv[j] = scaled(qv[j], up_q);
+        qv[j] = scaled(qv[j], up_r);
         kv[j] = scaled(kv[j], up_k);
         pin(qv[j]), pin(kv[j]);
       }
@@ -544,6 +555,8 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       pin(av[j]), pin(qv[j]), pin(bv[j]), pin(kv[j]), pin(rest[j]);
       if (j == 1) half_barrier();
     }
+    up_r = exponent_to(4, over_groups(big_r));
+    up_k = exponent_to(4, over_groups(big_k));
     if constexpr (!SCALE_LATE) even_out();
     // two steps ahead of their use, into the registers that are free by now
     // (the operands are made before, not after; past the end too, as a branch here
@@ -638,7 +651,7 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     o.nb[1][lane] = nbp.lo;
     o.nk[0][lane] = nkp.hi;
     o.nk[1][lane] = nkp.lo;
-    if (lane < 2 * CH) o.exps[lane] = g == 0 ? -up_q : -up_k;
+    if (lane < 2 * CH) o.exps[lane] = g == 0 ? -up_r : -up_k;
     if (lane == 0) o.slow = slow;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
@@ -711,7 +724,7 @@ k_wkv_chunk(const WkvArgs a, int from) {
   // S, W and U of a value row are held times 2^lift, the row's own
   int lift;
   const auto center = [&](float m) {
-    lift = to_eight(over_groups(m));
+    lift = exponent_to(8, over_groups(m));
 #pragma unroll
     for (int j = 0; j < 4; j++) S[j] = scaled(S[j], lift);
   };
@@ -752,7 +765,7 @@ k_wkv_chunk(const WkvArgs a, int from) {
     const float row = over_groups(largest(Sq)), lead = of_first_group(W[0]);
     const u32 least = min(min(order_not_zero(W[0]), order_not_zero(W[1])),
                           min(order_not_zero(W[2]), order_not_zero(W[3])));
-    const bool small = row < SMALL_ROW && fabsf(lead) < SMALL_ROW &&
+    const bool small = row < SMALL_ROW && fabsf(lead) < SMALL_W &&
                        (row > 0.0f || least < order_not_zero(SMALL_W));
     slow = slow || __ballot(small) != 0;
     const P4 vs = split(W);
