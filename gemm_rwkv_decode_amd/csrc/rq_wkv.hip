@@ -482,15 +482,16 @@ __device__ __forceinline__ u32 order_not_zero(float x) {
   return (__builtin_bit_cast(u32, x) << 1) - 1u;
 }
 
-template <typename T, int PRODUCERS>
+// SCALE_LATE: the scaling of q and k goes to segment 2, as segment 1 is else the
+// longest of three (1531 ragged tokens, 40 heads, binary16 62.8 -> 59.9 us; 256
+// tokens, 64 heads, binary32 23.5 -> 22.7).  With four state waves on the same
+// SIMDs only conversions make it so (in binary32 63.0 -> 63.7 us; 4096 tokens of 16
+// sequences, 64 heads 135.8 -> 138.4).
+template <typename T, int PRODUCERS, bool SCALE_LATE>
 __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDecays* decays,
                                         int p, int lo, int hi, size_t base, size_t ld) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int n = (hi - lo + CH - 1) / CH;
-  // Segment 1 is the longest of three with binary16 inputs (conversions): there
-  // the scaling of q and k goes to segment 2 (1531 ragged tokens, 40 heads 62.8 ->
-  // 59.6 us; in binary32 62.8 and 63.4).
-  constexpr bool SCALE_LATE = PRODUCERS == 3 && sizeof(T) == 2;
   ChunkIn<T> in;
   const auto live = [&](int c) { return lo + c * CH + l16 < hi; };
   const u32 at = (u32)((l16 * ld + 4 * g) * sizeof(T));
@@ -541,6 +542,8 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
     int up_r, up_k;
     bool slow;
     const auto even_out = [&] {
+      up_r = exponent_to(4, over_groups(big_r));
+      up_k = exponent_to(4, over_groups(big_k));
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         qv[j] = scaled(qv[j], up_r);
@@ -555,8 +558,6 @@ __device__ __forceinline__ void produce(const WkvArgs& a, ChunkOps* ops, ChunkDe
       pin(av[j]), pin(qv[j]), pin(bv[j]), pin(kv[j]), pin(rest[j]);
       if (j == 1) half_barrier();
     }
-    up_r = exponent_to(4, over_groups(big_r));
-    up_k = exponent_to(4, over_groups(big_k));
     if constexpr (!SCALE_LATE) even_out();
     // two steps ahead of their use, into the registers that are free by now
     // (the operands are made before, not after; past the end too, as a branch here
@@ -688,8 +689,9 @@ k_wkv_chunk(const WkvArgs a, int from) {
     // where a producer shares a SIMD with a state wave, it is the later one (1531
     // ragged tokens, 40 heads: 64 -> 60 us)
     if (PRODUCERS == 3) __builtin_amdgcn_s_setprio(1);
-    produce<T, PRODUCERS>(a, ops, decays, PRODUCERS == 6 ? nth - nth / 4 : nth - NR, lo, hi, base,
-                          ld);
+    constexpr bool LATE = PRODUCERS == 3 && (sizeof(T) == 2 || NR < 4);
+    produce<T, PRODUCERS, LATE>(a, ops, decays, PRODUCERS == 6 ? nth - nth / 4 : nth - NR, lo, hi,
+                                base, ld);
     return;
   }
   const int wave = PRODUCERS == 6 ? nth / 4 : nth;
@@ -885,10 +887,10 @@ void launch_chunks(const WkvArgs& a, unsigned heads, int from, hipStream_t s) {
 // 137 us.
 //
 // At 16 rows a SIMD's second wave is free, and six producers keep up with the
-// state better than three (4096 tokens, 64 heads, binary32 271 / 245 us with
-// three / six), but its chain starts three steps later: binary32 inputs take six
-// past 256 tokens (128 tokens 15.4 / 16.5 us, 256 23.6 / 23.8, 512 39.8 / 38.3).
-// With binary16 inputs three have conversions to do as well, and six always pay.
+// state better than three, but its chain starts three steps later: binary32 inputs
+// take six past 512 tokens (64 heads, three / six: 128 tokens 15.5 / 17.0 us, 512
+// 40.0 / 40.0, 1024 72.8 / 71.0, 4096 256 / 246).  With binary16 inputs three have
+// conversions to do as well, and six always pay.
 template <typename T>
 void launch(const WkvArgs& a, hipStream_t s) {
   const unsigned heads = (unsigned)a.sequences * a.H;
@@ -901,7 +903,7 @@ void launch(const WkvArgs& a, hipStream_t s) {
                        all_short ? a.T + 1 : from);
   if (all_short) return;
   const int least = all_long ? 0 : from;
-  if (heads <= 64 && (sizeof(T) == 2 || a.T > 256))
+  if (heads <= 64 && (sizeof(T) == 2 || a.T > 512))
     launch_chunks<T, 1, 6>(a, heads, least, s);
   else if (heads <= 64)
     launch_chunks<T, 1, 3>(a, heads, least, s);

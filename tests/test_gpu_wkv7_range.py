@@ -133,10 +133,10 @@ def test_small_removal_keys_with_large_rates(H, size):
 @pytest.mark.parametrize("which", ["r", "k", "v", "channel"])
 def test_small_values_in_a_long_sequence(which, half, scale):
     """Long enough for the kernel of long prompts."""
-    ins = inputs(300, 2, 34)
+    ins = inputs(600, 2, 34)
     if which == "channel":
         ins["v"][:, :, [5, 40]] *= scale
     else:
-        ins[which][[0, 150, 299]] *= scale
+        ins[which][[0, 150, 599]] *= scale
     ins = {n: t.to(torch.float16 if half else torch.float32) for n, t in ins.items()}
     compare(ins, start_state(2, 35) * 0, f"long {which} {scale}")
