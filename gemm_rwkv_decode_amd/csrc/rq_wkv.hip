@@ -157,11 +157,11 @@ k_wkv_seq(const WkvArgs a, int below) {
 // producers cut the segments in two.
 //
 // Bound by the chain of chunks where heads are few: a step is as long as a
-// producer's longest segment (2250 cycles) or the state's chain of five dependent
-// products (2100), of which two thirds are instructions issued and the rest
-// their latencies.  One prompt of 4096 tokens, 64 heads: 243 us, 2280 cycles a
-// chunk, 472 MB at 1.9 TB/s.  Bound by the SIMDs' instruction rate where heads
-// are many (4096 tokens in 16 sequences, 64 heads: 131 us).
+// producer's longest segment or the state's chain of five dependent products,
+// most of which are instructions issued and the rest their latencies.  One prompt
+// of 4096 tokens, 64 heads: 243 us, 2280 cycles a chunk, 472 MB at 1.9 TB/s.  Bound
+// by the SIMDs' instruction rate where heads are many (4096 tokens in 16 sequences,
+// 64 heads: 136 us).
 // ---------------------------------------------------------------------------
 constexpr int CH = 16;  // tokens of a chunk
 constexpr float UP = 2048.0f, DOWN = 1.0f / 2048.0f;  // the low part's scale
@@ -863,9 +863,9 @@ void launch_chunks(const WkvArgs& a, unsigned heads, int from, hipStream_t s) {
 }
 
 // Sequences go token by token below a length, in chunks from it on.  Few heads:
-// 8 tokens (token by token / chunks: 64 heads, one sequence of 4 tokens 4.8 / 6.4
-// us, 8 6.5 / 6.4, 16 10.2 / 6.5); many: 16 (1024 heads, sequences of 8 tokens
-// 15 / 24 us, 16 28 / 25; 2048 heads 29 / 47 and 48 / 47 us).
+// 8 tokens (token by token / chunks: 64 heads, one sequence of 4 tokens 4.5 / 6.6
+// us, 8 6.4 / 6.6, 12 8.3 / 6.6); many: 16 (1024 heads, sequences of 8 tokens
+// 18 / 26 us, 16 28 / 27; 2048 heads 28 / 48 and 53 / 52 us).
 //
 // The lengths are on the device.  Where no sequence reaches that length, as all of
 // them have a token, or all together have not as many, all go token by token
@@ -873,18 +873,18 @@ void launch_chunks(const WkvArgs& a, unsigned heads, int from, hipStream_t s) {
 // 255 tokens in one of 256 slots, 64 heads 151 -> 43 us; a second launch for every batch
 // of single tokens would cost it 2 to 6 us).  Where sequences have on average more
 // than 12 tokens beyond their first, all go in chunks; between the two each kind
-// has a launch of its own, which passes over the other's sequences (chunks only / both: 64
-// heads, 31 single tokens beside one sequence of 48 49 / 22 us, of 500 56 / 61; 16
-// sequences of 8 24 / 18, of 16 25 / 27).
+// has a launch of its own, which passes over the other's sequences (chunks only /
+// both: 64 heads, 31 single tokens before one sequence of 48 52 / 26 us, of 500 93 /
+// 70 but behind it 61 / 67; 16 sequences of 8 26 / 20, of 16 27 / 29).
 //
 // A workgroup of the chunk kernel takes 16, 32 or 64 of a head's value rows.
 // Fewer rows make a chunk's step shorter (a state wave then has a SIMD to
 // itself), but the producers' work is done again by each of a head's
 // workgroups, which pays while there is a compute unit for each of these 4 or 2
-// workgroups.  Binary32, 16 / 32 / 64 rows: one prompt of 4096 tokens, 64 heads
-// 264 / 324 / 350 us; of 1000 tokens, 72 heads 104 / 83 / 90, 128 heads 112 / 88 /
-// 91, 160 heads 164 / 163 / 95; 4096 tokens in 16 sequences, 64 heads 253 / 200 /
-// 137 us.
+// workgroups.  Binary32, 16 / 32 / 64 rows on one card: one prompt of 4096 tokens, 64
+// heads 267 / 342 / 365 us, of 256 23.1 / 27.4 / 29.5; of 1000 tokens, 72 heads 134 /
+// 90 / 96, 128 heads 135 / 92 / 96, 160 heads 200 / 177 / 102; 4096 tokens in 16
+// sequences, 64 heads 354 / 210 / 130.
 //
 // At 16 rows a SIMD's second wave is free, and six producers keep up with the
 // state better than three, but its chain starts three steps later: binary32 inputs
