@@ -304,11 +304,11 @@ hipError_t launch_logits(const LogitsArgs& a, void* ws, hipStream_t s) {
   int stride = 2 * LOGITS_MAX_M;  // in 8 bytes
   for (int m = 1; m < a.M; m *= 2) stride /= 2;
   // Workgroups of 512 threads and 2048 tokens while that makes no more than one
-  // for each compute unit (1 x 65536 5.3 us, in slices of 8192 7.0; 8 x 65536 7.3
-  // and 8.3), or where a row has no more tokens (4000 x 2000 44 and 84 us).  Else
-  // 1024 threads, and as many workgroups as compute units or rows: the history
-  // is read by few (200 x 4096 7.6 and 9.1 us; 64 x 65536 with histories of 4000
-  // 12.8 and 27 us; 16 x 65536 8.1 and 8.0 us).
+  // for each compute unit, or where a row has no more tokens; else 1024 threads, and
+  // as many workgroups as compute units or rows, so that the history is read by few.
+  // Both ways, tokens wanted: histories of 257 1 x 65536 5.9 / 6.8 us, 8 x 65536 6.3 /
+  // 7.2, 16 x 65536 7.4 / 7.5, 200 x 4096 7.3 / 6.4; of 1000 64 x 65536 24 / 12, of 4000
+  // 28 / 13; of 100 4000 x 2000 37 / 70.
   const int small = (a.V + 2047) / 2048;
   const bool few = (long long)a.M * small <= 256 || small == 1;
   const int workgroups = few ? small : a.M < 256 ? 256 / a.M : 1;

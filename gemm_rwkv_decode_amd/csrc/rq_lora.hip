@@ -22,8 +22,8 @@
 // A y of many rows goes past the caches both ways, a smaller one stays there for
 // its reader (below).  2047 rows of 16384 outputs, rank 64: 75 us, 291 MB at 3.9
 // TB/s.  32 requests of 24 adapters of rank 64 on three
-// 4096x4096 projections: 25 us, 56 MB, 11 and 13 us of it in the two launches,
-// a third of each the chain ids, offsets, first loads.
+// 4096x4096 projections: 25 us, 56 MB (traced apart, the two launches take 11 and
+// 14), a third of each the chain ids, offsets, first loads.
 #include <algorithm>
 
 #include "rq_common.h"
