@@ -1,0 +1,316 @@
+"""Measured cases of the 8-bit floating point path with a scale for each block of
+128: the quantizer of activations (rq_quant_fp8), the product of two block-scaled
+operands (rq_gemm_fp8), and the group norm that stands between the state
+recurrence and the output projection (rq_groupnorm).
+
+A case names one operator and its sizes.  ``run`` makes one pass, either in
+plain torch operations (``own`` false) or through the package's entry points
+(``own`` true).  Widths, head counts and the vocabulary are those of this
+repository's workloads (gemm_rwkv_decode_amd/synth.py); the rest are generic.
+
+8-bit values come back as the E4M3 numbers they are, their scales beside them
+(binary32, or E8M0, the 8-bit powers of two).
+"""
+import math
+
+import torch
+
+own = False
+
+BLOCK = 128          # values that share a scale
+HEAD = 64            # channels of a head
+VOCAB = 65536        # rows of the vocabulary head
+EPS = 64e-5          # of the group norm
+TOP = 448.0          # the largest E4M3 number
+LEAST = -126         # the exponent of the smallest scale
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+# --------------------------------------------------------------------------
+# cases
+# --------------------------------------------------------------------------
+def listed():
+    return [
+        # one token's row of the smallest model
+        {"name": "quant 1 token", "op": "quant", "M": 1, "K": 768, "half": True, "relu2": False,
+         "e8m0": True},
+        # receptance, key and value inputs of a ragged batch of prompts, one after another
+        {"name": "quant mixes", "op": "quant", "M": 4593, "K": 2560, "half": True, "relu2": False,
+         "e8m0": False},
+        # an FFN key's binary32 outputs (adapters added) on the way to the FFN value
+        {"name": "quant FFN", "op": "quant", "M": 2047, "K": 16384, "half": False, "relu2": True,
+         "e8m0": True},
+        # one token, the smallest matrix
+        {"name": "product 1 token 768", "op": "product", "M": 1, "N": 768, "K": 768, "count": 1,
+         "e8m0": True, "residual": False, "relu2": False},
+        # receptance, key and value of one token of the largest model: the weights are the traffic
+        {"name": "products rkv 1 token", "op": "product", "M": 1, "N": 4096, "K": 4096, "count": 3,
+         "e8m0": False, "residual": False, "relu2": False},
+        # a decode batch on an FFN value, added to the residual stream: few, long rows
+        {"name": "product 32 FFN value", "op": "product", "M": 32, "N": 4096, "K": 16384,
+         "count": 1, "e8m0": True, "residual": True, "relu2": False},
+        # the vocabulary head of a decode batch, an odd number of rows
+        {"name": "product 61 head", "op": "product", "M": 61, "N": VOCAB - 7, "K": 2048,
+         "count": 1, "e8m0": False, "residual": False, "relu2": False},
+        # a few short prompts on an FFN value
+        {"name": "product 203 FFN value", "op": "product", "M": 203, "N": 2560, "K": 10240,
+         "count": 1, "e8m0": False, "residual": True, "relu2": False},
+        # a long ragged batch of prompts on receptance, key and value
+        {"name": "products rkv prompts", "op": "product", "M": 4001, "N": 2560, "K": 2560,
+         "count": 3, "e8m0": False, "residual": False, "relu2": False},
+        # prompts on an FFN key, activated and quantized for the FFN value behind it
+        {"name": "product FFN key relu2", "op": "product", "M": 2047, "N": 16384, "K": 4096,
+         "count": 1, "e8m0": True, "residual": False, "relu2": True},
+        # one token of the smallest model
+        {"name": "norm 1 token", "op": "norm", "T": 1, "H": 12, "half": False, "gate": True,
+         "bonus": True, "silu": False, "out": "f16"},
+        # prompts of the largest model, quantized for the output projection
+        {"name": "norm prompts", "op": "norm", "T": 4001, "H": 64, "half": False, "gate": True,
+         "bonus": True, "silu": False, "out": "e4m3"},
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(("quant", "product", "product", "norm"))
+    if op == "quant":
+        k = BLOCK * _log(rng, 6, 128)
+        return {"op": op, "M": _log(rng, 1, min(4593, 33e6 / k)), "K": k,
+                "half": rng.random() < 0.5, "relu2": rng.random() < 0.4,
+                "e8m0": rng.random() < 0.5}
+    if op == "product":
+        relu2 = rng.random() < 0.3
+        count = 1 if relu2 else rng.choice((1, 1, 3))
+        n, k = BLOCK * _log(rng, 6, 64), BLOCK * _log(rng, 6, 64)
+        if count == 1:
+            n, k = rng.choice(((n, k), (2 * n, k), (n, 2 * k)))
+        if not relu2:
+            n -= rng.choice((0, 0, 0, 5, 64))
+        m = _log(rng, 1, min(4001, 270e9 / (2 * n * k * count)))
+        return {"op": op, "M": m, "N": n, "K": k, "count": count,
+                "e8m0": relu2 or rng.random() < 0.5,
+                "residual": not relu2 and rng.random() < 0.4, "relu2": relu2}
+    h, out = rng.randint(12, 64), rng.choice(("f16", "f32", "e4m3"))
+    return {"op": op, "T": _log(rng, 1, 4001), "H": h // 2 * 2 if out == "e4m3" else h,
+            "half": rng.random() < 0.3, "gate": rng.random() < 0.8, "bonus": rng.random() < 0.8,
+            "silu": rng.random() < 0.3, "out": out}
+
+
+def work(case):
+    op = case["op"]
+    sb = 1 if case.get("e8m0", True) else 4
+    if op == "quant":
+        m, k = case["M"], case["K"]
+        return {"bytes": m * k * (2 if case["half"] else 4) + m * k + m * (k // BLOCK) * sb,
+                "flops": 3 * m * k}
+    if op == "product":
+        m, n, k, c = case["M"], case["N"], case["K"], case["count"]
+        kb, nb = k // BLOCK, (n + BLOCK - 1) // BLOCK
+        out = m * n + m * nb if case["relu2"] else m * n * (8 if case["residual"] else 4)
+        return {"bytes": c * (n * k + m * k + sb * kb * (nb + m) + out),
+                "flops": 2 * c * m * n * k}
+    t, ch = case["T"], case["H"] * HEAD
+    e = 2 if case["half"] else 4
+    each = 4 + e * (3 * case["bonus"] + case["gate"]) + {"f16": 2, "f32": 4, "e4m3": 1}[case["out"]]
+    scales = t * ch // BLOCK if case["out"] == "e4m3" else 0
+    return {"bytes": t * ch * each + scales + 4 * ch * (2 + case["bonus"]), "flops": 14 * t * ch}
+
+
+# --------------------------------------------------------------------------
+# inputs
+# --------------------------------------------------------------------------
+def _rows(shape, g, half=False):
+    """Activations: normal, with a few massive channels that hold most of the energy."""
+    x = torch.randn(shape, generator=g, device="cuda")
+    x[:, torch.randint(shape[1], (4,), generator=g, device="cuda")] *= 30.0
+    return x.half() if half else x
+
+
+def _weights(n, k, e8m0, g):
+    """A matrix in E4M3 with a scale for each block of 128 x 128."""
+    nb = (n + BLOCK - 1) // BLOCK
+    w = torch.randn((nb * BLOCK, k), generator=g, device="cuda") * k ** -0.5
+    w *= torch.exp(0.5 * torch.randn((nb * BLOCK, 1), generator=g, device="cuda"))
+    v = w.view(nb, BLOCK, k // BLOCK, BLOCK)
+    s = v.abs().amax((1, 3)) / TOP
+    if e8m0:
+        s = torch.exp2(torch.ceil(torch.log2(s)))
+    codes = (v / s[:, None, :, None]).clamp(-TOP, TOP).to(E4M3).view(nb * BLOCK, k)[:n]
+    return codes.contiguous(), s.to(E8M0) if e8m0 else s
+
+
+def prepare(case, seed):
+    dev = "cuda"
+    g = torch.Generator(device=dev).manual_seed(seed)
+    op = case["op"]
+    scale_type = E8M0 if case.get("e8m0", True) else torch.float32
+    s = {"case": case}
+
+    def blocks(m, k):  # room for E4M3 rows and their scales
+        return (torch.empty((m, k), dtype=E4M3, device=dev),
+                torch.empty((m, k // BLOCK), dtype=scale_type, device=dev))
+
+    if op == "quant":
+        s["x"] = _rows((case["M"], case["K"]), g, case["half"])
+        s["out"] = blocks(case["M"], case["K"])
+    elif op == "product":
+        m, n, k = case["M"], case["N"], case["K"]
+        s["problems"] = []
+        for _ in range(case["count"]):
+            w, ws = _weights(n, k, case["e8m0"], g)
+            x, xs = _blocks(_rows((m, k), g), scale_type)
+            y_in = torch.randn((m, n), generator=g, device=dev) if case["residual"] else None
+            y = blocks(m, n) if case["relu2"] else torch.empty((m, n), device=dev)
+            s["problems"].append((w, ws, x, xs, y_in, y, n, k))
+    else:
+        t, ch = case["T"], case["H"] * HEAD
+        dt = torch.float16 if case["half"] else torch.float32
+
+        def randn(*shape):
+            return torch.randn(shape, generator=g, device=dev)
+        # the recurrence's outputs: heads of different sizes
+        s["y"] = (randn(t, case["H"], HEAD) * torch.exp(randn(t, case["H"], 1))).view(t, ch)
+        s["weight"], s["bias"] = 1 + 0.1 * randn(ch), 0.1 * randn(ch)
+        s["bonus"] = s["gate"] = None
+        if case["bonus"]:
+            s["bonus"] = (randn(t, ch).to(dt), randn(t, ch).to(dt), 0.1 * randn(ch),
+                          randn(t, ch).to(dt))
+        if case["gate"]:
+            s["gate"] = randn(t, ch).to(dt)
+        if case["out"] == "e4m3":
+            s["out"] = blocks(t, ch)
+        else:
+            s["out"] = torch.empty((t, ch), device=dev,
+                                   dtype=torch.float16 if case["out"] == "f16" else torch.float32)
+    if own:
+        s["call"] = _call(s)
+    return s
+
+
+def _call(s):
+    """The prepared call that a step loop keeps."""
+    import gemm_rwkv_decode_amd as rq
+    case = s["case"]
+    if case["op"] == "quant":
+        return rq.prepare("rq_quant_fp8", s["x"], *s["out"],
+                          act=rq.RQ_ACT_RELU2 if case["relu2"] else rq.RQ_ACT_NONE)
+    if case["op"] == "product":
+        return rq.prepare("rq_gemm_fp8", s["problems"])
+    return rq.prepare("rq_groupnorm", s["y"], case["H"], s["weight"], s["bias"], EPS, s["out"],
+                      bonus=s["bonus"], gate=s["gate"],
+                      act=rq.RQ_ACT_SILU if case["silu"] else rq.RQ_ACT_NONE)
+
+
+# --------------------------------------------------------------------------
+# one pass
+# --------------------------------------------------------------------------
+def run(s):
+    op = s["case"]["op"]
+    if own:
+        s["call"]()
+        return [p[5] for p in s["problems"]] if op == "product" else s["out"]
+    if op == "quant":
+        x = s["x"].float()
+        if s["case"]["relu2"]:
+            x = torch.relu(x).square()
+        return _blocks(x, s["out"][1].dtype)
+    if op == "product":
+        return [_product(s["case"], *p[:5]) for p in s["problems"]]
+    return _norm(s)
+
+
+def _blocks(x, scale_type):
+    """(E4M3 numbers, scales) of float32 rows: a block's scale is the smallest
+    power of two s >= 2^-126 that has no finite value of the block past 448 s;
+    numbers are x / s to the nearest, NaN where x is not finite."""
+    v = x.view(x.shape[0], -1, BLOCK)
+    fine = v.isfinite()
+    m, e = torch.frexp(torch.where(fine, v.abs(), 0.0).amax(-1))  # m in [0.5, 1); 448 = 0.875 * 2^9
+    e = (e - 8 - (m <= TOP / 512).int()).clamp(min=LEAST)
+    q = torch.where(fine, torch.ldexp(v, -e[..., None]), float("nan")).to(E4M3)
+    return q.view(x.shape), torch.ldexp(torch.ones_like(m), e).to(scale_type)
+
+
+def _product(case, w, ws, x, xs, y_in):
+    n, k = w.shape
+    wf = w.float() * ws.float().repeat_interleave(BLOCK, 0)[:n].repeat_interleave(BLOCK, 1)
+    xf = x.float() * xs.float().repeat_interleave(BLOCK, 1)
+    y = xf @ wf.T
+    if y_in is not None:
+        y = y_in + y
+    return _blocks(torch.relu(y).square(), xs.dtype) if case["relu2"] else y
+
+
+def _norm(s):
+    case = s["case"]
+    shape = (case["T"], case["H"], HEAD)
+    y = s["y"].view(shape)
+    y = y - y.mean(-1, keepdim=True)
+    y = y * torch.rsqrt(y.square().mean(-1, keepdim=True) + EPS)
+    z = y.view(case["T"], -1) * s["weight"] + s["bias"]
+    if s["bonus"] is not None:
+        r, k, r_k, v = s["bonus"]
+        dot = (r.float() * k.float() * r_k).view(shape).sum(-1, keepdim=True)
+        z = z + (dot * v.float().view(shape)).view(z.shape)
+    if s["gate"] is not None:
+        gate = s["gate"].float()
+        z = z * (gate * torch.sigmoid(gate) if case["silu"] else gate)
+    return _blocks(z, E8M0) if case["out"] == "e4m3" else z.to(s["out"].dtype)
+
+
+# --------------------------------------------------------------------------
+# the definitions in 64 bits
+# --------------------------------------------------------------------------
+def _exact_blocks(a):
+    """[E4M3 values, scales] of float64 rows, from the definition."""
+    parts = a.unflatten(1, (-1, BLOCK))
+    big = parts.abs().amax(2, keepdim=True).clamp(min=2.0 ** -150)
+    power = torch.ceil(torch.log2(big / TOP))
+    power = torch.where(big <= TOP * torch.exp2(power - 1), power - 1, power)  # log2's last bit
+    power = torch.where(big > TOP * torch.exp2(power), power + 1, power).clamp(min=float(LEAST))
+    scale = torch.exp2(power)
+    u = parts / scale
+    # the spacing of E4M3 around u: eight numbers to a power of two, from 2^-6 down evenly
+    step = torch.exp2(torch.floor(torch.log2(u.abs().clamp(min=2.0 ** -6))) - 3)
+    return [(torch.round(u / step) * step).flatten(1), scale[..., 0]]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    f8 = torch.float64
+    if case["op"] == "quant":
+        a = s["x"].to(f8)
+        if case["relu2"]:  # the square is a binary32 number
+            a = (a * a * (a > 0)).to(torch.float32).to(f8)
+        return _exact_blocks(a)
+    if case["op"] == "product":
+        out = []
+        for w, ws, x, xs, y_in, _, n, k in s["problems"]:
+            y = torch.zeros((case["M"], n), dtype=f8, device="cuda")
+            if y_in is not None:
+                y += y_in
+            wd = w.to(torch.float32).to(f8)
+            for b in range(-(-n // BLOCK)):
+                rows = slice(b * BLOCK, min(n, (b + 1) * BLOCK))
+                wd[rows].view(-1, k // BLOCK, BLOCK).mul_(ws[b].to(torch.float32).to(f8)[:, None])
+            xd = x.to(torch.float32).to(f8).unflatten(1, (-1, BLOCK))
+            xd = (xd * xs.to(torch.float32).to(f8)[..., None]).flatten(1)
+            y += torch.mm(wd, xd.T.contiguous()).T
+            out.append(_exact_blocks(y * y * (y > 0)) if case["relu2"] else y)
+        return out
+    heads = (case["T"], case["H"], HEAD)
+    y = s["y"].to(f8).view(heads)
+    var, mean = torch.var_mean(y, 2, correction=0, keepdim=True)
+    z = (y - mean) / torch.sqrt(var + EPS)
+    z = z * s["weight"].to(f8).view(heads[1:]) + s["bias"].to(f8).view(heads[1:])
+    if s["bonus"] is not None:
+        r, k, r_k, v = (c.to(f8).view(-1, *heads[1:]) for c in s["bonus"])
+        z = z + (r * k * r_k).sum(2, keepdim=True) * v
+    z = z.view(case["T"], -1)
+    if s["gate"] is not None:
+        gate = s["gate"].to(f8)
+        z = z * (gate / (1 + torch.exp(-gate)) if case["silu"] else gate)
+    return _exact_blocks(z) if case["out"] == "e4m3" else z
