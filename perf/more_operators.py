@@ -9,7 +9,9 @@ plain torch operations (``own`` false) or through the package's entry points
 repository's workloads (gemm_rwkv_decode_amd/synth.py); the rest are generic.
 
 8-bit values come back as the E4M3 numbers they are, their scales beside them
-(binary32, or E8M0, the 8-bit powers of two).
+(binary32, or E8M0, the 8-bit powers of two).  What a product or the norm
+quantizes is its binary16 output, so the call is the same as the two calls one
+after the other; ``exact`` leaves that rounding out.
 """
 import math
 
@@ -42,25 +44,25 @@ def listed():
          "e8m0": True},
         # one token, the smallest matrix
         {"name": "product 1 token 768", "op": "product", "M": 1, "N": 768, "K": 768, "count": 1,
-         "e8m0": True, "residual": False, "relu2": False},
+         "e8m0": True, "residual": False, "out": "f32"},
         # receptance, key and value of one token of the largest model: the weights are the traffic
         {"name": "products rkv 1 token", "op": "product", "M": 1, "N": 4096, "K": 4096, "count": 3,
-         "e8m0": False, "residual": False, "relu2": False},
+         "e8m0": False, "residual": False, "out": "f32"},
         # a decode batch on an FFN value, added to the residual stream: few, long rows
         {"name": "product 32 FFN value", "op": "product", "M": 32, "N": 4096, "K": 16384,
-         "count": 1, "e8m0": True, "residual": True, "relu2": False},
+         "count": 1, "e8m0": True, "residual": True, "out": "f32"},
         # the vocabulary head of a decode batch, an odd number of rows
         {"name": "product 61 head", "op": "product", "M": 61, "N": VOCAB - 7, "K": 2048,
-         "count": 1, "e8m0": False, "residual": False, "relu2": False},
+         "count": 1, "e8m0": False, "residual": False, "out": "f32"},
         # a few short prompts on an FFN value
         {"name": "product 203 FFN value", "op": "product", "M": 203, "N": 2560, "K": 10240,
-         "count": 1, "e8m0": False, "residual": True, "relu2": False},
-        # a long ragged batch of prompts on receptance, key and value
+         "count": 1, "e8m0": False, "residual": True, "out": "f32"},
+        # a long ragged batch of prompts on receptance, key and value, for a recurrence in binary16
         {"name": "products rkv prompts", "op": "product", "M": 4001, "N": 2560, "K": 2560,
-         "count": 3, "e8m0": False, "residual": False, "relu2": False},
-        # prompts on an FFN key, activated and quantized for the FFN value behind it
-        {"name": "product FFN key relu2", "op": "product", "M": 2047, "N": 16384, "K": 4096,
-         "count": 1, "e8m0": True, "residual": False, "relu2": True},
+         "count": 3, "e8m0": False, "residual": False, "out": "f16"},
+        # prompts on an FFN key, squared above zero and quantized for the FFN value behind it
+        {"name": "product FFN key e4m3", "op": "product", "M": 2047, "N": 16384, "K": 4096,
+         "count": 1, "e8m0": True, "residual": False, "out": "e4m3"},
         # one token of the smallest model
         {"name": "norm 1 token", "op": "norm", "T": 1, "H": 12, "half": False, "gate": True,
          "bonus": True, "silu": False, "out": "f16"},
@@ -82,17 +84,17 @@ def draw(rng):
                 "half": rng.random() < 0.5, "relu2": rng.random() < 0.4,
                 "e8m0": rng.random() < 0.5}
     if op == "product":
-        relu2 = rng.random() < 0.3
-        count = 1 if relu2 else rng.choice((1, 1, 3))
+        out = rng.choice(("f32", "f16", "e4m3"))
+        count = 1 if out == "e4m3" else rng.choice((1, 1, 3))
         n, k = BLOCK * _log(rng, 6, 64), BLOCK * _log(rng, 6, 64)
         if count == 1:
             n, k = rng.choice(((n, k), (2 * n, k), (n, 2 * k)))
-        if not relu2:
+        if out != "e4m3":
             n -= rng.choice((0, 0, 0, 5, 64))
         m = _log(rng, 1, min(4001, 270e9 / (2 * n * k * count)))
         return {"op": op, "M": m, "N": n, "K": k, "count": count,
-                "e8m0": relu2 or rng.random() < 0.5,
-                "residual": not relu2 and rng.random() < 0.4, "relu2": relu2}
+                "e8m0": out == "e4m3" or rng.random() < 0.5,
+                "residual": out == "f32" and rng.random() < 0.5, "out": out}
     h, out = rng.randint(12, 64), rng.choice(("f16", "f32", "e4m3"))
     return {"op": op, "T": _log(rng, 1, 4001), "H": h // 2 * 2 if out == "e4m3" else h,
             "half": rng.random() < 0.3, "gate": rng.random() < 0.8, "bonus": rng.random() < 0.8,
@@ -109,7 +111,8 @@ def work(case):
     if op == "product":
         m, n, k, c = case["M"], case["N"], case["K"], case["count"]
         kb, nb = k // BLOCK, (n + BLOCK - 1) // BLOCK
-        out = m * n + m * nb if case["relu2"] else m * n * (8 if case["residual"] else 4)
+        out = m * n * {"f16": 2, "f32": 8 if case["residual"] else 4, "e4m3": 1}[case["out"]]
+        out += m * nb if case["out"] == "e4m3" else 0
         return {"bytes": c * (n * k + m * k + sb * kb * (nb + m) + out),
                 "flops": 2 * c * m * n * k}
     t, ch = case["T"], case["H"] * HEAD
@@ -153,6 +156,12 @@ def prepare(case, seed):
         return (torch.empty((m, k), dtype=E4M3, device=dev),
                 torch.empty((m, k // BLOCK), dtype=scale_type, device=dev))
 
+    def output(m, n):
+        if case["out"] == "e4m3":
+            return blocks(m, n)
+        return torch.empty((m, n), device=dev,
+                           dtype=torch.float16 if case["out"] == "f16" else torch.float32)
+
     if op == "quant":
         s["x"] = _rows((case["M"], case["K"]), g, case["half"])
         s["out"] = blocks(case["M"], case["K"])
@@ -163,8 +172,7 @@ def prepare(case, seed):
             w, ws = _weights(n, k, case["e8m0"], g)
             x, xs = _blocks(_rows((m, k), g), scale_type)
             y_in = torch.randn((m, n), generator=g, device=dev) if case["residual"] else None
-            y = blocks(m, n) if case["relu2"] else torch.empty((m, n), device=dev)
-            s["problems"].append((w, ws, x, xs, y_in, y, n, k))
+            s["problems"].append((w, ws, x, xs, y_in, output(m, n), n, k))
     else:
         t, ch = case["T"], case["H"] * HEAD
         dt = torch.float16 if case["half"] else torch.float32
@@ -180,11 +188,7 @@ def prepare(case, seed):
                           randn(t, ch).to(dt))
         if case["gate"]:
             s["gate"] = randn(t, ch).to(dt)
-        if case["out"] == "e4m3":
-            s["out"] = blocks(t, ch)
-        else:
-            s["out"] = torch.empty((t, ch), device=dev,
-                                   dtype=torch.float16 if case["out"] == "f16" else torch.float32)
+        s["out"] = output(t, ch)
     if own:
         s["call"] = _call(s)
     return s
@@ -241,7 +245,10 @@ def _product(case, w, ws, x, xs, y_in):
     y = xf @ wf.T
     if y_in is not None:
         y = y_in + y
-    return _blocks(torch.relu(y).square(), xs.dtype) if case["relu2"] else y
+    if case["out"] == "f32":
+        return y
+    y = y.half()
+    return y if case["out"] == "f16" else _blocks(torch.relu(y.float()).square(), xs.dtype)
 
 
 def _norm(s):
@@ -258,7 +265,10 @@ def _norm(s):
     if s["gate"] is not None:
         gate = s["gate"].float()
         z = z * (gate * torch.sigmoid(gate) if case["silu"] else gate)
-    return _blocks(z, E8M0) if case["out"] == "e4m3" else z.to(s["out"].dtype)
+    if case["out"] == "f32":
+        return z
+    z = z.half()
+    return z if case["out"] == "f16" else _blocks(z.float(), E8M0)  # as the two calls
 
 
 # --------------------------------------------------------------------------
@@ -299,7 +309,7 @@ def exact(case, seed):
             xd = x.to(torch.float32).to(f8).unflatten(1, (-1, BLOCK))
             xd = (xd * xs.to(torch.float32).to(f8)[..., None]).flatten(1)
             y += torch.mm(wd, xd.T.contiguous()).T
-            out.append(_exact_blocks(y * y * (y > 0)) if case["relu2"] else y)
+            out.append(_exact_blocks(y * y * (y > 0)) if case["out"] == "e4m3" else y)
         return out
     heads = (case["T"], case["H"], HEAD)
     y = s["y"].to(f8).view(heads)
