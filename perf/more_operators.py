@@ -202,7 +202,8 @@ def _call(s):
         return rq.prepare("rq_quant_fp8", s["x"], *s["out"],
                           act=rq.RQ_ACT_RELU2 if case["relu2"] else rq.RQ_ACT_NONE)
     if case["op"] == "product":
-        return rq.prepare("rq_gemm_fp8", s["problems"])
+        return rq.prepare("rq_gemm_fp8", s["problems"],
+                          act=rq.RQ_ACT_RELU2 if case["out"] == "e4m3" else rq.RQ_ACT_NONE)
     return rq.prepare("rq_groupnorm", s["y"], case["H"], s["weight"], s["bias"], EPS, s["out"],
                       bonus=s["bonus"], gate=s["gate"],
                       act=rq.RQ_ACT_SILU if case["silu"] else rq.RQ_ACT_NONE)
