@@ -14,9 +14,11 @@ Tensors are torch tensors on the GPU, contiguous:
   records (asymmetric);
 * ``x``: float16 ``[M][K]``; ``y``: float32 ``[M][N]``.
 
-Around the products (``rq_shift``, ``rq_lora``, ``rq_wkv7``, ``rq_logits``) sizes
-are read from the tensors, whose types and shapes are checked here; index
-tensors are int32 on the GPU.
+Around the products (``rq_shift``, ``rq_lora``, ``rq_wkv7``, ``rq_logits``,
+``rq_groupnorm``) sizes are read from the tensors, whose types and shapes are
+checked here; index tensors are int32 on the GPU.  So are those of the
+block-scaled FP8 calls (``rq_quant_fp8``, ``rq_gemm_fp8``): E4M3 values are
+float8_e4m3fn or uint8 tensors, scales float32, float8_e8m0fnu or uint8 (E8M0).
 
 Work is enqueued on torch's current stream (or the ``stream`` given).
 """
@@ -30,7 +32,8 @@ __all__ = [
     "RQ_MAX_M", "RQ_MAX_BATCH", "RqError", "RqLibraryMissing", "rq_dequant", "rq_gemv",
     "rq_gemv_batched", "rq_gemm_smallm", "rq_gemm_smallm_ws", "rq_gemm_smallm_workspace_size",
     "rq_gemm_smallm_noalloc", "rq_shift", "rq_lora", "rq_lora_workspace_size", "rq_wkv7",
-    "rq_logits", "rq_status_string", "rq_version", "prepare", "gemm_workspace",
+    "rq_logits", "rq_quant_fp8", "rq_gemm_fp8", "rq_gemm_fp8_workspace_size", "rq_groupnorm",
+    "RQ_ACT_NONE", "RQ_ACT_RELU2", "RQ_ACT_SILU", "rq_status_string", "rq_version", "prepare", "gemm_workspace",
     "lib", "LIB_PATH",
 ]
 
@@ -47,7 +50,11 @@ RQ_MAX_SEQUENCES = 65536
 RQ_MAX_TOKENS = 1 << 24
 RQ_SHIFT_MAX_MIXES = 8
 RQ_WKV_HEAD = 64
-RQ_TYPE_F32, RQ_TYPE_F16 = 0, 1
+RQ_TYPE_F32, RQ_TYPE_F16, RQ_TYPE_E4M3 = 0, 1, 2
+RQ_SCALE_F32, RQ_SCALE_E8M0 = 0, 1
+RQ_ACT_NONE, RQ_ACT_RELU2, RQ_ACT_SILU = 0, 1, 2
+RQ_FP8_BLOCK, RQ_FP8_MAX_K, RQ_FP8_MAX_BATCH = 128, 1 << 22, 8
+RQ_FP8_MAX_VALUES = 1 << 34
 RQ_LORA_MAX_M, RQ_LORA_MAX_RANK, RQ_LORA_MAX_BATCH = 8192, 128, 8
 RQ_LOGITS_MAX_M = 4096
 RQ_LOGITS_WORKSPACE_BYTES = 64 << 10
@@ -82,6 +89,22 @@ class RqLogitsArgs(ctypes.Structure):
                 ("bias", ctypes.c_void_p), ("bias_offsets", ctypes.c_void_p),
                 ("bias_len", ctypes.c_int), ("masks", ctypes.c_void_p),
                 ("mask_ids", ctypes.c_void_p), ("nmasks", ctypes.c_int)]
+
+
+class RqFp8Problem(ctypes.Structure):
+    """rq_fp8_problem of include/rq.h."""
+    _fields_ = [("w", ctypes.c_void_p), ("w_scales", ctypes.c_void_p), ("x", ctypes.c_void_p),
+                ("x_scales", ctypes.c_void_p), ("y_in", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("y_scales", ctypes.c_void_p), ("N", ctypes.c_int),
+                ("K", ctypes.c_int)]
+
+
+class RqGroupnormArgs(ctypes.Structure):
+    """rq_groupnorm_args of include/rq.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("y", "weight", "bias", "r", "k", "r_k", "v", "gate",
+                                               "out", "out_scales")] + \
+               [(n, ctypes.c_int) for n in ("input_type", "act", "out_type", "scale_type", "T",
+                                            "C", "groups")] + [("eps", ctypes.c_float)]
 
 
 class RqLibraryMissing(RuntimeError):
@@ -130,6 +153,16 @@ def lib():
             L.rq_lora_workspace_size.restype = i
             L.rq_logits.argtypes = [ctypes.POINTER(RqLogitsArgs), vp, ctypes.c_size_t, vp]
             L.rq_logits.restype = i
+            L.rq_quant_fp8.argtypes = [vp, i, i, vp, vp, i, i, i, vp]
+            L.rq_quant_fp8.restype = i
+            L.rq_gemm_fp8.argtypes = [ctypes.POINTER(RqFp8Problem), i, i, i, i, i, vp,
+                                      ctypes.c_size_t, vp]
+            L.rq_gemm_fp8.restype = i
+            L.rq_gemm_fp8_workspace_size.argtypes = [ctypes.POINTER(RqFp8Problem), i, i, i, i,
+                                                     ctypes.POINTER(ctypes.c_size_t)]
+            L.rq_gemm_fp8_workspace_size.restype = i
+            L.rq_groupnorm.argtypes = [ctypes.POINTER(RqGroupnormArgs), vp]
+            L.rq_groupnorm.restype = i
             L.rq_status_string.argtypes = [i]
             L.rq_status_string.restype = ctypes.c_char_p
             L.rq_version.argtypes = []
@@ -513,8 +546,166 @@ def rq_logits(logits, out, tokens=None, *, history=None, repetition=None, presen
     return out
 
 
+def _float_type(what, t):
+    """RQ_TYPE_F16 or RQ_TYPE_F32 of a tensor."""
+    for name, kind in (("float16", RQ_TYPE_F16), ("float32", RQ_TYPE_F32)):
+        if str(t.dtype) == "torch." + name:
+            return kind
+    raise ValueError(f"{what}: float16 or float32 expected, got {t.dtype}")
+
+
+def _scale_type(what, t):
+    """RQ_SCALE_F32 or RQ_SCALE_E8M0 of a tensor of scales."""
+    name = str(t.dtype)
+    if name == "torch.float32":
+        return RQ_SCALE_F32
+    if name in ("torch.float8_e8m0fnu", "torch.uint8"):
+        return RQ_SCALE_E8M0
+    raise ValueError(f"{what}: float32, float8_e8m0fnu or uint8 expected, got {t.dtype}")
+
+
+def _scales(what, t, kind, shape):
+    """Pointer of a tensor of scales of this kind and shape."""
+    if _scale_type(what, t) != kind:
+        raise ValueError(f"{what}: scales of one type expected")
+    return _typed(what, t, str(t.dtype)[6:], shape)
+
+
+def _e4m3(what, t, shape):
+    """Pointer of a tensor of E4M3 values of this shape."""
+    name = str(t.dtype)[6:]
+    if name not in ("float8_e4m3fn", "uint8"):
+        raise ValueError(f"{what}: float8_e4m3fn or uint8 expected, got {t.dtype}")
+    return _typed(what, t, name, shape)
+
+
+def _blocks_of(what, K):
+    if K % RQ_FP8_BLOCK:
+        raise ValueError(f"{what}: whole blocks of {RQ_FP8_BLOCK} expected, got {K}")
+    return K // RQ_FP8_BLOCK
+
+
+def _quant_fp8_cargs(x, q, scales, *, act=RQ_ACT_NONE, stream=None):
+    M, K = x.shape
+    kind = _scale_type("scales", scales)
+    return (_ptr(x), _float_type("x", x), int(act), _e4m3("q", q, (M, K)),
+            _scales("scales", scales, kind, (M, _blocks_of("x", K))), kind, M, K,
+            _stream(stream, x))
+
+
+def rq_quant_fp8(x, q, scales, act=RQ_ACT_NONE, stream=None):
+    """Rows quantized in blocks of 128: a = act(x) (RQ_ACT_NONE, RQ_ACT_RELU2), a
+    block's scale the smallest power of two s with |a| <= 448 s (2^-126 at
+    least), q the E4M3 number nearest a / s.  x float16 or float32 [M][K], q
+    E4M3 [M][K], scales float32 or E8M0 [M][K / 128]."""
+    st = lib().rq_quant_fp8(*_quant_fp8_cargs(x, q, scales, act=act, stream=stream))
+    if st != RQ_OK:
+        raise RqError("rq_quant_fp8", st)
+    return q, scales
+
+
+def _gemm_fp8_cargs(problems, *, act=RQ_ACT_NONE, stream=None, workspace=AUTO):
+    arr = (RqFp8Problem * len(problems))()
+    M = problems[0][2].shape[0]
+    kind = _scale_type("w_scales", problems[0][1])
+    first = problems[0][5]
+    out = RQ_TYPE_E4M3 if isinstance(first, (tuple, list)) else _float_type("y", first)
+    for i, (w, ws, x, xs, y_in, y, N, K) in enumerate(problems):
+        kb, nb = _blocks_of("w", K), (N + RQ_FP8_BLOCK - 1) // RQ_FP8_BLOCK
+        if isinstance(y, (tuple, list)) != (out == RQ_TYPE_E4M3):
+            raise ValueError("y: outputs of one type expected")
+        if out == RQ_TYPE_E4M3:
+            py = _e4m3("y", y[0], (M, N))
+            ps = _scales("y_scales", y[1], kind, (M, _blocks_of("y", N)))
+        else:
+            py, ps = _typed("y", y, "float16" if out == RQ_TYPE_F16 else "float32", (M, N)), None
+        arr[i] = RqFp8Problem(_e4m3("w", w, (N, K)), _scales("w_scales", ws, kind, (nb, kb)),
+                              _e4m3("x", x, (M, K)), _scales("x_scales", xs, kind, (M, kb)),
+                              _typed("y_in", y_in, "float32", (M, N)), py, ps, int(N), int(K))
+    return (arr, len(problems), M, kind, out, int(act),
+            *_ws_args(workspace, stream, problems[0][2]), _stream(stream, problems[0][2]))
+
+
+def rq_gemm_fp8(problems, act=RQ_ACT_NONE, stream=None, workspace=AUTO):
+    """Products of block-scaled operands, y = y_in + x W^T, in one launch.
+    ``problems`` is a sequence of (w, w_scales, x, x_scales, y_in, y, N, K): w
+    E4M3 [N][K] with scales [(N + 127) // 128][K / 128], x E4M3 [M][K] with
+    scales [M][K / 128], y_in float32 [M][N] (y itself, another tensor, or
+    None), y float32 or float16 [M][N], or a pair (E4M3 [M][N], scales [M][N /
+    128]) for the float16 output quantized as rq_quant_fp8 with ``act`` does.
+    All share M, the type of scales and the type of y.  ``workspace``: AUTO
+    (the binding's, per stream), a tensor of rq_gemm_fp8_workspace_size bytes
+    (zero before its first use), or None to keep K whole."""
+    st = lib().rq_gemm_fp8(*_gemm_fp8_cargs(problems, act=act, stream=stream,
+                                            workspace=workspace))
+    if st != RQ_OK:
+        raise RqError("rq_gemm_fp8", st)
+    return [p[5] for p in problems]
+
+
+def rq_gemm_fp8_workspace_size(shapes, M, scale_type, out_type):
+    """Bytes of workspace rq_gemm_fp8 uses for products of these (N, K).
+    Host-only."""
+    arr = (RqFp8Problem * len(shapes))()
+    for i, (N, K) in enumerate(shapes):
+        arr[i].N, arr[i].K = int(N), int(K)
+    b = ctypes.c_size_t(0)
+    st = lib().rq_gemm_fp8_workspace_size(arr, len(shapes), int(M), int(scale_type),
+                                          int(out_type), ctypes.byref(b))
+    if st != RQ_OK:
+        raise RqError("rq_gemm_fp8_workspace_size", st)
+    return b.value
+
+
+def _groupnorm_cargs(y, groups, weight, bias, eps, out, *, bonus=None, gate=None,
+                     act=RQ_ACT_NONE, stream=None):
+    T, C = y.shape
+    a = RqGroupnormArgs(y=_typed("y", y, "float32", (T, C)),
+                        weight=_typed("weight", weight, "float32", (C,)),
+                        bias=_typed("bias", bias, "float32", (C,)), T=T, C=C, groups=int(groups),
+                        eps=float(eps), act=int(act))
+    like = gate if bonus is None else bonus[0]
+    name = "float32"
+    if like is not None:
+        a.input_type = _float_type("gate" if bonus is None else "r", like)
+        name = "float16" if a.input_type == RQ_TYPE_F16 else "float32"
+    if bonus is not None:
+        r, k, r_k, v = bonus
+        a.r, a.k, a.v = (_typed(n, t, name, (T, C)) for n, t in (("r", r), ("k", k), ("v", v)))
+        a.r_k = _typed("r_k", r_k, "float32", (C,))
+    a.gate = _typed("gate", gate, name, (T, C))
+    if isinstance(out, (tuple, list)):
+        a.out_type = RQ_TYPE_E4M3
+        a.scale_type = _scale_type("out scales", out[1])
+        a.out = _e4m3("out", out[0], (T, C))
+        a.out_scales = _scales("out scales", out[1], a.scale_type, (T, _blocks_of("out", C)))
+    else:
+        a.out_type = _float_type("out", out)
+        a.out = _typed("out", out, str(out.dtype)[6:], (T, C))
+    return ctypes.pointer(a), _stream(stream, y)
+
+
+def rq_groupnorm(y, groups, weight, bias, eps, out, bonus=None, gate=None, act=RQ_ACT_NONE,
+                 stream=None):
+    """Group norm of every token's channels with what follows it in the time
+    mix: out = (norm(y) * weight + bias + sum(r * k * r_k) * v) * act(gate), the
+    norm and the sum over each of ``groups`` groups of 32, 64, 128 or 256
+    channels.  y float32 [T][C]; weight and bias float32 [C] or None; bonus
+    (r, k, r_k, v) or None, r, k, v [T][C] all float32 or all float16, r_k
+    float32 [C]; gate [T][C] of their type or None; act RQ_ACT_NONE or
+    RQ_ACT_SILU; out float32 (y itself too) or float16 [T][C], or a pair (E4M3
+    [T][C], scales [T][C / 128]) for the float16 output as rq_quant_fp8
+    quantizes it."""
+    st = lib().rq_groupnorm(*_groupnorm_cargs(y, groups, weight, bias, eps, out, bonus=bonus,
+                                              gate=gate, act=act, stream=stream))
+    if st != RQ_OK:
+        raise RqError("rq_groupnorm", st)
+    return out
+
+
 _CARGS = {"rq_shift": _shift_cargs, "rq_wkv7": _wkv7_cargs, "rq_lora": _lora_cargs,
-          "rq_logits": _logits_cargs}
+          "rq_logits": _logits_cargs, "rq_quant_fp8": _quant_fp8_cargs,
+          "rq_gemm_fp8": _gemm_fp8_cargs, "rq_groupnorm": _groupnorm_cargs}
 
 
 def prepare(name, *args, stream=None, workspace=AUTO, **options):
@@ -522,13 +713,14 @@ def prepare(name, *args, stream=None, workspace=AUTO, **options):
     repeats it with no per-call argument conversion in Python (for step loops
     and graph capture).  ``name`` is "rq_gemv", "rq_gemm_smallm",
     "rq_gemm_smallm_noalloc", "rq_gemv_batched", "rq_dequant", "rq_shift",
-    "rq_wkv7", "rq_lora" or "rq_logits"; ``args`` (and ``options``, the keyword
-    arguments of rq_logits) are those of the Python function of that name,
-    without ``stream`` (and ``workspace``, which rq_gemm_smallm, rq_lora and
-    rq_logits take as a keyword, resolved now).  The tensors must stay alive."""
+    "rq_wkv7", "rq_lora", "rq_logits", "rq_quant_fp8", "rq_gemm_fp8" or
+    "rq_groupnorm"; ``args`` (and ``options``, the keyword arguments of the last
+    four) are those of the Python function of that name, without ``stream`` (and
+    ``workspace``, which rq_gemm_smallm, rq_lora, rq_logits and rq_gemm_fp8 take
+    as a keyword, resolved now).  The tensors must stay alive."""
     L = lib()
     if name in _CARGS:
-        if name in ("rq_lora", "rq_logits"):
+        if name in ("rq_lora", "rq_logits", "rq_gemm_fp8"):
             options["workspace"] = workspace
         return _prepared(name, getattr(L, name), _CARGS[name](*args, stream=stream, **options))
     if options:

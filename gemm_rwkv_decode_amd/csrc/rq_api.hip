@@ -18,7 +18,10 @@
 static_assert(RQ_SHIFT_MAX_MIXES == rq::SHIFT_MAX_MIXES && RQ_WKV_HEAD == rq::WKV_HEAD &&
               RQ_LORA_MAX_RANK == rq::LORA_MAX_RANK &&
               RQ_LORA_MAX_BATCH == rq::LORA_BATCH && RQ_LOGITS_MAX_M == rq::LOGITS_MAX_M &&
-              RQ_LOGITS_MAX_M * 16 <= RQ_LOGITS_WORKSPACE_BYTES,
+              RQ_LOGITS_MAX_M * 16 <= RQ_LOGITS_WORKSPACE_BYTES &&
+              RQ_FP8_BLOCK == rq::FP8_BLOCK && RQ_FP8_MAX_BATCH == rq::FP8_BATCH &&
+              (int)RQ_TYPE_F32 == rq::OUT_F32 && (int)RQ_TYPE_F16 == rq::OUT_F16 &&
+              (int)RQ_TYPE_E4M3 == rq::OUT_E4M3,
               "the interface's limits are the kernels'");
 
 namespace rq {
@@ -742,6 +745,177 @@ rq_status rq_logits(const rq_logits_args* args, void* workspace, size_t workspac
   return rq::launch_logits(a, workspace, static_cast<hipStream_t>(stream)) == hipSuccess
              ? RQ_OK
              : RQ_ERR_LAUNCH;
+}
+
+// --------------------------------------------------------------------------
+// Block-scaled FP8
+// --------------------------------------------------------------------------
+static Operand scale_array(const void* p, size_t n, int scale_type) {
+  const size_t e = scale_type == RQ_SCALE_F32 ? 4 : 1;
+  return Operand{p, n * e, e};
+}
+static bool fp8_values(size_t rows, size_t columns) {
+  return rows * columns <= (size_t)RQ_FP8_MAX_VALUES;
+}
+static bool fp8_k(int K) { return K >= RQ_FP8_BLOCK && K <= RQ_FP8_MAX_K && K % RQ_FP8_BLOCK == 0; }
+static size_t type_bytes(int type) { return type == RQ_TYPE_F32 ? 4 : (type == RQ_TYPE_F16 ? 2 : 1); }
+
+rq_status rq_quant_fp8(const void* x, int input_type, int act, void* q, void* scales,
+                       int scale_type, int M, int K, void* stream) {
+  if (!x || !q || !scales) return RQ_ERR_NULL;
+  if ((input_type != RQ_TYPE_F32 && input_type != RQ_TYPE_F16) ||
+      (act != RQ_ACT_NONE && act != RQ_ACT_RELU2) ||
+      (scale_type != RQ_SCALE_F32 && scale_type != RQ_SCALE_E8M0))
+    return RQ_ERR_UNSUPPORTED;
+  if (M < 1 || M > RQ_MAX_TOKENS || !fp8_k(K) || !fp8_values(M, K)) return RQ_ERR_SHAPE;
+  const size_t n = (size_t)M * K;
+  const Operand o[] = {array(q, n), scale_array(scales, n / RQ_FP8_BLOCK, scale_type),
+                       array(x, n * type_bytes(input_type))};
+  rq_status st = check_align(o, 3);
+  if (st == RQ_OK) st = check_apart(o[0], o + 1, 2);
+  if (st == RQ_OK) st = check_apart(o[1], o + 2, 1);
+  int dev;
+  if (st == RQ_OK) st = check_device(&dev);
+  if (st != RQ_OK) return st;
+  const rq::QuantArgs a{x, q, scales, input_type == RQ_TYPE_F16, act == RQ_ACT_RELU2,
+                        scale_type == RQ_SCALE_E8M0, M, K};
+  return rq::launch_quant(a, static_cast<hipStream_t>(stream)) == hipSuccess ? RQ_OK
+                                                                            : RQ_ERR_LAUNCH;
+}
+
+// Types and sizes of a call of rq_gemm_fp8, without its pointers.
+static rq_status fp8_plan(const rq_fp8_problem* problems, int count, int M, int scale_type,
+                          int out_type, rq::Fp8Args* a) {
+  if (!problems) return RQ_ERR_NULL;
+  if ((scale_type != RQ_SCALE_F32 && scale_type != RQ_SCALE_E8M0) ||
+      (out_type != RQ_TYPE_F32 && out_type != RQ_TYPE_F16 && out_type != RQ_TYPE_E4M3))
+    return RQ_ERR_UNSUPPORTED;
+  if (count < 1 || count > RQ_FP8_MAX_BATCH || M < 1 || M > RQ_MAX_TOKENS) return RQ_ERR_SHAPE;
+  *a = rq::Fp8Args{};
+  a->count = count;
+  a->M = M;
+  a->e8m0 = scale_type == RQ_SCALE_E8M0;
+  a->out = out_type;
+  for (int i = 0; i < count; i++) {
+    const int N = problems[i].N, K = problems[i].K;
+    if (N < 1 || N > MAX_SIZE || !fp8_k(K) || !fp8_values(M, N)) return RQ_ERR_SHAPE;
+    if (out_type == RQ_TYPE_E4M3 && N % RQ_FP8_BLOCK != 0) return RQ_ERR_SHAPE;
+    a->p[i].N = N;
+    a->p[i].K = K;
+  }
+  return RQ_OK;
+}
+
+rq_status rq_gemm_fp8_workspace_size(const rq_fp8_problem* problems, int count, int M,
+                                     int scale_type, int out_type, size_t* bytes) {
+  if (!bytes) return RQ_ERR_NULL;
+  *bytes = 0;
+  rq::Fp8Args a;
+  const rq_status st = fp8_plan(problems, count, M, scale_type, out_type, &a);
+  if (st == RQ_OK) *bytes = rq::fp8_workspace_bytes(a);
+  return st;
+}
+
+rq_status rq_gemm_fp8(const rq_fp8_problem* problems, int count, int M, int scale_type,
+                      int out_type, int act, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  rq::Fp8Args a;
+  rq_status st = fp8_plan(problems, count, M, scale_type, out_type, &a);
+  if (st != RQ_OK) return st;
+  if (act != RQ_ACT_NONE && !(act == RQ_ACT_RELU2 && out_type == RQ_TYPE_E4M3))
+    return RQ_ERR_UNSUPPORTED;
+  a.relu2 = act == RQ_ACT_RELU2;
+  // read: five of every problem; written: its y and y_scales
+  Operand in[5 * RQ_FP8_MAX_BATCH], out[2 * RQ_FP8_MAX_BATCH];
+  for (int i = 0; i < count; i++) {
+    const rq_fp8_problem& q = problems[i];
+    const bool blocks = out_type == RQ_TYPE_E4M3;
+    if (!q.w || !q.w_scales || !q.x || !q.x_scales || !q.y || (blocks && !q.y_scales))
+      return RQ_ERR_NULL;
+    if (q.y_in && out_type != RQ_TYPE_F32) return RQ_ERR_UNSUPPORTED;
+    const size_t kb = q.K / RQ_FP8_BLOCK, nb = ((size_t)q.N + RQ_FP8_BLOCK - 1) / RQ_FP8_BLOCK;
+    const size_t m = M, n = q.N;
+    in[5 * i] = array(q.w, n * q.K);
+    in[5 * i + 1] = scale_array(q.w_scales, nb * kb, scale_type);
+    in[5 * i + 2] = array(q.x, m * q.K);
+    in[5 * i + 3] = scale_array(q.x_scales, m * kb, scale_type);
+    in[5 * i + 4] = array(q.y_in, m * n * 4);
+    out[2 * i] = array(q.y, m * n * type_bytes(out_type));
+    out[2 * i + 1] = scale_array(blocks ? q.y_scales : nullptr, m * nb, scale_type);
+    rq::Fp8Problem& p = a.p[i];
+    p.w = static_cast<const uint8_t*>(q.w);
+    p.ws = q.w_scales;
+    p.x = static_cast<const uint8_t*>(q.x);
+    p.xs = q.x_scales;
+    p.y_in = q.y_in;
+    p.y = q.y;
+    p.ys = out[2 * i + 1].p ? q.y_scales : nullptr;
+  }
+  const size_t need = workspace ? rq::fp8_workspace_bytes(a) : 0;
+  const Operand ws = array(need ? workspace : nullptr, need);
+  st = check_align(in, 5 * count);
+  if (st == RQ_OK) st = check_align(out, 2 * count);
+  if (st == RQ_OK && workspace && !aligned16(workspace)) st = RQ_ERR_ALIGN;
+  if (st != RQ_OK) return st;
+  for (int i = 0; i < 2 * count; i++) {
+    for (int j = 0; j < 5 * count; j++) {
+      if (i % 2 == 0 && j == 5 * (i / 2) + 4 && in[j].p == out[i].p) continue;  // in place
+      if (check_apart(out[i], in + j, 1) != RQ_OK) return RQ_ERR_ALIAS;
+    }
+    if (check_apart(out[i], out + i + 1, 2 * count - i - 1) != RQ_OK) return RQ_ERR_ALIAS;
+  }
+  if (workspace_bytes < need) return RQ_ERR_SCRATCH;
+  if (check_apart(ws, in, 5 * count) != RQ_OK || check_apart(ws, out, 2 * count) != RQ_OK)
+    return RQ_ERR_ALIAS;
+  int dev;
+  st = check_device(&dev);
+  if (st != RQ_OK) return st;
+  return rq::launch_fp8(a, need ? workspace : nullptr, static_cast<hipStream_t>(stream)) ==
+                 hipSuccess
+             ? RQ_OK
+             : RQ_ERR_LAUNCH;
+}
+
+rq_status rq_groupnorm(const rq_groupnorm_args* args, void* stream) {
+  if (!args || !args->y || !args->out) return RQ_ERR_NULL;
+  const rq_groupnorm_args& g = *args;
+  if (g.r && (!g.k || !g.r_k || !g.v)) return RQ_ERR_NULL;
+  const bool blocks = g.out_type == RQ_TYPE_E4M3;
+  if (blocks && !g.out_scales) return RQ_ERR_NULL;
+  if ((g.input_type != RQ_TYPE_F32 && g.input_type != RQ_TYPE_F16) ||
+      (g.act != RQ_ACT_NONE && g.act != RQ_ACT_SILU) ||
+      (g.out_type != RQ_TYPE_F32 && g.out_type != RQ_TYPE_F16 && !blocks) ||
+      (blocks && g.scale_type != RQ_SCALE_F32 && g.scale_type != RQ_SCALE_E8M0))
+    return RQ_ERR_UNSUPPORTED;
+  if (g.T < 1 || g.T > RQ_MAX_TOKENS || g.C < 32 || g.C > 1 << 20 || g.groups < 1 ||
+      g.C % g.groups != 0 || !fp8_values(g.T, g.C) || (blocks && g.C % RQ_FP8_BLOCK != 0))
+    return RQ_ERR_SHAPE;
+  const int size = g.C / g.groups;
+  if (size != 32 && size != 64 && size != 128 && size != 256) return RQ_ERR_SHAPE;
+  if (!(g.eps >= 0.0f) || g.eps > 3.4e38f) return RQ_ERR_SHAPE;
+  const size_t c = g.C, n = (size_t)g.T * c, e = type_bytes(g.input_type);
+  const Operand in[] = {array(g.y, n * 4), array(g.weight, c * 4), array(g.bias, c * 4),
+                        array(g.r, n * e), array(g.r ? g.k : nullptr, n * e),
+                        array(g.r ? g.r_k : nullptr, c * 4), array(g.r ? g.v : nullptr, n * e),
+                        array(g.gate, n * e)};
+  const Operand out[] = {array(g.out, n * type_bytes(g.out_type)),
+                         scale_array(blocks ? g.out_scales : nullptr, n / RQ_FP8_BLOCK,
+                                     g.scale_type)};
+  rq_status st = check_align(in, 8);
+  if (st == RQ_OK) st = check_align(out, 2);
+  const int first = g.out == g.y && g.out_type == RQ_TYPE_F32 ? 1 : 0;  // in place
+  if (st == RQ_OK) st = check_apart(out[0], in + first, 8 - first);
+  if (st == RQ_OK) st = check_apart(out[1], in, 8);
+  if (st == RQ_OK) st = check_apart(out[0], out + 1, 1);
+  int dev;
+  if (st == RQ_OK) st = check_device(&dev);
+  if (st != RQ_OK) return st;
+  const rq::GroupnormArgs a{g.y, g.weight, g.bias, g.r, g.k, g.r_k, g.v, g.gate, g.out,
+                            blocks ? g.out_scales : nullptr, g.input_type == RQ_TYPE_F16,
+                            g.act == RQ_ACT_SILU, g.out_type, g.scale_type == RQ_SCALE_E8M0, g.T,
+                            g.C, g.groups, g.eps};
+  return rq::launch_groupnorm(a, static_cast<hipStream_t>(stream)) == hipSuccess ? RQ_OK
+                                                                                : RQ_ERR_LAUNCH;
 }
 
 const char* rq_status_string(int status) {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <stdint.h>
 
 #include <atomic>
 
@@ -178,5 +179,47 @@ struct LogitsArgs {
 // ws: 16 bytes per row (LOGITS_MAX_M of them), zero between launches (unused
 // without tokens)
 hipError_t launch_logits(const LogitsArgs& a, void* ws, hipStream_t s);
+
+// Block-scaled FP8 (rq_quant.hip, rq_gemm_fp8.hip, rq_groupnorm.hip).
+constexpr int FP8_BLOCK = 128;
+struct QuantArgs {
+  const void* x;  // [M][K], binary16 or binary32
+  void* q;        // E4M3 [M][K]
+  void* scales;   // [M][K / 128]
+  int half, relu2, e8m0, M, K;
+};
+hipError_t launch_quant(const QuantArgs& a, hipStream_t s);
+
+// Types of outputs, as rq_type of rq.h.
+enum Out { OUT_F32 = 0, OUT_F16 = 1, OUT_E4M3 = 2 };
+
+constexpr int FP8_BATCH = 8;
+struct Fp8Problem {
+  const uint8_t* w;  // E4M3 [N][K]
+  const void* ws;    // [ceil(N / 128)][K / 128]
+  const uint8_t* x;  // E4M3 [M][K]
+  const void* xs;    // [M][K / 128]
+  const float* y_in; // [M][N] or NULL
+  void* y;           // [M][N]
+  void* ys;          // [M][N / 128] with OUT_E4M3
+  int N, K;
+};
+struct Fp8Args {
+  Fp8Problem p[FP8_BATCH];
+  int count, M, e8m0, out, relu2;
+};
+size_t fp8_workspace_bytes(const Fp8Args& a);
+hipError_t launch_fp8(const Fp8Args& a, void* ws, hipStream_t s);
+
+struct GroupnormArgs {
+  const float *y, *weight, *bias;  // [T][C], [C], [C] (NULL: 1, 0)
+  const void *r, *k;               // [T][C] (r NULL: no bonus)
+  const float* r_k;                // [C]
+  const void *v, *gate;            // [T][C] (gate NULL: 1)
+  void *out, *out_scales;
+  int half, silu, out_type, e8m0, T, C, groups;
+  float eps;
+};
+hipError_t launch_groupnorm(const GroupnormArgs& a, hipStream_t s);
 
 }  // namespace rq

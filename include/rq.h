@@ -310,8 +310,8 @@ rq_status rq_shift(const void* x, const void* mu, void* state, void* out, const 
 /* Channels of a head of rq_wkv7. */
 #define RQ_WKV_HEAD 64
 
-/* Types of rq_wkv7's inputs. */
-typedef enum { RQ_TYPE_F32 = 0, RQ_TYPE_F16 = 1 } rq_type;
+/* Types of values: rq_wkv7's inputs are of the first two. */
+typedef enum { RQ_TYPE_F32 = 0, RQ_TYPE_F16 = 1, RQ_TYPE_E4M3 = 2 } rq_type;
 
 /*
  * rq_wkv7 -- the RWKV-7 state recurrence between the receptance/key/value
@@ -446,6 +446,136 @@ typedef struct {
  */
 rq_status rq_logits(const rq_logits_args* args, void* workspace, size_t workspace_bytes,
                     void* stream);
+
+/*
+ * Block-scaled FP8.  Both operands of a product are OCP E4M3 numbers with a
+ * scale for each block of 128: activations one for 128 consecutive values of a
+ * row, weights one for 128 x 128.  Scales are binary32, or E8M0: one byte b that
+ * stands for 2^(b - 127), 255 for NaN.  These calls keep the rules of the calls
+ * around the products; scales need the alignment of their type only.
+ */
+#define RQ_FP8_BLOCK 128
+
+/* Types of scales (a call's weights, activations and outputs share one). */
+typedef enum { RQ_SCALE_F32 = 0, RQ_SCALE_E8M0 = 1 } rq_scale_type;
+
+typedef enum {
+    RQ_ACT_NONE = 0,
+    RQ_ACT_RELU2 = 1, /* max(z, 0)^2     */
+    RQ_ACT_SILU = 2   /* z / (1 + e^-z)  */
+} rq_act;
+
+/* Limits of the block-scaled calls. */
+#define RQ_FP8_MAX_K (1 << 22)
+#define RQ_FP8_MAX_BATCH 8
+#define RQ_FP8_MAX_VALUES (1ll << 34)
+
+/*
+ * rq_quant_fp8 -- rows quantized in blocks of 128 values:
+ *   a = act(x) (RQ_ACT_NONE or RQ_ACT_RELU2; the square is rounded to binary32),
+ *   s = the smallest power of two, 2^-126 at least, with |a| <= 448 s for every
+ *       finite a of the block,
+ *   q = the E4M3 number nearest a / s, ties to even; NaN where a is not finite.
+ * The scale is a power of two in either type, so a / s is exact and there is one
+ * right answer.  A block of zeros has the scale 2^-126.
+ *   x: binary32 or binary16 (input_type) [M][K].  q: E4M3 [M][K].  scales: of
+ *   scale_type, [M][K/128].
+ * Shape rules: 1 <= M <= RQ_MAX_TOKENS, 128 <= K <= RQ_FP8_MAX_K, K % 128 == 0, at
+ * most RQ_FP8_MAX_VALUES values.
+ */
+rq_status rq_quant_fp8(const void* x, int input_type, int act, void* q, void* scales,
+                       int scale_type, int M, int K, void* stream);
+
+/* One product of rq_gemm_fp8. */
+typedef struct {
+    const void* w;        /* E4M3 [N][K]                                           */
+    const void* w_scales; /* [(N + 127) / 128][K / 128]                            */
+    const void* x;        /* E4M3 [M][K]                                           */
+    const void* x_scales; /* [M][K / 128]                                          */
+    const float* y_in;    /* float [M][N], NULL for zero; y itself, or disjoint    */
+    void* y;              /* [M][N] of out_type                                    */
+    void* y_scales;       /* [M][N / 128] with RQ_TYPE_E4M3, else not used         */
+    int N;
+    int K;
+} rq_fp8_problem;
+
+/*
+ * rq_gemm_fp8 -- y = y_in + x W^T of block-scaled operands, for `count`
+ * independent products with M rows each (receptance, key and value, say) in one
+ * launch:
+ *   y[m][n] = y_in[m][n] + sum_b xs[m][b] ws[n/128][b] sum_{k in block b} x[m][k] w[n][k].
+ *   out_type RQ_TYPE_F32: binary32.  Every sum is held in binary32: errors are
+ *     about 2^-23 of the sum of the products' magnitudes.
+ *   RQ_TYPE_F16: rounded to binary16 (past 65504 infinite); no y_in.
+ *   RQ_TYPE_E4M3: what rq_quant_fp8 with `act` makes of the RQ_TYPE_F16 output, to
+ *     the bit, without that output in memory; no y_in, N % 128 == 0.
+ *     Calls of many rows take the FP8 matrix instructions for these two.  Those
+ *     drop what lies 2^-13 or more below the largest of eight products: within
+ *     2^-10 of the sum of the products' magnitudes, about 2^-15 of an ordinary
+ *     output.
+ *   act: RQ_ACT_NONE, or RQ_ACT_RELU2 with RQ_TYPE_E4M3.
+ * NaN in an operand or a scale reaches its outputs.  The product of an x scale and
+ * a w scale has to be a normal binary32 number (or zero); what a smaller or larger
+ * one gives is not specified.  Rows are independent: what is in row m of x does
+ * not change another row's results.
+ *   workspace: device memory, 16-byte aligned, overlapping nothing else, whose first
+ *   64 KiB are zero before its first use; every call leaves them zero (a workspace of
+ *   rq_gemm_smallm_ws will do).  Calls that share it must not overlap in time.  NULL
+ *   keeps K whole, which is slower for few rows.  RQ_ERR_SCRATCH: smaller than
+ *   rq_gemm_fp8_workspace_size reports.
+ * Results are deterministic; which sums are taken together follows from the sizes
+ * of the call (and from whether it has a workspace).
+ * Shape rules: 1 <= count <= RQ_FP8_MAX_BATCH, 1 <= M <= RQ_MAX_TOKENS, 1 <= N <=
+ * 1 << 24, 128 <= K <= RQ_FP8_MAX_K, K % 128 == 0, at most RQ_FP8_MAX_VALUES outputs of a product.
+ * `problems` is a host array the call reads before it returns.
+ */
+rq_status rq_gemm_fp8(const rq_fp8_problem* problems, int count, int M, int scale_type,
+                      int out_type, int act, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* The workspace rq_gemm_fp8 uses at these arguments (N, K of `problems` only), at
+ * most RQ_GEMM_WORKSPACE_MAX_BYTES.  Host-only. */
+rq_status rq_gemm_fp8_workspace_size(const rq_fp8_problem* problems, int count, int M,
+                                     int scale_type, int out_type, size_t* bytes);
+
+/* Arguments of rq_groupnorm. */
+typedef struct {
+    const float* y;      /* [T][C]                                                 */
+    const float* weight; /* [C], NULL for 1                                        */
+    const float* bias;   /* [C], NULL for 0                                        */
+    const void* r;       /* [T][C] of input_type, NULL for no bonus; with it:      */
+    const void* k;       /*   [T][C] of input_type                                 */
+    const float* r_k;    /*   [C]                                                  */
+    const void* v;       /*   [T][C] of input_type                                 */
+    const void* gate;    /* [T][C] of input_type, NULL for 1                       */
+    void* out;           /* [T][C] of out_type; y itself with RQ_TYPE_F32, or disjoint */
+    void* out_scales;    /* [T][C / 128] with RQ_TYPE_E4M3, else not used          */
+    int input_type;      /* RQ_TYPE_F32 or RQ_TYPE_F16                             */
+    int act;             /* of the gate: RQ_ACT_NONE or RQ_ACT_SILU                */
+    int out_type;
+    int scale_type;      /* of out_scales                                          */
+    int T;
+    int C;
+    int groups;
+    float eps;
+} rq_groupnorm_args;
+
+/*
+ * rq_groupnorm -- the norm between the state recurrence and the output
+ * projection: every token's channels in groups of C / groups (the heads), and
+ * per group
+ *   z   = (y - mean(y)) / sqrt(mean((y - mean(y))^2) + eps) * weight + bias
+ *         + sum(r * k * r_k) * v,
+ *   out = z * act(gate),
+ * in binary32, the variance from the centred values.  RQ_TYPE_F16 is rounded
+ * once; RQ_TYPE_E4M3 is what rq_quant_fp8 makes of the RQ_TYPE_F16 output, to the
+ * bit.  A group's non-finite inputs stay in that group, but for the E4M3 outputs of
+ * their own block, whose scale is that of its finite values.
+ * Shape rules: 1 <= T <= RQ_MAX_TOKENS, C / groups 32, 64, 128 or 256, C <= 1 <<
+ * 20, at most RQ_FP8_MAX_VALUES values, C % 128 == 0 with RQ_TYPE_E4M3, eps >= 0 and
+ * finite.
+ */
+rq_status rq_groupnorm(const rq_groupnorm_args* args, void* stream);
 
 /* A static, NUL-terminated English description of a status value. */
 const char* rq_status_string(int status);
