@@ -1,9 +1,5 @@
 // rq_gemm_fp8.hip -- products of block-scaled E4M3 operands:
 //   y[m][n] = y_in[m][n] + sum_b xs[m][b] ws[n/128][b] sum_{k in b} x[m][k] w[n][k].
-//
-// Inside a block of 128 the E4M3 numbers are widened to binary16 (exact) and meet
-// in the binary16 matrix instructions, whose sums are binary32; the block's sum
-// then enters the binary32 total with one multiply-add by the two scales.
 #include "rq_common.h"
 #include "rq_fp8.h"
 #include "rq_internal.h"
@@ -11,7 +7,14 @@
 namespace rq {
 namespace {
 
-constexpr int NT = 8;  // 16-row tiles of w of a wave: one block of outputs
+typedef int i8v __attribute__((ext_vector_type(8)));
+
+// How a block of 128 meets:
+//   WIDE   widened to binary16 (exact), binary16 matrix instructions, one
+//          multiply-add by the scales for each block's sum;
+//   FP8S   the FP8 matrix instruction of depth 128, the same multiply-add;
+//   FP8E   the FP8 matrix instruction with the power of two as its own scale.
+enum Mode { WIDE, FP8S, FP8E };
 
 // The 16 E4M3 numbers of a 16-byte piece as two operands of 8.
 __device__ __forceinline__ void widen(u32x4 v, h8 (&o)[2]) {
@@ -25,105 +28,506 @@ __device__ __forceinline__ void widen(u32x4 v, h8 (&o)[2]) {
   o[1] = u.o[1];
 }
 
-template <bool E8M0>
-__device__ __forceinline__ float scale_value(const void* s, size_t i) {
-  if constexpr (E8M0)
-    return e8m0_value(static_cast<const uint8_t*>(s)[i]);
-  else
-    return static_cast<const float*>(s)[i];
+// The product of two scales: its binary32 value, or (FP8E) the exponent byte.
+template <Mode MODE>
+__device__ __forceinline__ u32 joint_scale(u32 a, u32 b, bool e8m0) {
+  if constexpr (MODE == FP8E) {
+    const int e = (int)a + (int)b - 127;
+    return a == 255 || b == 255 ? 255u : (u32)min(max(e, 0), 254);
+  } else {
+    const float fa = e8m0 ? e8m0_value(a) : __builtin_bit_cast(float, a);
+    const float fb = e8m0 ? e8m0_value(b) : __builtin_bit_cast(float, b);
+    return __builtin_bit_cast(u32, fa * fb);
+  }
+}
+__device__ __forceinline__ u32 load_scale(const void* s, size_t i, bool e8m0) {
+  return e8m0 ? (u32) static_cast<const uint8_t*>(s)[i] : static_cast<const u32*>(s)[i];
 }
 
-// Lane l of a 16 x 16 tile holds row m = l % 16 and columns n = 4 * (l / 16) + i.
-template <bool E8M0>
-__global__ void __launch_bounds__(64) k_fp8(const Fp8Args a) {
-  const Fp8Problem& p = a.p[blockIdx.y];
-  const int lane = threadIdx.x, r = lane & 15, h = lane >> 4;
-  const u32 mt = (a.M + 15) / 16, nb = blockIdx.x / mt;  // block of outputs
-  const int n0 = nb * 16 * NT;
-  const size_t m = (size_t)(blockIdx.x % mt) * 16 + r;
-  if (n0 >= p.N) return;
-  const size_t mc = min(m, (size_t)a.M - 1);  // rows past the end repeat the last one
-  const int kb = p.K / 128;
-  const uint8_t* xp = p.x + mc * p.K + 16 * h;
-  f4 acc[NT];
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+__device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t r, void* dst, u32 voff, u32 soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16,
+                                           voff, soff, 0, 0);
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, -1, 0x00020000);
+}
+
+// Work of a launch: tiles of all problems one after another, m fastest, each in
+// `splits` ranges of K.
+struct Launch {
+  int tile0[FP8_BATCH + 1];  // first tile of each problem
+  int mt;                    // tiles of M
+  int splits;
+  unsigned* counters;        // one per tile, zero between launches
+  float* partial;            // [tile][split][outputs of a tile, as the lanes hold them]
+};
+
+constexpr int TN = 8;  // 16-row tiles of w of a wave: one block of outputs
+
+// WN x WM waves, each 128 outputs of 16 * TM rows; ST stages of 128 columns.
+template <int WN_, int WM_, int TM_, int ST_>
+struct Tile {
+  static constexpr int WN = WN_, WM = WM_, TM = TM_, ST = ST_;
+  static constexpr int W = WN * WM, THREADS = 64 * W;
+  static constexpr int BN = 128 * WN, BM = 16 * TM * WM;
+  static constexpr int STAGE = (BN + BM) * 128;
+  static constexpr int COPIES = (BN + BM) / 8 / W;  // of a wave for a stage
+  static constexpr int WCOPIES = BN / 8 / W;        // of these, rows of w
+  static constexpr int SC = 4;                      // blocks of K whose scales are staged together
+  static constexpr int SCALES = SC * WN * BM;       // dwords of a buffer of scales
+  static constexpr int LDS = ST * STAGE + 2 * SCALES * 4;
+  static_assert((BN + BM) / 8 % W == 0 && BN / 8 % W == 0, "whole copies");
+  static_assert(LDS <= 160 * 1024, "LDS");
+  static constexpr int PER = SC * BM / THREADS;  // scales of x that a thread stages
+  static_assert(SC * BM % THREADS == 0 || SC * BM < THREADS, "scales");
+};
+
+// The products of one block of K from a stage in LDS.
+template <typename T, Mode MODE>
+__device__ __forceinline__ void multiply(const char* stage, const u32* scales, int wn, int wm,
+                                         f4 (&acc)[TN][T::TM]) {
+  constexpr int TM = T::TM;
+  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+  // chunk 4 p + h of a row, in the slot its row's last bits exchange it to
+  const int o0 = r * 128 + ((h ^ (r & 7)) << 4), o1 = r * 128 + (((4 + h) ^ (r & 7)) << 4);
+  const char* wp = stage + wn * 128 * 128;
+  const char* xp = stage + T::BN * 128 + wm * TM * 16 * 128;
+  u32 s[TM];
 #pragma unroll
-  for (int t = 0; t < NT; t++) acc[t] = f4{0, 0, 0, 0};
-  for (int b = 0; b < kb; b++) {
-    h8 x[2][2];
+  for (int j = 0; j < TM; j++) s[j] = scales[wn * T::BM + (wm * TM + j) * 16 + r];
+  if constexpr (MODE == WIDE) {
+    h8 x[TM][2][2];
 #pragma unroll
-    for (int q = 0; q < 2; q++)
-      widen(*reinterpret_cast<const u32x4*>(xp + b * 128 + 64 * q), x[q]);
-    const float s = scale_value<E8M0>(p.xs, mc * kb + b) *
-                    scale_value<E8M0>(p.ws, (size_t)nb * kb + b);
+    for (int j = 0; j < TM; j++) {
+      widen(*reinterpret_cast<const u32x4*>(xp + j * 2048 + o0), x[j][0]);
+      widen(*reinterpret_cast<const u32x4*>(xp + j * 2048 + o1), x[j][1]);
+    }
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-      const int n = min(n0 + 16 * t + r, p.N - 1);
-      const uint8_t* wp = p.w + (size_t)n * p.K + 16 * h + b * 128;
-      f4 d = {0, 0, 0, 0};
+    for (int t = 0; t < TN; t++) {
+      h8 w[2][2];
+      widen(*reinterpret_cast<const u32x4*>(wp + t * 2048 + o0), w[0]);
+      widen(*reinterpret_cast<const u32x4*>(wp + t * 2048 + o1), w[1]);
 #pragma unroll
-      for (int q = 0; q < 2; q++) {
-        h8 w[2];
-        widen(*reinterpret_cast<const u32x4*>(wp + 64 * q), w);
-        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[0], x[q][0], d, 0, 0, 0);
-        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[1], x[q][1], d, 0, 0, 0);
+      for (int j = 0; j < TM; j++) {
+        f4 d = {0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < 2; q++)
+#pragma unroll
+          for (int e = 0; e < 2; e++)
+            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[q][e], x[j][q][e], d, 0, 0, 0);
+        const float f = __builtin_bit_cast(float, s[j]);
+#pragma unroll
+        for (int i = 0; i < 4; i++) acc[t][j][i] = __builtin_fmaf(d[i], f, acc[t][j][i]);
       }
+    }
+  } else {
+    union Op {
+      u32x4 q[2];
+      i8v v;
+    };
+    Op x[TM];
 #pragma unroll
-      for (int i = 0; i < 4; i++) acc[t][i] = __builtin_fmaf(d[i], s, acc[t][i]);
+    for (int j = 0; j < TM; j++) {
+      x[j].q[0] = *reinterpret_cast<const u32x4*>(xp + j * 2048 + o0);
+      x[j].q[1] = *reinterpret_cast<const u32x4*>(xp + j * 2048 + o1);
+    }
+#pragma unroll
+    for (int t = 0; t < TN; t++) {
+      Op w;
+      w.q[0] = *reinterpret_cast<const u32x4*>(wp + t * 2048 + o0);
+      w.q[1] = *reinterpret_cast<const u32x4*>(wp + t * 2048 + o1);
+#pragma unroll
+      for (int j = 0; j < TM; j++) {
+        if constexpr (MODE == FP8E) {
+          acc[t][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              w.v, x[j].v, acc[t][j], 0, 0, 0, 127, 0, (int)s[j]);
+        } else {
+          const f4 z = {0, 0, 0, 0};
+          const f4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x[j].v, z, 0, 0, 0, 127,
+                                                                       0, 127);
+          const float f = __builtin_bit_cast(float, s[j]);
+#pragma unroll
+          for (int i = 0; i < 4; i++) acc[t][j][i] = __builtin_fmaf(d[i], f, acc[t][j][i]);
+        }
+      }
     }
   }
-  if (a.out == OUT_E4M3) {
-    // the block's largest of a row is spread over the four lanes of the row
-    float v[NT * 4];
+}
+
+// Four consecutive outputs of row m.
+__device__ __forceinline__ void store4(const Fp8Problem& p, int out, size_t m, int n, f4 v) {
+  const size_t at = m * p.N + n;
+  const bool whole = p.N % 4 == 0 && n < p.N;
+  if (out == OUT_F32) {
+    float* y = static_cast<float*>(p.y) + at;
+    if (whole) {
+      if (p.y_in) v = *reinterpret_cast<const f4*>(p.y_in + at) + v;
+      *reinterpret_cast<f4*>(y) = v;
+    } else {
 #pragma unroll
-    for (int t = 0; t < NT; t++)
+      for (int i = 0; i < 4; i++)
+        if (n + i < p.N) y[i] = p.y_in ? p.y_in[at + i] + v[i] : v[i];
+    }
+  } else {
+    _Float16* y = static_cast<_Float16*>(p.y) + at;
+    const h4 o = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+    if (whole) {
+      *reinterpret_cast<h4*>(y) = o;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (n + i < p.N) y[i] = o[i];
+    }
+  }
+}
+
+// A wave's 128 outputs of its rows.  Lane l holds rows 16 j + l % 16 and outputs
+// 16 t + 4 (l / 16) + i.
+template <int TM>
+__device__ __forceinline__ void store_tile(const Fp8Args& a, const Fp8Problem& p, int n0, size_t m0,
+                                           const f4 (&acc)[TN][TM]) {
+  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < TM; j++) {
+    const size_t m = m0 + 16 * j + r;
+    if (a.out != OUT_E4M3) {
+      if (m < (size_t)a.M) {
+#pragma unroll
+        for (int t = 0; t < TN; t++) store4(p, a.out, m, n0 + 16 * t + 4 * h, acc[t][j]);
+      }
+      continue;
+    }
+    // the four lanes of a row hold its block
+    float v[TN * 4];
+#pragma unroll
+    for (int t = 0; t < TN; t++)
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const float z = (float)(_Float16)acc[t][i];
+        const float z = (float)(_Float16)acc[t][j][i];
         v[4 * t + i] = a.relu2 ? relu2(z) : z;
       }
     u32 top = 0;
 #pragma unroll
-    for (int i = 0; i < NT * 4; i++) top = max(top, abs_bits(v[i]) < INF_BITS ? abs_bits(v[i]) : 0u);
+    for (int i = 0; i < TN * 4; i++) {
+      const u32 b = abs_bits(v[i]);
+      top = max(top, b < INF_BITS ? b : 0u);
+    }
     top = max(top, (u32)__shfl_xor((int)top, 16, 64));
     top = max(top, (u32)__shfl_xor((int)top, 32, 64));
     const u32 se = scale_exponent(top);
     const float inv = pow2_bits(254 - se);
-    if (m >= (size_t)a.M) return;
+    if (m < (size_t)a.M && n0 < p.N) {
+      uint8_t* y = static_cast<uint8_t*>(p.y) + m * p.N + n0 + 4 * h;
 #pragma unroll
-    for (int t = 0; t < NT; t++)
-      *reinterpret_cast<u32*>(static_cast<uint8_t*>(p.y) + m * p.N + n0 + 16 * t + 4 * h) =
-          e4m3x4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3], inv);
-    if (h == 0) store_scale(p.ys, m * (p.N / 128) + nb, se, E8M0);
-    return;
-  }
-  if (m >= (size_t)a.M) return;
-#pragma unroll
-  for (int t = 0; t < NT; t++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int n = n0 + 16 * t + 4 * h + i;
-      if (n >= p.N) continue;
-      const size_t at = m * p.N + n;
-      if (a.out == OUT_F32)
-        static_cast<float*>(p.y)[at] = p.y_in ? p.y_in[at] + acc[t][i] : acc[t][i];
-      else
-        static_cast<_Float16*>(p.y)[at] = (_Float16)acc[t][i];
+      for (int t = 0; t < TN; t++)
+        *reinterpret_cast<u32*>(y + 16 * t) =
+            e4m3x4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3], inv);
+      if (h == 0) store_scale(p.ys, m * (p.N / 128) + n0 / 128, se, a.e8m0);
     }
+  }
+}
+
+template <typename T, Mode MODE>
+__global__ void __launch_bounds__(T::THREADS, T::W / 4 > 0 ? T::W / 4 : 1)
+k_tile(const Fp8Args a, const Launch l) {
+  constexpr int W = T::W, TM = T::TM, ST = T::ST, SC = T::SC;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  u32* const scales = reinterpret_cast<u32*>(lds + ST * T::STAGE);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave / T::WM, wm = wave % T::WM;
+
+  // workgroup -> (tile, split): every XCD (workgroups go to them in turn) takes a
+  // run of neighbouring tiles, which share rows of x and w in its L2
+  const u32 total = gridDim.x, xcd = blockIdx.x & 7, each = total >> 3, more = total & 7;
+  const u32 id = xcd * each + min(xcd, more) + (blockIdx.x >> 3);
+  const int split = id % l.splits, tile = id / l.splits;
+  int pi = 0;
+  while (pi + 1 < a.count && tile >= l.tile0[pi + 1]) pi++;
+  const Fp8Problem& p = a.p[pi];
+  const int n0 = (tile - l.tile0[pi]) / l.mt * T::BN;
+  const size_t m0 = (size_t)((tile - l.tile0[pi]) % l.mt) * T::BM;
+  const int KB = p.K / 128, nb = (p.N + 127) / 128;
+  const int b0 = (int)((long long)KB * split / l.splits);
+  const int steps = (int)((long long)KB * (split + 1) / l.splits) - b0;
+  const bool e8m0 = a.e8m0;
+
+  // copies of this wave: eight rows of 128 bytes each; slot s of row q holds
+  // chunk s ^ (q % 8), so that the reads of 16 rows' equal chunks spread over all
+  // banks.  Rows past the end repeat the last one.
+  const __amdgpu_buffer_rsrc_t wr = buffer(p.w + (size_t)n0 * p.K + (size_t)b0 * 128);
+  const __amdgpu_buffer_rsrc_t xr = buffer(p.x + m0 * p.K + (size_t)b0 * 128);
+  const int w_last = p.N - 1 - n0, x_last = (int)min((size_t)a.M - 1 - m0, (size_t)T::BM);
+  u32 off[T::COPIES];
+#pragma unroll
+  for (int c = 0; c < T::COPIES; c++) {
+    const int row = (c * W + wave) * 8 + (lane >> 3);
+    const int q = c < T::WCOPIES ? min(row, w_last) : min(row - T::BN, x_last);
+    off[c] = (u32)q * p.K + (((lane & 7) ^ (lane >> 3)) << 4);
+  }
+  auto copy = [&](int step) {
+    char* dst = lds + step % ST * T::STAGE + wave * 1024;
+#pragma unroll
+    for (int c = 0; c < T::COPIES; c++)
+      lds_copy16(c < T::WCOPIES ? wr : xr, dst + c * W * 1024, off[c], step * 128);
+  };
+
+  // scales of SC blocks: thread -> row of x and blocks
+  constexpr int PER = T::PER > 0 ? T::PER : 1;
+  const int srow = tid % T::BM;
+  const bool stager = T::PER > 0 || tid < SC * T::BM;
+  const size_t xs_row = (m0 + min(srow, x_last)) * KB + b0;
+  u32 sx[PER], sw[T::WN][PER];
+  auto load_scales = [&](int first) {
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+      const int b = min(first + tid / T::BM + i * (T::THREADS / T::BM > 0 ? T::THREADS / T::BM : 1),
+                        steps - 1);
+      sx[i] = load_scale(p.xs, xs_row + b, e8m0);
+#pragma unroll
+      for (int n = 0; n < T::WN; n++)
+        sw[n][i] = load_scale(p.ws, (size_t)min(n0 / 128 + n, nb - 1) * KB + b0 + b, e8m0);
+    }
+  };
+  auto keep_scales = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+      const int b = tid / T::BM + i * (T::THREADS / T::BM > 0 ? T::THREADS / T::BM : 1);
+#pragma unroll
+      for (int n = 0; n < T::WN; n++)
+        if (stager)
+          scales[buf * T::SCALES + (b * T::WN + n) * T::BM + srow] =
+              joint_scale<MODE>(sx[i], sw[n][i], e8m0);
+    }
+  };
+
+  f4 acc[TN][TM];
+#pragma unroll
+  for (int t = 0; t < TN; t++)
+#pragma unroll
+    for (int j = 0; j < TM; j++) acc[t][j] = f4{0, 0, 0, 0};
+
+  load_scales(0);
+#pragma unroll
+  for (int s = 0; s < ST - 1; s++)
+    if (s < steps) copy(s);
+  keep_scales(0);
+  for (int s = 0; s < steps; s++) {
+    // the stage has arrived (this wave's copies, then everybody's), and everybody
+    // has left the stage that the next copies go to
+    if (s + ST - 2 < steps)
+      wait_vm<(ST - 2) * T::COPIES>();
+    else
+      wait_vm<0>();
+    __syncthreads();
+    if (s + ST - 1 < steps) copy(s + ST - 1);
+    if (s % SC == 0 && s + SC < steps) load_scales(s + SC);
+    multiply<T, MODE>(lds + s % ST * T::STAGE,
+                      scales + (s / SC & 1) * T::SCALES + s % SC * T::WN * T::BM, wn, wm, acc);
+    if (s % SC == SC / 2 && s - s % SC + SC < steps) keep_scales((s / SC & 1) ^ 1);
+  }
+
+  const int wave_n0 = n0 + wn * 128;
+  const size_t wave_m0 = m0 + wm * TM * 16;
+  if (l.splits > 1) {
+    // this range's sums, as the lanes hold them, past the caches that other XCDs
+    // do not see; then the arrival.  The last to arrive adds the ranges in order.
+    constexpr int PART = T::BN * T::BM;
+    float* mine = l.partial + ((size_t)tile * l.splits) * PART;
+    const __amdgpu_buffer_rsrc_t pr = buffer(mine);
+    constexpr int AGENT = 16;  // scope bit of the buffer instructions
+#pragma unroll
+    for (int t = 0; t < TN; t++)
+#pragma unroll
+      for (int j = 0; j < TM; j++)
+        __builtin_amdgcn_raw_buffer_store_b128(
+            __builtin_bit_cast(u32x4, acc[t][j]), pr,
+            (split * PART + ((t * TM + j) * W + wave) * 256 + lane * 4) * 4, 0, AGENT);
+    wait_vm<0>();
+    __syncthreads();
+    unsigned* const flag = reinterpret_cast<unsigned*>(lds);
+    if (tid == 0)
+      *flag = __hip_atomic_fetch_add(l.counters + tile, 1u, __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (*flag != (unsigned)(l.splits - 1)) return;
+    if (tid == 0)
+      __hip_atomic_store(l.counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int t = 0; t < TN; t++)
+#pragma unroll
+      for (int j = 0; j < TM; j++) acc[t][j] = f4{0, 0, 0, 0};
+    for (int q = 0; q < l.splits; q++) {
+#pragma unroll
+      for (int t = 0; t < TN; t++)
+#pragma unroll
+        for (int j = 0; j < TM; j++)
+          acc[t][j] += __builtin_bit_cast(
+              f4, __builtin_amdgcn_raw_buffer_load_b128(
+                      pr, (q * PART + ((t * TM + j) * W + wave) * 256 + lane * 4) * 4, 0, AGENT));
+    }
+  }
+  store_tile<TM>(a, p, wave_n0, wave_m0, acc);
+}
+
+// One row tile, few rows: every wave takes 16 outputs and every 8th block of K,
+// straight from memory to the operands; the eight sums meet in LDS.
+constexpr int SW = 8;
+template <int U>
+__global__ void __launch_bounds__(64 * SW, 2) k_rows(const Fp8Args a, const Launch l) {
+  __shared__ f4 sums[SW][64];
+  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tile = blockIdx.x;
+  int pi = 0;
+  while (pi + 1 < a.count && tile >= l.tile0[pi + 1]) pi++;
+  const Fp8Problem& p = a.p[pi];
+  const int n0 = (tile - l.tile0[pi]) * 16, KB = p.K / 128;
+  const bool e8m0 = a.e8m0;
+  const uint8_t* wp = p.w + (size_t)min(n0 + r, p.N - 1) * p.K + 16 * h;
+  const int mc = min(r, a.M - 1);
+  const uint8_t* xp = p.x + (size_t)mc * p.K + 16 * h;
+  f4 acc = {0, 0, 0, 0};
+  for (int b = wave; b < KB; b += SW * U) {
+    u32x4 w[U][2], x[U][2];
+    u32 sx[U], sw[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int bu = min(b + u * SW, KB - 1);
+#pragma unroll
+      for (int q = 0; q < 2; q++)
+        w[u][q] = load_stream16(wp + (size_t)bu * 128 + 64 * q);
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int bu = min(b + u * SW, KB - 1);
+#pragma unroll
+      for (int q = 0; q < 2; q++)
+        x[u][q] = *reinterpret_cast<const u32x4*>(xp + (size_t)bu * 128 + 64 * q);
+      sx[u] = load_scale(p.xs, (size_t)mc * KB + bu, e8m0);
+      sw[u] = load_scale(p.ws, (size_t)(n0 / 128) * KB + bu, e8m0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (b + u * SW >= KB) break;
+      f4 d = {0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < 2; q++) {
+        h8 wh[2], xh[2];
+        widen(w[u][q], wh);
+        widen(x[u][q], xh);
+        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(wh[0], xh[0], d, 0, 0, 0);
+        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(wh[1], xh[1], d, 0, 0, 0);
+      }
+      const float f = __builtin_bit_cast(float, joint_scale<WIDE>(sx[u], sw[u], e8m0));
+#pragma unroll
+      for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(d[i], f, acc[i]);
+    }
+  }
+  sums[wave][lane] = acc;
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int w = 1; w < SW; w++) acc += sums[w][lane];
+  if (r < a.M && n0 + 4 * h < p.N) store4(p, a.out, r, n0 + 4 * h, acc);
+}
+
+typedef Tile<2, 4, 4, 2> T256;  // 256 x 256
+typedef Tile<1, 4, 2, 2> T128;  // 128 outputs x 128 rows
+typedef Tile<1, 4, 1, 3> T64;   // 128 x 64
+typedef Tile<1, 2, 1, 4> T32;   // 128 x 32
+
+struct Plan {
+  int kind;  // 0 k_rows, 1 T32, 2 T64, 3 T128, 4 T256
+  int splits;
+};
+constexpr int BNS[] = {16, 128, 128, 128, 256}, BMS[] = {16, 32, 64, 128, 256};
+
+int tiles_of(const Fp8Args& a, int kind) {
+  long long n = 0;
+  for (int i = 0; i < a.count; i++)
+    n += (long long)((a.M + BMS[kind] - 1) / BMS[kind]) * ((a.p[i].N + BNS[kind] - 1) / BNS[kind]);
+  return n > (1 << 30) ? 1 << 30 : (int)n;
+}
+
+constexpr int COUNTERS = 16384;  // arrival counters at the front of a workspace
+constexpr size_t WS_MAX = (size_t)64 << 20;
+
+size_t plan_bytes(const Fp8Args& a, const Plan& c) {
+  if (c.splits <= 1) return 0;
+  return COUNTERS * 4 + (size_t)tiles_of(a, c.kind) * c.splits * BNS[c.kind] * BMS[c.kind] * 4;
+}
+
+Plan choose(const Fp8Args& a, bool split) {
+  Plan c{0, 1};
+  if (a.M <= 16 && a.out == OUT_F32) return c;
+  if (a.M <= 32)
+    c.kind = 1;
+  else if (a.M <= 64)
+    c.kind = 2;
+  else
+    c.kind = tiles_of(a, 4) >= 192 ? 4 : 3;
+  const int tiles = tiles_of(a, c.kind);
+  int kb = 1 << 30;
+  for (int i = 0; i < a.count; i++) kb = a.p[i].K / 128 < kb ? a.p[i].K / 128 : kb;
+  if (split && c.kind < 4 && tiles <= COUNTERS) {
+    int want = 256 / tiles;
+    if (want > kb / 4) want = kb / 4;
+    if (want > 16) want = 16;
+    for (; want > 1; want--) {
+      c.splits = want;
+      if (plan_bytes(a, c) <= WS_MAX) break;
+    }
+    c.splits = want > 1 ? want : 1;
+  }
+  return c;
+}
+
+template <typename T, Mode MODE>
+hipError_t launch_tile(const Fp8Args& a, const Launch& l, int tiles, hipStream_t s) {
+  static LdsLimit limit;
+  const auto kernel = k_tile<T, MODE>;
+  const hipError_t e = limit.raise(reinterpret_cast<const void*>(kernel), T::LDS);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)tiles * l.splits), dim3(T::THREADS), T::LDS, s, a, l);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_mode(const Fp8Args& a, const Launch& l, int tiles, hipStream_t s) {
+  if (a.out == OUT_F32) return launch_tile<T, WIDE>(a, l, tiles, s);
+  return a.e8m0 ? launch_tile<T, FP8E>(a, l, tiles, s) : launch_tile<T, FP8S>(a, l, tiles, s);
 }
 
 }  // namespace
 
-size_t fp8_workspace_bytes(const Fp8Args&) { return 0; }
+size_t fp8_workspace_bytes(const Fp8Args& a) { return plan_bytes(a, choose(a, true)); }
 
-hipError_t launch_fp8(const Fp8Args& a, void*, hipStream_t s) {
-  int n = 0;
-  for (int i = 0; i < a.count; i++) n = a.p[i].N > n ? a.p[i].N : n;
-  const dim3 grid((a.M + 15) / 16 * ((n + 16 * NT - 1) / (16 * NT)), a.count);
-  if (a.e8m0)
-    hipLaunchKernelGGL((k_fp8<true>), grid, dim3(64), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_fp8<false>), grid, dim3(64), 0, s, a);
-  return hipGetLastError();
+hipError_t launch_fp8(const Fp8Args& a, void* ws, hipStream_t s) {
+  const Plan c = choose(a, ws != nullptr);
+  Launch l{};
+  l.mt = (a.M + BMS[c.kind] - 1) / BMS[c.kind];
+  l.splits = c.splits;
+  l.counters = static_cast<unsigned*>(ws);
+  l.partial = static_cast<float*>(ws) + COUNTERS;
+  for (int i = 0; i < a.count; i++)
+    l.tile0[i + 1] = l.tile0[i] + l.mt * ((a.p[i].N + BNS[c.kind] - 1) / BNS[c.kind]);
+  const int tiles = l.tile0[a.count];
+  switch (c.kind) {
+    case 0:
+      hipLaunchKernelGGL((k_rows<4>), dim3(tiles), dim3(64 * SW), 0, s, a, l);
+      return hipGetLastError();
+    case 1: return launch_mode<T32>(a, l, tiles, s);
+    case 2: return launch_mode<T64>(a, l, tiles, s);
+    case 3: return launch_mode<T128>(a, l, tiles, s);
+    default: return launch_mode<T256>(a, l, tiles, s);
+  }
 }
 
 }  // namespace rq
