@@ -4,6 +4,8 @@
 #include "rq_fp8.h"
 #include "rq_internal.h"
 
+#include <type_traits>
+
 namespace rq {
 namespace {
 
@@ -233,6 +235,30 @@ __device__ __forceinline__ void store_tile(const Fp8Args& a, const Fp8Problem& p
   }
 }
 
+// A workgroup's tile and range of K.
+struct Where {
+  int problem, tile, split, n0, b0, steps;
+  size_t m0;
+};
+template <typename T>
+__device__ __forceinline__ Where where(const Fp8Args& a, const Launch& l) {
+  // every XCD (workgroups go to them in turn) takes a run of neighbouring tiles,
+  // which share rows of x and w in its L2
+  const u32 total = gridDim.x, xcd = blockIdx.x & 7, each = total >> 3, more = total & 7;
+  const u32 id = xcd * each + min(xcd, more) + (blockIdx.x >> 3);
+  Where o;
+  o.split = id % l.splits;
+  o.tile = id / l.splits;
+  o.problem = 0;
+  while (o.problem + 1 < a.count && o.tile >= l.tile0[o.problem + 1]) o.problem++;
+  const int at = o.tile - l.tile0[o.problem], KB = a.p[o.problem].K / 128;
+  o.n0 = at / l.mt * T::BN;
+  o.m0 = (size_t)(at % l.mt) * T::BM;
+  o.b0 = (int)((long long)KB * o.split / l.splits);
+  o.steps = (int)((long long)KB * (o.split + 1) / l.splits) - o.b0;
+  return o;
+}
+
 template <typename T, Mode MODE>
 __global__ void __launch_bounds__(T::THREADS, T::W / 4 > 0 ? T::W / 4 : 1)
 k_tile(const Fp8Args a, const Launch l) {
@@ -243,19 +269,11 @@ k_tile(const Fp8Args a, const Launch l) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave / T::WM, wm = wave % T::WM;
 
-  // workgroup -> (tile, split): every XCD (workgroups go to them in turn) takes a
-  // run of neighbouring tiles, which share rows of x and w in its L2
-  const u32 total = gridDim.x, xcd = blockIdx.x & 7, each = total >> 3, more = total & 7;
-  const u32 id = xcd * each + min(xcd, more) + (blockIdx.x >> 3);
-  const int split = id % l.splits, tile = id / l.splits;
-  int pi = 0;
-  while (pi + 1 < a.count && tile >= l.tile0[pi + 1]) pi++;
-  const Fp8Problem& p = a.p[pi];
-  const int n0 = (tile - l.tile0[pi]) / l.mt * T::BN;
-  const size_t m0 = (size_t)((tile - l.tile0[pi]) % l.mt) * T::BM;
+  const Where o = where<T>(a, l);
+  const Fp8Problem& p = a.p[o.problem];
+  const int n0 = o.n0, b0 = o.b0, steps = o.steps, split = o.split, tile = o.tile;
+  const size_t m0 = o.m0;
   const int KB = p.K / 128, nb = (p.N + 127) / 128;
-  const int b0 = (int)((long long)KB * split / l.splits);
-  const int steps = (int)((long long)KB * (split + 1) / l.splits) - b0;
   const bool e8m0 = a.e8m0;
 
   // copies of this wave: eight rows of 128 bytes each; slot s of row q holds
@@ -376,6 +394,187 @@ k_tile(const Fp8Args a, const Launch l) {
   store_tile<TM>(a, p, wave_n0, wave_m0, acc);
 }
 
+// Large tiles: eight waves in two groups that take turns, one reading operands
+// from LDS while the other multiplies.  A step (128 columns) is four phases:
+// read x and half of w, multiply, read the other half, multiply; the second group
+// is one phase behind, so that the matrix units of a SIMD, which has a wave of
+// each group, always have work.
+union Op {
+  u32x4 q[2];
+  i8v v;
+};
+
+template <typename V>
+__device__ __forceinline__ void pin(V& v) {
+  asm volatile("" : "+v"(v));
+}
+
+// End of a phase: this wave's LDS accesses are done, then everybody's.
+__device__ __forceinline__ void phase_end() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+template <typename T, Mode MODE>
+__global__ void __launch_bounds__(T::THREADS, 2) k_big(const Fp8Args a, const Launch l) {
+  constexpr int W = T::W, TM = T::TM, SC = T::SC;
+  static_assert(W == 8 && T::ST == 2 && MODE != WIDE, "two groups of four waves");
+  constexpr bool E8 = MODE == FP8E;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  u32* const scales = reinterpret_cast<u32*>(lds + 2 * T::STAGE);
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave / T::WM, wm = wave % T::WM;
+  const Where o = where<T>(a, l);
+  const Fp8Problem& p = a.p[o.problem];
+  const int n0 = o.n0, steps = o.steps;
+  const size_t m0 = o.m0;
+  const int KB = p.K / 128, nb = (p.N + 127) / 128;
+
+  const __amdgpu_buffer_rsrc_t wr = buffer(p.w + (size_t)n0 * p.K + (size_t)o.b0 * 128);
+  const __amdgpu_buffer_rsrc_t xr = buffer(p.x + m0 * p.K + (size_t)o.b0 * 128);
+  const int w_last = p.N - 1 - n0, x_last = (int)min((size_t)a.M - 1 - m0, (size_t)T::BM);
+  u32 off[T::COPIES];
+#pragma unroll
+  for (int c = 0; c < T::COPIES; c++) {
+    const int row = (c * W + wave) * 8 + (lane >> 3);
+    const int q = c < T::WCOPIES ? min(row, w_last) : min(row - T::BN, x_last);
+    off[c] = (u32)q * p.K + (((lane & 7) ^ (lane >> 3)) << 4);
+  }
+  auto copy = [&](int step) {
+    if (step >= steps) return;
+    char* dst = lds + (step & 1) * T::STAGE + wave * 1024;
+#pragma unroll
+    for (int c = 0; c < T::COPIES; c++)
+      lds_copy16(c < T::WCOPIES ? wr : xr, dst + c * W * 1024, off[c], step * 128);
+  };
+  constexpr int PER = T::PER, SPAN = T::THREADS / T::BM;
+  const int srow = tid % T::BM;
+  const size_t xs_row = (m0 + min(srow, x_last)) * KB + o.b0;
+  u32 sx[PER], sw[T::WN][PER];
+  auto load_scales = [&](int first) {
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+      const int b = min(first + tid / T::BM + i * SPAN, steps - 1);
+      sx[i] = load_scale(p.xs, xs_row + b, E8);
+#pragma unroll
+      for (int n = 0; n < T::WN; n++)
+        sw[n][i] = load_scale(p.ws, (size_t)min(n0 / 128 + n, nb - 1) * KB + o.b0 + b, E8);
+    }
+  };
+  auto keep_scales = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+#pragma unroll
+      for (int n = 0; n < T::WN; n++)
+        scales[buf * T::SCALES + ((tid / T::BM + i * SPAN) * T::WN + n) * T::BM + srow] =
+            joint_scale<MODE>(sx[i], sw[n][i], E8);
+  };
+
+  f4 acc[TN][TM];
+#pragma unroll
+  for (int t = 0; t < TN; t++)
+#pragma unroll
+    for (int j = 0; j < TM; j++) acc[t][j] = f4{0, 0, 0, 0};
+  // chunk 4 q + h of a row, in the slot its row's last bits exchange it to
+  const int o0 = r * 128 + ((h ^ (r & 7)) << 4), o1 = r * 128 + (((4 + h) ^ (r & 7)) << 4);
+  const char* const wl = lds + wn * 128 * 128;
+  const char* const xl = lds + T::BN * 128 + wm * TM * 16 * 128;
+  Op x[TM], w[TN / 2];
+  u32 s[TM];
+  auto read_w = [&](int step, int half) {
+    const char* b = wl + (step & 1) * T::STAGE + half * (TN / 2) * 2048;
+#pragma unroll
+    for (int t = 0; t < TN / 2; t++) {
+      w[t].q[0] = *reinterpret_cast<const u32x4*>(b + t * 2048 + o0);
+      w[t].q[1] = *reinterpret_cast<const u32x4*>(b + t * 2048 + o1);
+    }
+  };
+  auto read_x = [&](int step) {
+    const char* b = xl + (step & 1) * T::STAGE;
+#pragma unroll
+    for (int j = 0; j < TM; j++) {
+      x[j].q[0] = *reinterpret_cast<const u32x4*>(b + j * 2048 + o0);
+      x[j].q[1] = *reinterpret_cast<const u32x4*>(b + j * 2048 + o1);
+    }
+    const u32* sp = scales + (step / SC & 1) * T::SCALES + (step % SC * T::WN + wn) * T::BM +
+                    wm * TM * 16 + r;
+#pragma unroll
+    for (int j = 0; j < TM; j++) s[j] = sp[16 * j];
+  };
+  auto multiply_half = [&](auto half) {
+    constexpr int T0 = decltype(half)::value * (TN / 2);
+    __builtin_amdgcn_s_setprio(1);
+    if constexpr (E8) {
+#pragma unroll
+      for (int t = 0; t < TN / 2; t++)
+#pragma unroll
+        for (int j = 0; j < TM; j++)
+          acc[T0 + t][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              w[t].v, x[j].v, acc[T0 + t][j], 0, 0, 0, 127, 0, (int)s[j]);
+    } else {
+      // a product's multiply-adds come two products later, when it is there
+      constexpr int L = 2, N = TN / 2 * TM;
+      f4 d[L + 1];
+#pragma unroll
+      for (int i = 0; i < N + L; i++) {
+        if (i < N) {
+          const f4 z = {0, 0, 0, 0};
+          d[i % (L + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              w[i / TM].v, x[i % TM].v, z, 0, 0, 0, 127, 0, 127);
+        }
+        if (i >= L) {
+          const int q = i - L;
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            acc[T0 + q / TM][q % TM][e] = __builtin_fmaf(d[q % (L + 1)][e], __builtin_bit_cast(float, s[q % TM]),
+                                                         acc[T0 + q / TM][q % TM][e]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // made here: left alone, the compiler moves products over a barrier into
+    // another phase
+#pragma unroll
+    for (int t = 0; t < TN / 2; t++)
+#pragma unroll
+      for (int j = 0; j < TM; j++) pin(acc[T0 + t][j]);
+    __builtin_amdgcn_s_setprio(0);
+  };
+  load_scales(0);
+  copy(0);
+  wait_vm<0>();
+  keep_scales(0);
+  phase_end();
+  // Phase g of the workgroup is phase g % 4 of step g / 4 in the first group and
+  // phase g - 1 in the second.  A stage is last read in phase 4 step + 3 (the
+  // second group's third), so copies into it are allowed from phase 4 (step + 1)
+  // on, which is where both groups begin; the next step is first read one phase
+  // after the second group's third, where both have waited.
+  if (wave >= 4) phase_end();
+  for (int step = 0; step < steps; step++) {
+    copy(step + 1);
+    if (step % SC == 0 && step + SC < steps) load_scales(step + SC);
+    read_x(step);
+    read_w(step, 0);
+    phase_end();
+    multiply_half(std::integral_constant<int, 0>{});
+    phase_end();
+    read_w(step, 1);
+    wait_vm<0>();
+    if (step % SC == SC - 2 && step + 2 < steps) keep_scales((step / SC & 1) ^ 1);
+    phase_end();
+    multiply_half(std::integral_constant<int, 1>{});
+    phase_end();
+  }
+  if (wave < 4) phase_end();
+  store_tile<TM>(a, p, n0 + wn * 128, m0 + wm * TM * 16, acc);
+}
+
 // One row tile, few rows: every wave takes 16 outputs and every 8th block of K,
 // straight from memory to the operands; the eight sums meet in LDS.
 constexpr int SW = 8;
@@ -492,7 +691,12 @@ Plan choose(const Fp8Args& a, bool split) {
 template <typename T, Mode MODE>
 hipError_t launch_tile(const Fp8Args& a, const Launch& l, int tiles, hipStream_t s) {
   static LdsLimit limit;
-  const auto kernel = k_tile<T, MODE>;
+  constexpr bool big = T::W == 8 && MODE != WIDE;
+  void (*kernel)(const Fp8Args, const Launch);
+  if constexpr (big)
+    kernel = k_big<T, MODE>;
+  else
+    kernel = k_tile<T, MODE>;
   const hipError_t e = limit.raise(reinterpret_cast<const void*>(kernel), T::LDS);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, dim3((unsigned)tiles * l.splits), dim3(T::THREADS), T::LDS, s, a, l);
