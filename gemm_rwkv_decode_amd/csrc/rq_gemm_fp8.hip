@@ -5,6 +5,7 @@
 #include "rq_internal.h"
 
 #include <type_traits>
+#include <utility>
 
 namespace rq {
 namespace {
@@ -189,50 +190,152 @@ __device__ __forceinline__ void store4(const Fp8Problem& p, int out, size_t m, i
   }
 }
 
+// f(0), f(1), ... with constants.
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+  each_of(f, std::make_integer_sequence<int, N>{});
+}
+
+// Dword i of quarter h of the wave <-> dword h of quarter i.
+__device__ __forceinline__ void transpose4(u32 (&v)[4]) { span_fix<4>(v); }
+
+// The largest over the four quarters of the wave.
+__device__ __forceinline__ float quarters_max(float v) {
+  u32 a = __builtin_bit_cast(u32, v), b = a;
+  lane_swap16(a, b);
+  v = fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+  a = b = __builtin_bit_cast(u32, v);
+  lane_swap32(a, b);
+  return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+
+// C rows' blocks of 128 outputs, each spread over four lanes (outputs 16 t + 4 h +
+// i), as E4M3 codes of their binary16 values: c[j][t] is tile t's dword of row j,
+// se[j] the biased exponent of its scale.  All rows together, so that a lone wave
+// has independent work.
+template <int C>
+__device__ __forceinline__ void quantize_rows(const f4 (&acc)[TN][C], bool square, u32 (&c)[C][TN],
+                                              u32 (&se)[C]) {
+  h2 z[C][2 * TN];
+  const h2 zero = {0, 0};
+  h2 odd = zero;  // NaN once a value is not finite
+  float top[C];
+#pragma unroll
+  for (int j = 0; j < C; j++) {
+    h2 most = zero;
+#pragma unroll
+    for (int t = 0; t < TN; t++)
+#pragma unroll
+      for (int q = 0; q < 2; q++) {
+        const h2 v = {(_Float16)acc[t][j][2 * q], (_Float16)acc[t][j][2 * q + 1]};
+        odd = __builtin_elementwise_fma(v, zero, odd);
+        z[j][2 * t + q] = square ? __builtin_elementwise_max(v, zero) : v;
+        most = __builtin_elementwise_max(most, square ? z[j][2 * t + q] : as_h2(as_u32(v) & 0x7FFF7FFFu));
+      }
+    top[j] = quarters_max(fmaxf((float)most[0], (float)most[1]));
+    // squares grow with what is squared, so the largest is the largest one's
+    if (square) top[j] *= top[j];
+  }
+  if (__builtin_expect(__any(odd[0] != odd[0] || odd[1] != odd[1]), 0)) {
+    // the largest finite one, and NaN as it is
+#pragma unroll
+    for (int j = 0; j < C; j++) {
+      u32 most = 0;
+#pragma unroll
+      for (int t = 0; t < TN; t++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const _Float16 v = (_Float16)acc[t][j][i];
+          z[j][2 * t + i / 2][i & 1] = square && v < (_Float16)0 ? (_Float16)0 : v;
+          const float f = square ? relu2((float)v) : (float)v;
+          most = max(most, abs_bits(f) < INF_BITS ? abs_bits(f) : 0u);
+        }
+      top[j] = quarters_max(__builtin_bit_cast(float, most));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < C; j++) {
+    se[j] = scale_exponent(__builtin_bit_cast(u32, top[j]) & 0x7FFFFFFFu);
+    const float inv = pow2_bits(254 - se[j]);
+#pragma unroll
+    for (int t = 0; t < TN; t++) {
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        f[i] = (float)z[j][2 * t + i / 2][i & 1];
+        if (square) f[i] *= f[i];
+      }
+      c[j][t] = e4m3x4(f[0], f[1], f[2], f[3], inv);
+    }
+  }
+}
+
 // A wave's 128 outputs of its rows.  Lane l holds rows 16 j + l % 16 and outputs
-// 16 t + 4 (l / 16) + i.
+// 16 t + 4 (l / 16) + i; exchanges between the quarters of the wave make whole
+// 16-byte stores of binary16 and E4M3 outputs.
 template <int TM>
 __device__ __forceinline__ void store_tile(const Fp8Args& a, const Fp8Problem& p, int n0, size_t m0,
                                            const f4 (&acc)[TN][TM]) {
   const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
-#pragma unroll
-  for (int j = 0; j < TM; j++) {
-    const size_t m = m0 + 16 * j + r;
-    if (a.out != OUT_E4M3) {
-      if (m < (size_t)a.M) {
-#pragma unroll
-        for (int t = 0; t < TN; t++) store4(p, a.out, m, n0 + 16 * t + 4 * h, acc[t][j]);
-      }
-      continue;
-    }
-    // the four lanes of a row hold its block
-    float v[TN * 4];
-#pragma unroll
-    for (int t = 0; t < TN; t++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float z = (float)(_Float16)acc[t][j][i];
-        v[4 * t + i] = a.relu2 ? relu2(z) : z;
-      }
-    u32 top = 0;
-#pragma unroll
-    for (int i = 0; i < TN * 4; i++) {
-      const u32 b = abs_bits(v[i]);
-      top = max(top, b < INF_BITS ? b : 0u);
-    }
-    top = max(top, (u32)__shfl_xor((int)top, 16, 64));
-    top = max(top, (u32)__shfl_xor((int)top, 32, 64));
-    const u32 se = scale_exponent(top);
-    const float inv = pow2_bits(254 - se);
-    if (m < (size_t)a.M && n0 < p.N) {
-      uint8_t* y = static_cast<uint8_t*>(p.y) + m * p.N + n0 + 4 * h;
+  if (a.out == OUT_E4M3) {
+    constexpr int C = TM < 2 ? TM : 2;
+    each<TM / C>([&](auto part) {
+      constexpr int j0 = decltype(part)::value * C;
+      f4 rows[TN][C];
+      u32 c[C][TN], se[C];
 #pragma unroll
       for (int t = 0; t < TN; t++)
-        *reinterpret_cast<u32*>(y + 16 * t) =
-            e4m3x4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3], inv);
-      if (h == 0) store_scale(p.ys, m * (p.N / 128) + n0 / 128, se, a.e8m0);
-    }
+#pragma unroll
+        for (int j = 0; j < C; j++) rows[t][j] = acc[t][j0 + j];
+      quantize_rows<C>(rows, a.relu2, c, se);
+#pragma unroll
+      for (int j = 0; j < C; j++) {
+        const size_t m = m0 + 16 * (j0 + j) + r;
+        const bool in = m < (size_t)a.M && n0 < p.N;
+#pragma unroll
+        for (int g = 0; g < TN / 4; g++) {
+          u32 v[4] = {c[j][4 * g], c[j][4 * g + 1], c[j][4 * g + 2], c[j][4 * g + 3]};
+          transpose4(v);
+          if (in)
+            *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(p.y) + m * p.N + n0 + 64 * g + 16 * h) =
+                u32x4{v[0], v[1], v[2], v[3]};
+        }
+        if (in && h == 0) store_scale(p.ys, m * (p.N / 128) + n0 / 128, se[j], a.e8m0);
+      }
+    });
+    return;
   }
+  each<TM>([&](auto column) {
+    constexpr int j = decltype(column)::value;
+    const size_t m = m0 + 16 * j + r;
+    const bool in = m < (size_t)a.M && n0 < p.N;
+    if (a.out == OUT_F16 && p.N % 8 == 0) {
+#pragma unroll
+      for (int g = 0; g < TN / 4; g++) {
+        u32 v[2][4];
+#pragma unroll
+        for (int t = 0; t < 4; t++)
+#pragma unroll
+          for (int q = 0; q < 2; q++) {
+            const f4 d = acc[4 * g + t][j];
+            v[q][t] = as_u32(h2{(_Float16)d[2 * q], (_Float16)d[2 * q + 1]});
+          }
+        transpose4(v[0]);
+        transpose4(v[1]);
+        const int n = n0 + 64 * g + 16 * h;
+        u32x4* y = reinterpret_cast<u32x4*>(static_cast<_Float16*>(p.y) + m * p.N + n);
+        if (in && n < p.N) y[0] = u32x4{v[0][0], v[1][0], v[0][1], v[1][1]};
+        if (in && n + 8 < p.N) y[1] = u32x4{v[0][2], v[1][2], v[0][3], v[1][3]};
+      }
+    } else if (in) {
+#pragma unroll
+      for (int t = 0; t < TN; t++) store4(p, a.out, m, n0 + 16 * t + 4 * h, acc[t][j]);
+    }
+  });
 }
 
 // A workgroup's tile and range of K.
@@ -557,10 +660,11 @@ __global__ void __launch_bounds__(T::THREADS, 2) k_big(const Fp8Args a, const La
   // after the second group's third, where both have waited.
   if (wave >= 4) phase_end();
   for (int step = 0; step < steps; step++) {
-    copy(step + 1);
     if (step % SC == 0 && step + SC < steps) load_scales(step + SC);
     read_x(step);
     read_w(step, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    copy(step + 1);
     phase_end();
     multiply_half(std::integral_constant<int, 0>{});
     phase_end();
