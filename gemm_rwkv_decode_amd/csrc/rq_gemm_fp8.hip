@@ -67,43 +67,100 @@ struct Launch {
   int tile0[FP8_BATCH + 1];  // first tile of each problem
   int mt;                    // tiles of M
   int splits;
-  unsigned* counters;        // one per tile, zero between launches
+  unsigned* counters;        // one per wave of a tile, zero between launches
   float* partial;            // [tile][split][outputs of a tile, as the lanes hold them]
 };
 
-constexpr int TN = 8;  // 16-row tiles of w of a wave: one block of outputs
-
-// WN x WM waves, each 128 outputs of 16 * TM rows; ST stages of 128 columns.
-template <int WN_, int WM_, int TM_, int ST_>
+// WN x WM waves, each 16 TN outputs of 16 TM rows; ST stages of 128 columns.
+template <int WN_, int WM_, int TN_, int TM_, int ST_>
 struct Tile {
-  static constexpr int WN = WN_, WM = WM_, TM = TM_, ST = ST_;
+  static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, ST = ST_;
   static constexpr int W = WN * WM, THREADS = 64 * W;
-  static constexpr int BN = 128 * WN, BM = 16 * TM * WM;
+  static constexpr int BN = 16 * TN * WN, BM = 16 * TM * WM, NB = BN / 128;
   static constexpr int STAGE = (BN + BM) * 128;
   static constexpr int COPIES = (BN + BM) / 8 / W;  // of a wave for a stage
   static constexpr int WCOPIES = BN / 8 / W;        // of these, rows of w
   static constexpr int SC = 4;                      // blocks of K whose scales are staged together
-  static constexpr int SCALES = SC * WN * BM;       // dwords of a buffer of scales
+  static constexpr int SCALES = SC * NB * BM;       // dwords of a buffer of scales
   static constexpr int LDS = ST * STAGE + 2 * SCALES * 4;
-  static_assert((BN + BM) / 8 % W == 0 && BN / 8 % W == 0, "whole copies");
+  static_assert(BN % 128 == 0 && (BN + BM) / 8 % W == 0 && BN / 8 % W == 0, "whole copies");
   static_assert(LDS <= 160 * 1024, "LDS");
-  static constexpr int PER = SC * BM / THREADS;  // scales of x that a thread stages
-  static_assert(SC * BM % THREADS == 0 || SC * BM < THREADS, "scales");
+  static constexpr int ROWS = THREADS / BM > 0 ? THREADS / BM : 1;  // blocks staged at once
+  static constexpr int PER = SC > ROWS ? SC / ROWS : 1;             // scales of x of a thread
+  static_assert(THREADS % BM == 0 && (SC % ROWS == 0 || ROWS % SC == 0), "scales");
 };
+
+union Op {
+  u32x4 q[2];
+  i8v v;
+};
+
+// acc += (a block's products of TN x TM tiles of widened operands) * f, the chains
+// of several tiles side by side: a product waits for the one before it in its chain.
+template <int TN, int TM>
+__device__ __forceinline__ void multiply_wide(const h8 (&w)[TN][2][2], const h8 (&x)[TM][2][2],
+                                              const float (&f)[TM], f4 (&acc)[TN][TM]) {
+  f4 v[TN][TM];
+#pragma unroll
+  for (int t = 0; t < TN; t++)
+#pragma unroll
+    for (int j = 0; j < TM; j++) v[t][j] = f4{0, 0, 0, 0};
+#pragma unroll
+  for (int q = 0; q < 2; q++)
+#pragma unroll
+    for (int e = 0; e < 2; e++)
+#pragma unroll
+      for (int t = 0; t < TN; t++)
+#pragma unroll
+        for (int j = 0; j < TM; j++)
+          v[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t][q][e], x[j][q][e], v[t][j], 0, 0, 0);
+#pragma unroll
+  for (int t = 0; t < TN; t++)
+#pragma unroll
+    for (int j = 0; j < TM; j++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) acc[t][j][i] = __builtin_fmaf(v[t][j][i], f[j], acc[t][j][i]);
+}
+
+// The same for TN tiles of w in LDS from `w` on, G at once.
+template <int TN, int TM>
+__device__ __forceinline__ void multiply_wide(const char* wl, int o0, int o1,
+                                              const h8 (&x)[TM][2][2], const float (&f)[TM],
+                                              f4 (&acc)[TN][TM]) {
+  constexpr int G = TM >= 4 || TN < 2 ? 1 : 2;
+#pragma unroll
+  for (int t = 0; t < TN; t += G) {
+    h8 w[G][2][2];
+    f4 part[G][TM];
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+      widen(*reinterpret_cast<const u32x4*>(wl + (t + g) * 2048 + o0), w[g][0]);
+      widen(*reinterpret_cast<const u32x4*>(wl + (t + g) * 2048 + o1), w[g][1]);
+#pragma unroll
+      for (int j = 0; j < TM; j++) part[g][j] = acc[t + g][j];
+    }
+    multiply_wide<G, TM>(w, x, f, part);
+#pragma unroll
+    for (int g = 0; g < G; g++)
+#pragma unroll
+      for (int j = 0; j < TM; j++) acc[t + g][j] = part[g][j];
+  }
+}
 
 // The products of one block of K from a stage in LDS.
 template <typename T, Mode MODE>
 __device__ __forceinline__ void multiply(const char* stage, const u32* scales, int wn, int wm,
-                                         f4 (&acc)[TN][T::TM]) {
-  constexpr int TM = T::TM;
+                                         f4 (&acc)[T::TN][T::TM]) {
+  constexpr int TN = T::TN, TM = T::TM;
   const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
   // chunk 4 p + h of a row, in the slot its row's last bits exchange it to
   const int o0 = r * 128 + ((h ^ (r & 7)) << 4), o1 = r * 128 + (((4 + h) ^ (r & 7)) << 4);
-  const char* wp = stage + wn * 128 * 128;
+  const char* wp = stage + wn * TN * 16 * 128;
   const char* xp = stage + T::BN * 128 + wm * TM * 16 * 128;
   u32 s[TM];
 #pragma unroll
-  for (int j = 0; j < TM; j++) s[j] = scales[wn * T::BM + (wm * TM + j) * 16 + r];
+  for (int j = 0; j < TM; j++)
+    s[j] = scales[wn * TN / 8 * T::BM + (wm * TM + j) * 16 + r];
   if constexpr (MODE == WIDE) {
     h8 x[TM][2][2];
 #pragma unroll
@@ -111,29 +168,11 @@ __device__ __forceinline__ void multiply(const char* stage, const u32* scales, i
       widen(*reinterpret_cast<const u32x4*>(xp + j * 2048 + o0), x[j][0]);
       widen(*reinterpret_cast<const u32x4*>(xp + j * 2048 + o1), x[j][1]);
     }
+    float f[TM];
 #pragma unroll
-    for (int t = 0; t < TN; t++) {
-      h8 w[2][2];
-      widen(*reinterpret_cast<const u32x4*>(wp + t * 2048 + o0), w[0]);
-      widen(*reinterpret_cast<const u32x4*>(wp + t * 2048 + o1), w[1]);
-#pragma unroll
-      for (int j = 0; j < TM; j++) {
-        f4 d = {0, 0, 0, 0};
-#pragma unroll
-        for (int q = 0; q < 2; q++)
-#pragma unroll
-          for (int e = 0; e < 2; e++)
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[q][e], x[j][q][e], d, 0, 0, 0);
-        const float f = __builtin_bit_cast(float, s[j]);
-#pragma unroll
-        for (int i = 0; i < 4; i++) acc[t][j][i] = __builtin_fmaf(d[i], f, acc[t][j][i]);
-      }
-    }
+    for (int j = 0; j < TM; j++) f[j] = __builtin_bit_cast(float, s[j]);
+    multiply_wide<TN, TM>(wp, o0, o1, x, f, acc);
   } else {
-    union Op {
-      u32x4 q[2];
-      i8v v;
-    };
     Op x[TM];
 #pragma unroll
     for (int j = 0; j < TM; j++) {
@@ -217,10 +256,11 @@ __device__ __forceinline__ float quarters_max(float v) {
 // i), as E4M3 codes of their binary16 values: c[j][t] is tile t's dword of row j,
 // se[j] the biased exponent of its scale.  All rows together, so that a lone wave
 // has independent work.
+constexpr int TB = 8;  // tiles of a block of outputs
 template <int C>
-__device__ __forceinline__ void quantize_rows(const f4 (&acc)[TN][C], bool square, u32 (&c)[C][TN],
+__device__ __forceinline__ void quantize_rows(const f4 (&acc)[TB][C], bool square, u32 (&c)[C][TB],
                                               u32 (&se)[C]) {
-  h2 z[C][2 * TN];
+  h2 z[C][2 * TB];
   const h2 zero = {0, 0};
   h2 odd = zero;  // NaN once a value is not finite
   float top[C];
@@ -228,7 +268,7 @@ __device__ __forceinline__ void quantize_rows(const f4 (&acc)[TN][C], bool squar
   for (int j = 0; j < C; j++) {
     h2 most = zero;
 #pragma unroll
-    for (int t = 0; t < TN; t++)
+    for (int t = 0; t < TB; t++)
 #pragma unroll
       for (int q = 0; q < 2; q++) {
         const h2 v = {(_Float16)acc[t][j][2 * q], (_Float16)acc[t][j][2 * q + 1]};
@@ -246,7 +286,7 @@ __device__ __forceinline__ void quantize_rows(const f4 (&acc)[TN][C], bool squar
     for (int j = 0; j < C; j++) {
       u32 most = 0;
 #pragma unroll
-      for (int t = 0; t < TN; t++)
+      for (int t = 0; t < TB; t++)
 #pragma unroll
         for (int i = 0; i < 4; i++) {
           const _Float16 v = (_Float16)acc[t][j][i];
@@ -262,7 +302,7 @@ __device__ __forceinline__ void quantize_rows(const f4 (&acc)[TN][C], bool squar
     se[j] = scale_exponent(__builtin_bit_cast(u32, top[j]) & 0x7FFFFFFFu);
     const float inv = pow2_bits(254 - se[j]);
 #pragma unroll
-    for (int t = 0; t < TN; t++) {
+    for (int t = 0; t < TB; t++) {
       float f[4];
 #pragma unroll
       for (int i = 0; i < 4; i++) {
@@ -279,16 +319,16 @@ __device__ __forceinline__ void quantize_rows(const f4 (&acc)[TN][C], bool squar
 // 16-byte stores of binary16 and E4M3 outputs.
 template <int TM>
 __device__ __forceinline__ void store_tile(const Fp8Args& a, const Fp8Problem& p, int n0, size_t m0,
-                                           const f4 (&acc)[TN][TM]) {
+                                           const f4 (&acc)[TB][TM]) {
   const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
   if (a.out == OUT_E4M3) {
     constexpr int C = TM < 2 ? TM : 2;
     each<TM / C>([&](auto part) {
       constexpr int j0 = decltype(part)::value * C;
-      f4 rows[TN][C];
-      u32 c[C][TN], se[C];
+      f4 rows[TB][C];
+      u32 c[C][TB], se[C];
 #pragma unroll
-      for (int t = 0; t < TN; t++)
+      for (int t = 0; t < TB; t++)
 #pragma unroll
         for (int j = 0; j < C; j++) rows[t][j] = acc[t][j0 + j];
       quantize_rows<C>(rows, a.relu2, c, se);
@@ -297,7 +337,7 @@ __device__ __forceinline__ void store_tile(const Fp8Args& a, const Fp8Problem& p
         const size_t m = m0 + 16 * (j0 + j) + r;
         const bool in = m < (size_t)a.M && n0 < p.N;
 #pragma unroll
-        for (int g = 0; g < TN / 4; g++) {
+        for (int g = 0; g < TB / 4; g++) {
           u32 v[4] = {c[j][4 * g], c[j][4 * g + 1], c[j][4 * g + 2], c[j][4 * g + 3]};
           transpose4(v);
           if (in)
@@ -315,7 +355,7 @@ __device__ __forceinline__ void store_tile(const Fp8Args& a, const Fp8Problem& p
     const bool in = m < (size_t)a.M && n0 < p.N;
     if (a.out == OUT_F16 && p.N % 8 == 0) {
 #pragma unroll
-      for (int g = 0; g < TN / 4; g++) {
+      for (int g = 0; g < TB / 4; g++) {
         u32 v[2][4];
 #pragma unroll
         for (int t = 0; t < 4; t++)
@@ -333,7 +373,7 @@ __device__ __forceinline__ void store_tile(const Fp8Args& a, const Fp8Problem& p
       }
     } else if (in) {
 #pragma unroll
-      for (int t = 0; t < TN; t++) store4(p, a.out, m, n0 + 16 * t + 4 * h, acc[t][j]);
+      for (int t = 0; t < TB; t++) store4(p, a.out, m, n0 + 16 * t + 4 * h, acc[t][j]);
     }
   });
 }
@@ -343,8 +383,7 @@ struct Where {
   int problem, tile, split, n0, b0, steps;
   size_t m0;
 };
-template <typename T>
-__device__ __forceinline__ Where where(const Fp8Args& a, const Launch& l) {
+__device__ __forceinline__ Where where(const Fp8Args& a, const Launch& l, int bn, int bm) {
   // every XCD (workgroups go to them in turn) takes a run of neighbouring tiles,
   // which share rows of x and w in its L2
   const u32 total = gridDim.x, xcd = blockIdx.x & 7, each = total >> 3, more = total & 7;
@@ -355,29 +394,43 @@ __device__ __forceinline__ Where where(const Fp8Args& a, const Launch& l) {
   o.problem = 0;
   while (o.problem + 1 < a.count && o.tile >= l.tile0[o.problem + 1]) o.problem++;
   const int at = o.tile - l.tile0[o.problem], KB = a.p[o.problem].K / 128;
-  o.n0 = at / l.mt * T::BN;
-  o.m0 = (size_t)(at % l.mt) * T::BM;
+  o.n0 = at / l.mt * bn;
+  o.m0 = (size_t)(at % l.mt) * bm;
   o.b0 = (int)((long long)KB * o.split / l.splits);
   o.steps = (int)((long long)KB * (o.split + 1) / l.splits) - o.b0;
   return o;
 }
 
-template <typename T, Mode MODE>
-__global__ void __launch_bounds__(T::THREADS, T::W / 4 > 0 ? T::W / 4 : 1)
+template <typename V>
+__device__ __forceinline__ void pin(V& v) {
+  asm volatile("" : "+v"(v));
+}
+
+// End of a phase or step (loads of later ones stay in flight): this wave's LDS accesses are done, then everybody's.
+__device__ __forceinline__ void phase_end() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+template <typename T, Mode MODE, bool E8>
+__global__ void __launch_bounds__(T::THREADS, T::W / 2 > 0 ? T::W / 2 : 1)
 k_tile(const Fp8Args a, const Launch l) {
-  constexpr int W = T::W, TM = T::TM, ST = T::ST, SC = T::SC;
+  constexpr int W = T::W, TN = T::TN, TM = T::TM, ST = T::ST, SC = T::SC;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   u32* const scales = reinterpret_cast<u32*>(lds + ST * T::STAGE);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave / T::WM, wm = wave % T::WM;
 
-  const Where o = where<T>(a, l);
+  const Where o = where(a, l, T::BN, T::BM);
   const Fp8Problem& p = a.p[o.problem];
   const int n0 = o.n0, b0 = o.b0, steps = o.steps, split = o.split, tile = o.tile;
   const size_t m0 = o.m0;
   const int KB = p.K / 128, nb = (p.N + 127) / 128;
-  const bool e8m0 = a.e8m0;
 
   // copies of this wave: eight rows of 128 bytes each; slot s of row q holds
   // chunk s ^ (q % 8), so that the reads of 16 rows' equal chunks spread over all
@@ -400,31 +453,28 @@ k_tile(const Fp8Args a, const Launch l) {
   };
 
   // scales of SC blocks: thread -> row of x and blocks
-  constexpr int PER = T::PER > 0 ? T::PER : 1;
-  const int srow = tid % T::BM;
-  const bool stager = T::PER > 0 || tid < SC * T::BM;
+  const int srow = tid % T::BM, sblock = tid / T::BM;
   const size_t xs_row = (m0 + min(srow, x_last)) * KB + b0;
-  u32 sx[PER], sw[T::WN][PER];
+  u32 sx[T::PER], sw[T::NB][T::PER];
   auto load_scales = [&](int first) {
 #pragma unroll
-    for (int i = 0; i < PER; i++) {
-      const int b = min(first + tid / T::BM + i * (T::THREADS / T::BM > 0 ? T::THREADS / T::BM : 1),
-                        steps - 1);
-      sx[i] = load_scale(p.xs, xs_row + b, e8m0);
+    for (int i = 0; i < T::PER; i++) {
+      const int b = min(first + sblock + i * T::ROWS, steps - 1);
+      sx[i] = load_scale(p.xs, xs_row + b, E8);
 #pragma unroll
-      for (int n = 0; n < T::WN; n++)
-        sw[n][i] = load_scale(p.ws, (size_t)min(n0 / 128 + n, nb - 1) * KB + b0 + b, e8m0);
+      for (int n = 0; n < T::NB; n++)
+        sw[n][i] = load_scale(p.ws, (size_t)min(n0 / 128 + n, nb - 1) * KB + b0 + b, E8);
     }
   };
   auto keep_scales = [&](int buf) {
 #pragma unroll
-    for (int i = 0; i < PER; i++) {
-      const int b = tid / T::BM + i * (T::THREADS / T::BM > 0 ? T::THREADS / T::BM : 1);
+    for (int i = 0; i < T::PER; i++) {
+      const int b = sblock + i * T::ROWS;
 #pragma unroll
-      for (int n = 0; n < T::WN; n++)
-        if (stager)
-          scales[buf * T::SCALES + (b * T::WN + n) * T::BM + srow] =
-              joint_scale<MODE>(sx[i], sw[n][i], e8m0);
+      for (int n = 0; n < T::NB; n++)
+        if (b < SC)
+          scales[buf * T::SCALES + (b * T::NB + n) * T::BM + srow] =
+              joint_scale<MODE>(sx[i], sw[n][i], E8);
     }
   };
 
@@ -446,55 +496,78 @@ k_tile(const Fp8Args a, const Launch l) {
       wait_vm<(ST - 2) * T::COPIES>();
     else
       wait_vm<0>();
-    __syncthreads();
+    phase_end();
     if (s + ST - 1 < steps) copy(s + ST - 1);
     if (s % SC == 0 && s + SC < steps) load_scales(s + SC);
     multiply<T, MODE>(lds + s % ST * T::STAGE,
-                      scales + (s / SC & 1) * T::SCALES + s % SC * T::WN * T::BM, wn, wm, acc);
+                      scales + (s / SC & 1) * T::SCALES + s % SC * T::NB * T::BM, wn, wm, acc);
     if (s % SC == SC / 2 && s - s % SC + SC < steps) keep_scales((s / SC & 1) ^ 1);
   }
 
-  const int wave_n0 = n0 + wn * 128;
+  const int wave_n0 = n0 + wn * TN * 16;
   const size_t wave_m0 = m0 + wm * TM * 16;
   if (l.splits > 1) {
-    // this range's sums, as the lanes hold them, past the caches that other XCDs
-    // do not see; then the arrival.  The last to arrive adds the ranges in order.
-    constexpr int PART = T::BN * T::BM;
-    float* mine = l.partial + ((size_t)tile * l.splits) * PART;
-    const __amdgpu_buffer_rsrc_t pr = buffer(mine);
-    constexpr int AGENT = 16;  // scope bit of the buffer instructions
+    // This range's sums, as the lanes hold them, past the caches that other XCDs do
+    // not see; then the wave's arrival at its part of the tile.  The last of the
+    // ranges' waves to arrive adds them in order, the sums of several ranges asked
+    // for together.
+    constexpr int PART = T::BN * T::BM, AGENT = 16;  // scope bit of the buffer instructions
+    const __amdgpu_buffer_rsrc_t pr = buffer(l.partial + (size_t)tile * l.splits * PART);
+    const u32 lane_at = (wave * 256 + lane * 4) * 4;
 #pragma unroll
     for (int t = 0; t < TN; t++)
 #pragma unroll
       for (int j = 0; j < TM; j++)
-        __builtin_amdgcn_raw_buffer_store_b128(
-            __builtin_bit_cast(u32x4, acc[t][j]), pr,
-            (split * PART + ((t * TM + j) * W + wave) * 256 + lane * 4) * 4, 0, AGENT);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[t][j]), pr,
+                                               lane_at + (split * PART + (t * TM + j) * W * 256) * 4, 0,
+                                               AGENT);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
     wait_vm<0>();
-    __syncthreads();
-    unsigned* const flag = reinterpret_cast<unsigned*>(lds);
-    if (tid == 0)
-      *flag = __hip_atomic_fetch_add(l.counters + tile, 1u, __ATOMIC_RELAXED,
-                                     __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (*flag != (unsigned)(l.splits - 1)) return;
-    if (tid == 0)
-      __hip_atomic_store(l.counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    unsigned* const counter = l.counters + tile * W + wave;
+    unsigned before = 0;
+    if (lane == 0)
+      before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__builtin_amdgcn_readfirstlane(before) != (unsigned)(l.splits - 1)) return;
+    if (lane == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
     for (int t = 0; t < TN; t++)
 #pragma unroll
       for (int j = 0; j < TM; j++) acc[t][j] = f4{0, 0, 0, 0};
-    for (int q = 0; q < l.splits; q++) {
+    constexpr int SB = TN * TM > 16 ? 1 : 32 / (TN * TM) > 4 ? 4 : 32 / (TN * TM);
+    for (int q0 = 0; q0 < l.splits; q0 += SB) {
+      u32x4 v[SB][TN][TM];
 #pragma unroll
-      for (int t = 0; t < TN; t++)
+      for (int q = 0; q < SB; q++)
 #pragma unroll
-        for (int j = 0; j < TM; j++)
-          acc[t][j] += __builtin_bit_cast(
-              f4, __builtin_amdgcn_raw_buffer_load_b128(
-                      pr, (q * PART + ((t * TM + j) * W + wave) * 256 + lane * 4) * 4, 0, AGENT));
+        for (int t = 0; t < TN; t++)
+#pragma unroll
+          for (int j = 0; j < TM; j++)
+            v[q][t][j] = __builtin_amdgcn_raw_buffer_load_b128(
+                pr, lane_at + (min(q0 + q, l.splits - 1) * PART + (t * TM + j) * W * 256) * 4, 0, AGENT);
+#pragma unroll
+      for (int q = 0; q < SB; q++) {
+        if (q0 + q >= l.splits) break;
+#pragma unroll
+        for (int t = 0; t < TN; t++)
+#pragma unroll
+          for (int j = 0; j < TM; j++) acc[t][j] += __builtin_bit_cast(f4, v[q][t][j]);
+      }
     }
   }
-  store_tile<TM>(a, p, wave_n0, wave_m0, acc);
+  if constexpr (MODE != WIDE) {
+    store_tile<TM>(a, p, wave_n0, wave_m0, acc);
+  } else {
+    const int r = lane & 15, h = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < TM; j++) {
+      const size_t m = wave_m0 + 16 * j + r;
+      if (m < (size_t)a.M) {
+#pragma unroll
+        for (int t = 0; t < TN; t++) store4(p, OUT_F32, m, wave_n0 + 16 * t + 4 * h, acc[t][j]);
+      }
+    }
+  }
 }
 
 // Large tiles: eight waves in two groups that take turns, one reading operands
@@ -502,37 +575,18 @@ k_tile(const Fp8Args a, const Launch l) {
 // read x and half of w, multiply, read the other half, multiply; the second group
 // is one phase behind, so that the matrix units of a SIMD, which has a wave of
 // each group, always have work.
-union Op {
-  u32x4 q[2];
-  i8v v;
-};
-
-template <typename V>
-__device__ __forceinline__ void pin(V& v) {
-  asm volatile("" : "+v"(v));
-}
-
-// End of a phase: this wave's LDS accesses are done, then everybody's.
-__device__ __forceinline__ void phase_end() {
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-}
 
 template <typename T, Mode MODE>
 __global__ void __launch_bounds__(T::THREADS, 2) k_big(const Fp8Args a, const Launch l) {
-  constexpr int W = T::W, TM = T::TM, SC = T::SC;
-  static_assert(W == 8 && T::ST == 2 && MODE != WIDE, "two groups of four waves");
+  constexpr int W = T::W, TN = T::TN, TM = T::TM, SC = T::SC;
+  static_assert(W == 8 && TN == 8 && T::ST == 2 && MODE != WIDE, "two groups of four waves");
   constexpr bool E8 = MODE == FP8E;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   u32* const scales = reinterpret_cast<u32*>(lds + 2 * T::STAGE);
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave / T::WM, wm = wave % T::WM;
-  const Where o = where<T>(a, l);
+  const Where o = where(a, l, T::BN, T::BM);
   const Fp8Problem& p = a.p[o.problem];
   const int n0 = o.n0, steps = o.steps;
   const size_t m0 = o.m0;
@@ -555,17 +609,17 @@ __global__ void __launch_bounds__(T::THREADS, 2) k_big(const Fp8Args a, const La
     for (int c = 0; c < T::COPIES; c++)
       lds_copy16(c < T::WCOPIES ? wr : xr, dst + c * W * 1024, off[c], step * 128);
   };
-  constexpr int PER = T::PER, SPAN = T::THREADS / T::BM;
+  constexpr int PER = T::PER, SPAN = T::ROWS;
   const int srow = tid % T::BM;
   const size_t xs_row = (m0 + min(srow, x_last)) * KB + o.b0;
-  u32 sx[PER], sw[T::WN][PER];
+  u32 sx[PER], sw[T::NB][PER];
   auto load_scales = [&](int first) {
 #pragma unroll
     for (int i = 0; i < PER; i++) {
       const int b = min(first + tid / T::BM + i * SPAN, steps - 1);
       sx[i] = load_scale(p.xs, xs_row + b, E8);
 #pragma unroll
-      for (int n = 0; n < T::WN; n++)
+      for (int n = 0; n < T::NB; n++)
         sw[n][i] = load_scale(p.ws, (size_t)min(n0 / 128 + n, nb - 1) * KB + o.b0 + b, E8);
     }
   };
@@ -573,8 +627,8 @@ __global__ void __launch_bounds__(T::THREADS, 2) k_big(const Fp8Args a, const La
 #pragma unroll
     for (int i = 0; i < PER; i++)
 #pragma unroll
-      for (int n = 0; n < T::WN; n++)
-        scales[buf * T::SCALES + ((tid / T::BM + i * SPAN) * T::WN + n) * T::BM + srow] =
+      for (int n = 0; n < T::NB; n++)
+        scales[buf * T::SCALES + ((tid / T::BM + i * SPAN) * T::NB + n) * T::BM + srow] =
             joint_scale<MODE>(sx[i], sw[n][i], E8);
   };
 
@@ -604,7 +658,7 @@ __global__ void __launch_bounds__(T::THREADS, 2) k_big(const Fp8Args a, const La
       x[j].q[0] = *reinterpret_cast<const u32x4*>(b + j * 2048 + o0);
       x[j].q[1] = *reinterpret_cast<const u32x4*>(b + j * 2048 + o1);
     }
-    const u32* sp = scales + (step / SC & 1) * T::SCALES + (step % SC * T::WN + wn) * T::BM +
+    const u32* sp = scales + (step / SC & 1) * T::SCALES + (step % SC * T::NB + wn) * T::BM +
                     wm * TM * 16 + r;
 #pragma unroll
     for (int j = 0; j < TM; j++) s[j] = sp[16 * j];
@@ -679,84 +733,225 @@ __global__ void __launch_bounds__(T::THREADS, 2) k_big(const Fp8Args a, const La
   store_tile<TM>(a, p, n0 + wn * 128, m0 + wm * TM * 16, acc);
 }
 
-// One row tile, few rows: every wave takes 16 outputs and every 8th block of K,
-// straight from memory to the operands; the eight sums meet in LDS.
+// Up to 16 rows, binary32 outputs: a workgroup takes 16 TW outputs and its eight
+// waves every eighth block of K, from memory straight to the operands, D blocks ahead;
+// the eight sums meet in LDS.  No wave waits for another before that.
 constexpr int SW = 8;
-template <int U>
+template <int TW>
+struct Block {
+  u32x4 w[TW][2], x[2];
+  u32 sx, sw;
+};
+
+template <int TW, int D, bool E8>
 __global__ void __launch_bounds__(64 * SW, 2) k_rows(const Fp8Args a, const Launch l) {
-  __shared__ f4 sums[SW][64];
+  __shared__ f4 sums[SW][TW][64];
   const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = blockIdx.x;
-  int pi = 0;
-  while (pi + 1 < a.count && tile >= l.tile0[pi + 1]) pi++;
-  const Fp8Problem& p = a.p[pi];
-  const int n0 = (tile - l.tile0[pi]) * 16, KB = p.K / 128;
-  const bool e8m0 = a.e8m0;
-  const uint8_t* wp = p.w + (size_t)min(n0 + r, p.N - 1) * p.K + 16 * h;
-  const int mc = min(r, a.M - 1);
-  const uint8_t* xp = p.x + (size_t)mc * p.K + 16 * h;
-  f4 acc = {0, 0, 0, 0};
-  for (int b = wave; b < KB; b += SW * U) {
-    u32x4 w[U][2], x[U][2];
-    u32 sx[U], sw[U];
+  const Where o = where(a, l, 16 * TW, 16);
+  const Fp8Problem& p = a.p[o.problem];
+  const int n0 = o.n0, KB = p.K / 128;
+  const uint8_t* wp[TW];
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int bu = min(b + u * SW, KB - 1);
+  for (int t = 0; t < TW; t++) wp[t] = p.w + (size_t)min(n0 + 16 * t + r, p.N - 1) * p.K + 16 * h;
+  const size_t m = min(r, a.M - 1);  // rows past the end repeat the last one
+  const uint8_t* xp = p.x + m * p.K + 16 * h;
+  const size_t xs = m * KB, ws = (size_t)(n0 / 128) * KB;
+  Block<TW> ring[D];
+  auto load = [&](Block<TW>& v, int b) {
+    const size_t at = (size_t)b * 128;
+#pragma unroll
+    for (int t = 0; t < TW; t++)
 #pragma unroll
       for (int q = 0; q < 2; q++)
-        w[u][q] = load_stream16(wp + (size_t)bu * 128 + 64 * q);
-    }
+        v.w[t][q] = *reinterpret_cast<const u32x4*>(wp[t] + at + 64 * q);
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int bu = min(b + u * SW, KB - 1);
+    for (int q = 0; q < 2; q++) v.x[q] = *reinterpret_cast<const u32x4*>(xp + at + 64 * q);
+    v.sx = load_scale(p.xs, xs + b, E8);
+    v.sw = load_scale(p.ws, ws + b, E8);
+  };
+  f4 acc[TW][1];
 #pragma unroll
-      for (int q = 0; q < 2; q++)
-        x[u][q] = *reinterpret_cast<const u32x4*>(xp + (size_t)bu * 128 + 64 * q);
-      sx[u] = load_scale(p.xs, (size_t)mc * KB + bu, e8m0);
-      sw[u] = load_scale(p.ws, (size_t)(n0 / 128) * KB + bu, e8m0);
-    }
+  for (int t = 0; t < TW; t++) acc[t][0] = f4{0, 0, 0, 0};
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-      if (b + u * SW >= KB) break;
-      f4 d = {0, 0, 0, 0};
+  for (int d = 0; d < D; d++)
+    if (wave + d * SW < KB) load(ring[d], wave + d * SW);
+  for (int b0 = wave; b0 < KB; b0 += D * SW) {
+#pragma unroll
+    for (int d = 0; d < D; d++) {
+      const int b = b0 + d * SW;
+      if (b >= KB) break;
+      h8 w[TW][2][2], x[1][2][2];
 #pragma unroll
       for (int q = 0; q < 2; q++) {
-        h8 wh[2], xh[2];
-        widen(w[u][q], wh);
-        widen(x[u][q], xh);
-        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(wh[0], xh[0], d, 0, 0, 0);
-        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(wh[1], xh[1], d, 0, 0, 0);
-      }
-      const float f = __builtin_bit_cast(float, joint_scale<WIDE>(sx[u], sw[u], e8m0));
 #pragma unroll
-      for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(d[i], f, acc[i]);
+        for (int t = 0; t < TW; t++) widen(ring[d].w[t][q], w[t][q]);
+        widen(ring[d].x[q], x[0][q]);
+      }
+      const float f[1] = {
+          __builtin_bit_cast(float, joint_scale<WIDE>(ring[d].sx, ring[d].sw, E8))};
+      multiply_wide<TW, 1>(w, x, f, acc);
+      if (b + D * SW < KB) load(ring[d], b + D * SW);
     }
   }
-  sums[wave][lane] = acc;
-  __syncthreads();
-  if (wave != 0) return;
 #pragma unroll
-  for (int w = 1; w < SW; w++) acc += sums[w][lane];
-  if (r < a.M && n0 + 4 * h < p.N) store4(p, a.out, r, n0 + 4 * h, acc);
+  for (int t = 0; t < TW; t++) sums[wave][t][lane] = acc[t][0];
+  __syncthreads();
+  for (int t = wave; t < TW; t += SW) {
+    f4 v = sums[0][t][lane];
+#pragma unroll
+    for (int w = 1; w < SW; w++) v += sums[w][t][lane];
+    const int n = n0 + 16 * t + 4 * h;
+    if (r < a.M && n < p.N) store4(p, OUT_F32, r, n, v);
+  }
 }
 
-typedef Tile<2, 4, 4, 2> T256;  // 256 x 256
-typedef Tile<1, 4, 2, 2> T128;  // 128 outputs x 128 rows
-typedef Tile<1, 4, 1, 3> T64;   // 128 x 64
-typedef Tile<1, 2, 1, 4> T32;   // 128 x 32
+template <int TW, int D>
+hipError_t launch_rows(const Fp8Args& a, const Launch& l, int tiles, hipStream_t s) {
+  if (a.e8m0)
+    hipLaunchKernelGGL((k_rows<TW, D, true>), dim3(tiles), dim3(64 * SW), 0, s, a, l);
+  else
+    hipLaunchKernelGGL((k_rows<TW, D, false>), dim3(tiles), dim3(64 * SW), 0, s, a, l);
+  return hipGetLastError();
+}
 
+// Some rows, binary32 outputs: a workgroup takes 16 TN outputs of 16 TM rows, and
+// each of its eight waves every eighth block of K through a ring of ST stages in LDS
+// of its own; the eight sums meet at the end.  No wave waits for another before that, and
+// no sums go through memory.
+template <int TN, int TM, int ST, bool E8>
+__global__ void __launch_bounds__(64 * SW, 2) k_ring(const Fp8Args a, const Launch l) {
+  constexpr int W = SW;
+  constexpr int STAGE = (TN + TM) * 2048, COPIES = 2 * (TN + TM), OPS = COPIES + TM + 1;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Where o = where(a, l, 16 * TN, 16 * TM);
+  const Fp8Problem& p = a.p[o.problem];
+  const int n0 = o.n0, KB = p.K / 128;
+  const size_t m0 = o.m0;
+  char* const ring = lds + wave * ST * STAGE;
+  const __amdgpu_buffer_rsrc_t wr = buffer(p.w + (size_t)n0 * p.K);
+  const __amdgpu_buffer_rsrc_t xr = buffer(p.x + m0 * p.K);
+  const int w_last = p.N - 1 - n0, x_last = (int)min((size_t)a.M - 1 - m0, (size_t)16 * TM);
+  u32 off[COPIES];
+#pragma unroll
+  for (int c = 0; c < COPIES; c++) {
+    const int row = c * 8 + (lane >> 3);
+    const int q = c < 2 * TN ? min(row, w_last) : min(row - 16 * TN, x_last);
+    off[c] = (u32)q * p.K + (((lane & 7) ^ (lane >> 3)) << 4);
+  }
+  size_t xs[TM];
+#pragma unroll
+  for (int j = 0; j < TM; j++) xs[j] = (m0 + min(16 * j + r, x_last)) * KB;
+  const size_t ws = (size_t)(n0 / 128) * KB;
+  u32 sx[ST][TM], sw[ST];
+  // the wave's step i in slot d; past its last one, the last block again, so that
+  // every step has the same loads behind it
+  auto ask = [&](int i, int d) {
+    const int b = min(wave + i * W, KB - 1);
+#pragma unroll
+    for (int c = 0; c < COPIES; c++)
+      lds_copy16(c < 2 * TN ? wr : xr, ring + d * STAGE + c * 1024, off[c], b * 128);
+#pragma unroll
+    for (int j = 0; j < TM; j++) sx[d][j] = load_scale(p.xs, xs[j] + b, E8);
+    sw[d] = load_scale(p.ws, ws + b, E8);
+    __builtin_amdgcn_sched_barrier(0);  // the order that the waits count on
+  };
+  f4 acc[TN][TM];
+#pragma unroll
+  for (int t = 0; t < TN; t++)
+#pragma unroll
+    for (int j = 0; j < TM; j++) acc[t][j] = f4{0, 0, 0, 0};
+  const int o0 = r * 128 + ((h ^ (r & 7)) << 4), o1 = r * 128 + (((4 + h) ^ (r & 7)) << 4);
+  const int n = (KB - wave + W - 1) / W;
+#pragma unroll
+  for (int d = 0; d < ST; d++) ask(d, d);
+  for (int i = 0; i < n; i += ST) {
+#pragma unroll
+    for (int d = 0; d < ST; d++) {
+      if (i + d >= n) break;
+      __builtin_amdgcn_sched_barrier(0);
+      wait_vm<(ST - 1) * OPS>();
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      const char* const st = ring + d * STAGE;
+      h8 x[TM][2][2];
+#pragma unroll
+      for (int j = 0; j < TM; j++) {
+        widen(*reinterpret_cast<const u32x4*>(st + (TN + j) * 2048 + o0), x[j][0]);
+        widen(*reinterpret_cast<const u32x4*>(st + (TN + j) * 2048 + o1), x[j][1]);
+      }
+      float f[TM];
+#pragma unroll
+      for (int j = 0; j < TM; j++)
+        f[j] = __builtin_bit_cast(float, joint_scale<WIDE>(sx[d][j], sw[d], E8));
+      multiply_wide<TN, TM>(st, o0, o1, x, f, acc);
+      // the slot has been read
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
+      __builtin_amdgcn_sched_barrier(0);
+      ask(i + d + ST, d);
+    }
+  }
+  wait_vm<0>();
+  __syncthreads();
+  f4* const sums = reinterpret_cast<f4*>(lds);
+#pragma unroll
+  for (int t = 0; t < TN; t++)
+#pragma unroll
+    for (int j = 0; j < TM; j++) sums[((t * TM + j) * W + wave) * 64 + lane] = acc[t][j];
+  __syncthreads();
+  for (int c = wave; c < TN * TM; c += W) {
+    f4 v = sums[c * W * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < W; w++) v += sums[(c * W + w) * 64 + lane];
+    const size_t m = m0 + 16 * (c % TM) + r;
+    const int at = n0 + 16 * (c / TM) + 4 * h;
+    if (m < (size_t)a.M && at < p.N) store4(p, OUT_F32, m, at, v);
+  }
+}
+
+template <int TN, int TM, int ST>
+hipError_t launch_ring(const Fp8Args& a, const Launch& l, int tiles, hipStream_t s) {
+  constexpr int BYTES = SW * ST * (TN + TM) * 2048;
+  static_assert(BYTES <= 160 * 1024 && SW * TN * TM * 1024 <= BYTES, "LDS");
+  static LdsLimit limits[2];
+  const auto kernel = a.e8m0 ? k_ring<TN, TM, ST, true> : k_ring<TN, TM, ST, false>;
+  const hipError_t e = limits[a.e8m0 != 0].raise(reinterpret_cast<const void*>(kernel), BYTES);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3(tiles), dim3(64 * SW), BYTES, s, a, l);
+  return hipGetLastError();
+}
+
+// FP8 operands: 128 outputs a wave, so that a row's block is one wave's
+typedef Tile<2, 4, 8, 4, 2> T256;  // 256 outputs x 256 rows
+typedef Tile<1, 4, 8, 2, 2> T128;  // 128 x 128
+typedef Tile<1, 4, 8, 1, 3> T64;   // 128 x 64
+typedef Tile<1, 2, 8, 1, 3> T32;   // 128 x 32
+// binary16 operands, widened by every wave that reads them: as square as they go
+typedef Tile<2, 4, 4, 2, 2> W128;  // 128 x 128
+typedef Tile<4, 2, 2, 2, 3> W64;   // 128 x 64
+
+// What a call runs: a kernel with its tile, and the ranges of K.
+enum Kind { ROWS16, ROWS64, RING16, RING32, RING64, WIDE64, WIDE128, FP32R, FP64R, FP128, FP256 };
+struct Shape {
+  int bn, bm, waves;
+};
+constexpr Shape SHAPES[] = {{16, 16, 8},  {64, 16, 8},   {16, 32, 8},  {32, 32, 8},
+                            {64, 64, 8},  {128, 64, 8},  {128, 128, 8}, {128, 32, 2},
+                            {128, 64, 4}, {128, 128, 4}, {256, 256, 8}};
 struct Plan {
-  int kind;  // 0 k_rows, 1 T32, 2 T64, 3 T128, 4 T256
+  Kind kind;
   int splits;
 };
-constexpr int BNS[] = {16, 128, 128, 128, 256}, BMS[] = {16, 32, 64, 128, 256};
+constexpr int CUS = 256;
 
-int tiles_of(const Fp8Args& a, int kind) {
+long long tiles_of(const Fp8Args& a, Kind kind) {
+  const Shape& s = SHAPES[kind];
   long long n = 0;
   for (int i = 0; i < a.count; i++)
-    n += (long long)((a.M + BMS[kind] - 1) / BMS[kind]) * ((a.p[i].N + BNS[kind] - 1) / BNS[kind]);
-  return n > (1 << 30) ? 1 << 30 : (int)n;
+    n += (long long)((a.M + s.bm - 1) / s.bm) * ((a.p[i].N + s.bn - 1) / s.bn);
+  return n;
 }
 
 constexpr int COUNTERS = 16384;  // arrival counters at the front of a workspace
@@ -764,43 +959,54 @@ constexpr size_t WS_MAX = (size_t)64 << 20;
 
 size_t plan_bytes(const Fp8Args& a, const Plan& c) {
   if (c.splits <= 1) return 0;
-  return COUNTERS * 4 + (size_t)tiles_of(a, c.kind) * c.splits * BNS[c.kind] * BMS[c.kind] * 4;
+  const Shape& s = SHAPES[c.kind];
+  return COUNTERS * 4 + (size_t)tiles_of(a, c.kind) * c.splits * s.bn * s.bm * 4;
+}
+
+// Binary32 outputs: the kernel follows from M and the numbers of tiles.
+Kind choose_wide(const Fp8Args& a) {
+  if (a.M <= 16) return a.M > 4 && tiles_of(a, ROWS64) >= 192 ? ROWS64 : ROWS16;
+  if (a.M <= 64 && tiles_of(a, WIDE64) >= 2 * CUS) return WIDE64;
+  if (tiles_of(a, WIDE128) >= CUS) return WIDE128;
+  int kb = 0;
+  for (int i = 0; i < a.count; i++) kb = a.p[i].K / 128 > kb ? a.p[i].K / 128 : kb;
+  // rounds of workgroups times what a round costs
+  const struct {
+    Kind kind;
+    double start, block;  // us
+  } rings[] = {{RING16, 4.0, 0.115}, {RING32, 4.0, 0.13}, {RING64, 5.0, 0.28}};
+  Kind best = RING64;
+  double least = 1e30;
+  for (const auto& q : rings) {
+    const double t = (double)((tiles_of(a, q.kind) + CUS - 1) / CUS) * (q.start + kb * q.block);
+    if (t < least) least = t, best = q.kind;
+  }
+  return best;
 }
 
 Plan choose(const Fp8Args& a, bool split) {
-  Plan c{0, 1};
-  if (a.M <= 16 && a.out == OUT_F32) return c;
-  if (a.M <= 32)
-    c.kind = 1;
-  else if (a.M <= 64)
-    c.kind = 2;
-  else
-    c.kind = tiles_of(a, 4) >= 192 ? 4 : 3;
-  const int tiles = tiles_of(a, c.kind);
+  if (a.out == OUT_F32) return Plan{choose_wide(a), 1};
+  Plan c{a.M <= 32 ? FP32R : a.M <= 64 ? FP64R : tiles_of(a, FP256) >= 192 ? FP256 : FP128, 1};
+  const long long tiles = tiles_of(a, c.kind);
+  if (!split || c.kind == FP256 || tiles > COUNTERS / SHAPES[c.kind].waves) return c;
   int kb = 1 << 30;
   for (int i = 0; i < a.count; i++) kb = a.p[i].K / 128 < kb ? a.p[i].K / 128 : kb;
-  if (split && c.kind < 4 && tiles <= COUNTERS) {
-    int want = 256 / tiles;
-    if (want > kb / 4) want = kb / 4;
-    if (want > 16) want = 16;
-    for (; want > 1; want--) {
-      c.splits = want;
-      if (plan_bytes(a, c) <= WS_MAX) break;
-    }
-    c.splits = want > 1 ? want : 1;
+  int want = (int)(CUS / tiles);
+  if (want > kb / 4) want = kb / 4;
+  if (want > 16) want = 16;
+  for (c.splits = want > 1 ? want : 1; c.splits > 1 && plan_bytes(a, c) > WS_MAX; c.splits--) {
   }
   return c;
 }
 
-template <typename T, Mode MODE>
+template <typename T, Mode MODE, bool E8>
 hipError_t launch_tile(const Fp8Args& a, const Launch& l, int tiles, hipStream_t s) {
   static LdsLimit limit;
-  constexpr bool big = T::W == 8 && MODE != WIDE;
   void (*kernel)(const Fp8Args, const Launch);
-  if constexpr (big)
+  if constexpr (T::BM == 256)
     kernel = k_big<T, MODE>;
   else
-    kernel = k_tile<T, MODE>;
+    kernel = k_tile<T, MODE, E8>;
   const hipError_t e = limit.raise(reinterpret_cast<const void*>(kernel), T::LDS);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, dim3((unsigned)tiles * l.splits), dim3(T::THREADS), T::LDS, s, a, l);
@@ -808,9 +1014,14 @@ hipError_t launch_tile(const Fp8Args& a, const Launch& l, int tiles, hipStream_t
 }
 
 template <typename T>
-hipError_t launch_mode(const Fp8Args& a, const Launch& l, int tiles, hipStream_t s) {
-  if (a.out == OUT_F32) return launch_tile<T, WIDE>(a, l, tiles, s);
-  return a.e8m0 ? launch_tile<T, FP8E>(a, l, tiles, s) : launch_tile<T, FP8S>(a, l, tiles, s);
+hipError_t launch_wide(const Fp8Args& a, const Launch& l, int tiles, hipStream_t s) {
+  return a.e8m0 ? launch_tile<T, WIDE, true>(a, l, tiles, s)
+                : launch_tile<T, WIDE, false>(a, l, tiles, s);
+}
+template <typename T>
+hipError_t launch_fp8_tile(const Fp8Args& a, const Launch& l, int tiles, hipStream_t s) {
+  return a.e8m0 ? launch_tile<T, FP8E, true>(a, l, tiles, s)
+                : launch_tile<T, FP8S, false>(a, l, tiles, s);
 }
 
 }  // namespace
@@ -819,22 +1030,27 @@ size_t fp8_workspace_bytes(const Fp8Args& a) { return plan_bytes(a, choose(a, tr
 
 hipError_t launch_fp8(const Fp8Args& a, void* ws, hipStream_t s) {
   const Plan c = choose(a, ws != nullptr);
+  const Shape& t = SHAPES[c.kind];
   Launch l{};
-  l.mt = (a.M + BMS[c.kind] - 1) / BMS[c.kind];
+  l.mt = (a.M + t.bm - 1) / t.bm;
   l.splits = c.splits;
   l.counters = static_cast<unsigned*>(ws);
   l.partial = static_cast<float*>(ws) + COUNTERS;
   for (int i = 0; i < a.count; i++)
-    l.tile0[i + 1] = l.tile0[i] + l.mt * ((a.p[i].N + BNS[c.kind] - 1) / BNS[c.kind]);
+    l.tile0[i + 1] = l.tile0[i] + l.mt * ((a.p[i].N + t.bn - 1) / t.bn);
   const int tiles = l.tile0[a.count];
   switch (c.kind) {
-    case 0:
-      hipLaunchKernelGGL((k_rows<4>), dim3(tiles), dim3(64 * SW), 0, s, a, l);
-      return hipGetLastError();
-    case 1: return launch_mode<T32>(a, l, tiles, s);
-    case 2: return launch_mode<T64>(a, l, tiles, s);
-    case 3: return launch_mode<T128>(a, l, tiles, s);
-    default: return launch_mode<T256>(a, l, tiles, s);
+    case ROWS16: return launch_rows<1, 2>(a, l, tiles, s);
+    case ROWS64: return launch_rows<4, 1>(a, l, tiles, s);
+    case RING16: return launch_ring<1, 2, 3>(a, l, tiles, s);
+    case RING32: return launch_ring<2, 2, 2>(a, l, tiles, s);
+    case RING64: return launch_ring<4, 4, 1>(a, l, tiles, s);
+    case WIDE64: return launch_wide<W64>(a, l, tiles, s);
+    case WIDE128: return launch_wide<W128>(a, l, tiles, s);
+    case FP32R: return launch_fp8_tile<T32>(a, l, tiles, s);
+    case FP64R: return launch_fp8_tile<T64>(a, l, tiles, s);
+    case FP128: return launch_fp8_tile<T128>(a, l, tiles, s);
+    default: return launch_fp8_tile<T256>(a, l, tiles, s);
   }
 }
 
