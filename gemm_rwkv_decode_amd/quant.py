@@ -7,7 +7,8 @@ The step before the hot path.  Every layout the library reads can be produced:
 * asymmetric superblocks of 256 weights with 4-, 5- or 6-bit unsigned codes,
   a scale and a shift per 32-wide group stored as 6-bit sub-codes of a
   binary16 superblock scale and min (w ~ (d*sc_j)*q - (m*mn_j));
-* FP8 E4M3 codes with one binary32 scale for the matrix.
+* FP8 E4M3 codes with one binary32 scale for the matrix;
+* FP8 E4M3 codes with an E8M0 scale for each block of 128 x 128 (rq_gemm_fp8).
 
 Two ways to choose the per-group scale (and shift):
 
@@ -77,6 +78,8 @@ def quantize(W, fmt: "S.Fmt", xsq: Optional[np.ndarray] = None, method: str = "s
     N, K = W.shape
     if fmt.layout == S.LAYOUT_FP8_TENSOR:
         return _fp8(W, fmt)
+    if fmt.layout == S.LAYOUT_FP8_BLOCK:
+        return S.Packed(*fp8_blocks(torch.from_numpy(W.astype(np.float32))), None, N, K, fmt)
     xw = _weights(xsq, K)
     if fmt.layout == S.LAYOUT_SYM:
         return _sym(W, fmt, xw, method)
@@ -183,3 +186,23 @@ def _fp8(W, fmt):
         codes = (Wt / scale).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
     return S.Packed(codes.contiguous(), scale, None, N, K, fmt)
 
+
+def fp8_blocks(W):
+    """(E4M3 codes, E8M0 scales, both uint8) of float32 weights [N][K] on any
+    device: a block of 128 x 128 has the smallest power of two s >= 2^-126 with
+    |w| <= 448 s, the rule that rq_quant_fp8 has for activations."""
+    N, K = W.shape
+    B = 128
+    if K % B:
+        raise ValueError(f"whole blocks of {B} columns expected, got {K}")
+    nb = -(-N // B)
+    W = W.to(torch.float32)
+    if not bool(W.isfinite().all()):
+        raise ValueError("finite weights expected")
+    padded = torch.zeros((nb * B, K), dtype=torch.float32, device=W.device)
+    padded[:N] = W
+    v = padded.view(nb, B, K // B, B)
+    m, e = torch.frexp(v.abs().amax((1, 3)))      # m in [0.5, 1); 448 = 0.875 * 2^9
+    e = torch.where(m > 0, e - 8 - (m <= 0.875).int(), -126).clamp(min=-126)
+    codes = torch.ldexp(v, -e[:, None, :, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    return codes.view(nb * B, K)[:N].contiguous(), (e + 127).to(torch.uint8)

@@ -14,6 +14,11 @@ those calls (norms, the small dense projections of decay, removal rate, value
 mix and gate) is plain torch.  The same code runs prompts and single tokens:
 only the offsets differ.
 
+With ``--format fp8b128`` both operands of the products are block-scaled FP8: the
+mixes are quantized in one call, the state's outputs by the group norm behind the
+recurrence, the FFN key's by their product, and the residual stream is added to
+in the output and FFN value products.
+
     python -m gemm_rwkv_decode_amd.serve --layers 4 --width 768 --requests 16
 
 Weights are synthetic (seeded, random codes), so the text is not meaningful.
@@ -25,6 +30,7 @@ import torch
 import torch.nn.functional as F
 
 import gemm_rwkv_decode_amd as rq
+from gemm_rwkv_decode_amd import quant as Q
 from gemm_rwkv_decode_amd import step as ST
 from gemm_rwkv_decode_amd import synth as S
 
@@ -33,7 +39,10 @@ MIXES = ("r", "k", "v", "w", "a", "g")  # the time mix's shifted inputs
 
 
 def _packed(N, K, fmt, g, device):
-    """Random codes whose rows have a 2-norm of about one (symmetric formats)."""
+    """Random codes whose rows have a 2-norm of about one."""
+    if fmt.layout == S.LAYOUT_FP8_BLOCK:
+        w = torch.randn((N, K), generator=g, device=device) * K ** -0.5
+        return S.Packed(*Q.fp8_blocks(w), None, N, K, fmt)
     top = 2 ** (fmt.bits - 1) - 1
     codes = torch.randint(-top, top + 1, (N, K), generator=g, device=device).to(torch.int8)
     scale = (3.0 / K) ** 0.5 / top
@@ -62,11 +71,16 @@ class Layer:
 
 class Model:
     """``layers`` layers of ``width`` channels (whole heads of 64) and a packed
-    head of ``vocab`` tokens; ``fmt`` is a symmetric format of synth."""
+    head of ``vocab`` tokens; ``fmt`` is a symmetric format of synth, or its
+    FP8_B128 (widths of whole blocks of 128)."""
 
     def __init__(self, layers, width, vocab, fmt=S.INT4_G64, low=64, seed=0, device="cuda"):
-        if width % HEAD or fmt.layout != S.LAYOUT_SYM:
-            raise ValueError("whole heads of 64 channels and a symmetric format expected")
+        self.fp8 = fmt.layout == S.LAYOUT_FP8_BLOCK
+        if width % HEAD or not (self.fp8 or fmt.layout == S.LAYOUT_SYM):
+            raise ValueError("whole heads of 64 channels and a symmetric or block-scaled FP8 "
+                             "format expected")
+        if self.fp8 and width % rq.RQ_FP8_BLOCK:
+            raise ValueError(f"whole blocks of {rq.RQ_FP8_BLOCK} channels expected")
         g = S.generator(seed, device)
         self.width, self.heads, self.vocab, self.ffn = width, width // HEAD, vocab, 4 * width
         self.device = torch.device(device)
@@ -135,6 +149,30 @@ def products(mats, xs):
     return ys
 
 
+def _room8(rows, columns, device):
+    """Room for E4M3 rows and their scales."""
+    return (torch.empty((rows, columns), dtype=torch.uint8, device=device),
+            torch.empty((rows, columns // rq.RQ_FP8_BLOCK), dtype=torch.uint8, device=device))
+
+
+def blocks(x, act=rq.RQ_ACT_NONE):
+    """Rows of x as block-scaled FP8."""
+    out = _room8(*x.shape, x.device)
+    rq.rq_quant_fp8(x, *out, act=act)
+    return out
+
+
+def products8(mats, xs, ys=None, add=False, act=rq.RQ_ACT_NONE):
+    """Outputs of block-scaled matrices: float32, or as ``ys`` says (a pair for
+    quantized ones); ``add``: onto what is in ys."""
+    rows = xs[0][0].shape[0]
+    if ys is None:
+        ys = [torch.empty((rows, p.N), device=xs[0][0].device) for p in mats]
+    rq.rq_gemm_fp8([(p.qweight, p.scales, *x, y if add else None, y, p.N, p.K)
+                    for p, x, y in zip(mats, xs, ys)], act=act)
+    return ys
+
+
 def _norm(x, ln):
     return F.layer_norm(x, x.shape[-1:], *ln)
 
@@ -158,7 +196,11 @@ def forward(model, state, tokens, offsets, slots, ids=None, adapters=None):
         mixed = torch.empty((len(MIXES),) + xn.shape, dtype=torch.float16, device=x.device)
         rq.rq_shift(xn, w.mu, state.att[l], mixed, offsets, slots)
         xr, xk, xv, xw, xa, xg = mixed.unbind(0)
-        r, k, v = products(w.mats[:3], (xr, xk, xv))
+        if model.fp8:
+            q, s = blocks(mixed[:3].view(3 * T, -1))
+            r, k, v = products8(w.mats[:3], list(zip(q.chunk(3), s.chunk(3))))
+        else:
+            r, k, v = products(w.mats[:3], (xr, xk, xv))
         if adapters is not None:
             adapters.add(adapters.rkv[l], (xr, xk, xv), (r, k, v), ids)
         decay = w.base["w"] + _low(w, "w", xw, torch.tanh)
@@ -172,20 +214,38 @@ def forward(model, state, tokens, offsets, slots, ids=None, adapters=None):
         k = k * (1 + (eta - 1) * w.k_a)
         y = torch.empty_like(r)
         rq.rq_wkv7(r, decay, k, v, kappa, eta, state.wkv[l], y, offsets, slots)
-        y = F.group_norm(y, H, *w.lnx, eps=64e-5)
-        own = (r * k * w.r_k).view(T, H, HEAD).sum(-1, keepdim=True)
-        y = (y + (own * v.view(T, H, HEAD)).view(T, -1)) * gate
-        x = x + products(w.mats[3:4], (y.half(),))[0]
+        if model.fp8:
+            y8 = _room8(T, model.width, x.device)
+            rq.rq_groupnorm(y, H, *w.lnx, 64e-5, y8, bonus=(r, k, w.r_k, v), gate=gate)
+            products8(w.mats[3:4], (y8,), (x,), add=True)
+        else:
+            y = F.group_norm(y, H, *w.lnx, eps=64e-5)
+            own = (r * k * w.r_k).view(T, H, HEAD).sum(-1, keepdim=True)
+            y = (y + (own * v.view(T, H, HEAD)).view(T, -1)) * gate
+            x = x + products(w.mats[3:4], (y.half(),))[0]
 
         xn = _norm(x, w.ln2).half()
         mixed = torch.empty((1,) + xn.shape, dtype=torch.float16, device=x.device)
         rq.rq_shift(xn, w.mu_ffn, state.ffn[l], mixed, offsets, slots)
+        if model.fp8:
+            x8 = blocks(mixed[0])
+            if adapters is not None:
+                key, = products8(w.mats[4:5], (x8,))
+                adapters.add(adapters.key[l:l + 1], (mixed[0],), (key,), ids)
+                key8 = blocks(key, act=rq.RQ_ACT_RELU2)
+            else:  # quantized by the product itself
+                key8, = products8(w.mats[4:5], (x8,), (_room8(T, model.ffn, x.device),),
+                                  act=rq.RQ_ACT_RELU2)
+            products8(w.mats[5:6], (key8,), (x,), add=True)
+            continue
         key, = products(w.mats[4:5], (mixed[0],))
         if adapters is not None:
             adapters.add(adapters.key[l:l + 1], (mixed[0],), (key,), ids)
         x = x + products(w.mats[5:6], (torch.relu(key).square().half(),))[0]
-    last = x[offsets[1:].long() - 1]
-    return products([model.head], (_norm(last, model.ln_out).half(),))[0]
+    last = _norm(x[offsets[1:].long() - 1], model.ln_out).half()
+    if model.fp8:
+        return products8([model.head], (blocks(last),))[0]
+    return products([model.head], (last,))[0]
 
 
 class Histories:
@@ -302,7 +362,7 @@ def main(argv=None):
     ap.add_argument("--layers", type=int, default=12)
     ap.add_argument("--width", type=int, default=768)
     ap.add_argument("--vocab", type=int, default=65536)
-    ap.add_argument("--format", choices=("int4g64", "int8g16"), default="int4g64")
+    ap.add_argument("--format", choices=("int4g64", "int8g16", "fp8b128"), default="int4g64")
     ap.add_argument("--requests", type=int, default=16)
     ap.add_argument("--prompt", type=int, default=128, help="longest prompt")
     ap.add_argument("--steps", type=int, default=32)
@@ -310,7 +370,8 @@ def main(argv=None):
     ap.add_argument("--rank", type=int, default=16)
     ap.add_argument("--eager", action="store_true", help="no graph for the steps")
     a = ap.parse_args(argv)
-    model = Model(a.layers, a.width, a.vocab, S.FORMATS[a.format])
+    formats = {f.tag: f for f in (S.INT4_G64, S.INT8_G16, S.FP8_B128)}
+    model = Model(a.layers, a.width, a.vocab, formats[a.format])
     adapters = Adapters(model, [a.rank] * a.adapters) if a.adapters else None
     # one request in adapters + 1 has none
     ids = [m % (a.adapters + 1) - 1 for m in range(a.requests)] if a.adapters else None

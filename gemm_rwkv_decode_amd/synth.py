@@ -40,6 +40,7 @@ import torch
 LAYOUT_SYM = 0
 LAYOUT_ASYM_SB = 1
 LAYOUT_FP8_TENSOR = 2
+LAYOUT_FP8_BLOCK = 3  # of rq_gemm_fp8: E4M3 with an E8M0 scale for 128 x 128
 SUPERBLOCK = 256
 
 
@@ -61,6 +62,8 @@ class Fmt:
         codes = N * K * self.bits // 8
         if self.layout == LAYOUT_FP8_TENSOR:
             return codes + 4  # one binary32 scale
+        if self.layout == LAYOUT_FP8_BLOCK:
+            return codes + -(-N // self.group) * (K // self.group)
         if self.layout == LAYOUT_ASYM_SB:
             return codes + 2 * 8 * N * (K // SUPERBLOCK)
         return codes + 2 * N * (K // self.group)
@@ -77,6 +80,9 @@ FP8_E4M3 = Fmt("fp8e4m3", 8, 0, LAYOUT_FP8_TENSOR)
 # 5 bits, FFN in 6 bits)
 ASYM5_G32 = Fmt("asym5g32", 5, 32, LAYOUT_ASYM_SB)
 ASYM6_G32 = Fmt("asym6g32", 6, 32, LAYOUT_ASYM_SB)
+# FP8 E4M3 weights with a power-of-two scale for each block of 128 x 128, for
+# products with block-scaled FP8 activations (rq_gemm_fp8, not rq_gemv)
+FP8_B128 = Fmt("fp8b128", 8, 128, LAYOUT_FP8_BLOCK)
 FORMATS = {f.tag: f for f in (INT4_G64, INT8_G16, ASYM4_G32, FP8_E4M3, ASYM5_G32, ASYM6_G32)}
 
 MAT_NAMES = ("att.receptance", "att.key", "att.value", "att.output",

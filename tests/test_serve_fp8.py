@@ -1,0 +1,206 @@
+"""The serving example with block-scaled FP8 products.
+
+Every call is checked on the very tensors it was given against its formula in
+64 bits, and the logits as a whole against the plain form of test_serve.py on the
+same weights, with products of operands rounded to E4M3 in the same places.  The
+bound does not count on the roundings agreeing: an E4M3 rounding is uniform within
+half a step, an eighth of a power of two, over logarithmically uniform values a
+relative 2-norm of 2^-3 / sqrt(12) * sqrt(0.75 / (2 ln 2)) = 0.0265.  In a layer
+three of them enter the recurrence, one the output product, one the FFN key (whose
+square doubles it) and one the FFN value: sqrt(3 + 1 + 4 + 1) = 3 of them if
+independent, so two layers and the head make sqrt(2 * 9 + 1) * 0.0265 = 0.116 of
+the logits' 2-norm on each side, and both sides' as much as twice that.  (Without
+the roundings in the plain form a first token may differ by more: from an empty
+state a head's output is v (k.r), whose sign the norm keeps and a small k.r loses.)
+"""
+import numpy as np
+import pytest
+import torch
+
+import gemm_rwkv_decode_amd as rq
+from gemm_rwkv_decode_amd import quant as Q
+from gemm_rwkv_decode_amd import serve as V
+from gemm_rwkv_decode_amd import synth as S
+from tests import aroundtest as A
+from tests import fp8test as F
+from tests import test_serve as T
+
+BOUND = 2 * 19 ** 0.5 * 0.0265
+
+
+def weights(p):
+    """float64 of a block-scaled matrix."""
+    q = F.TABLE[p.qweight.cpu().numpy()]
+    s = 2.0 ** (p.scales.cpu().numpy().astype(np.float64) - 127)
+    return q * np.repeat(np.repeat(s, 128, 0)[:p.N], 128, 1)
+
+
+class Product:
+    """A matrix that multiplies E4M3 operands."""
+
+    def __init__(self, p):
+        self.w = weights(p)
+
+    def __matmul__(self, x):
+        q, s = F.quant_ref(x[None])
+        return self.w @ (q * np.repeat(s, 128, 1))[0]
+
+
+class Plain(T.Plain):
+    def __init__(self, model, adapters, ident, plant=None):
+        self.m, self.ad, self.ident, self.plant = model, adapters, ident, plant
+        self.W = [[Product(p) for p in w.mats] for w in model.layers]
+        self.head = Product(model.head)
+        L, D = len(model.layers), model.width
+        self.att, self.ffn = np.zeros((L, D)), np.zeros((L, D))
+        self.wkv = np.zeros((L, model.heads, 64, 64))
+
+
+def plain_logits(monkeypatch, *args):
+    monkeypatch.setattr(T, "Plain", Plain)
+    return T.plain_logits(*args)
+
+
+# ------------------------------------------------------------- quantizer, CPU
+def test_blocks_of_weights():
+    g = torch.Generator().manual_seed(1)
+    for N, K in ((1, 128), (130, 256), (256, 384), (517, 128)):
+        W = torch.randn((N, K), generator=g) * torch.exp(2 * torch.randn((N, 1), generator=g))
+        W[0, 0] = 0.0
+        codes, scales = Q.fp8_blocks(W)
+        nb = -(-N // 128)
+        assert codes.shape == (N, K) and scales.shape == (nb, K // 128)
+        padded = np.zeros((nb * 128, K), np.float32)
+        padded[:N] = W.numpy()
+        # a block's rows one after another are a row of blocks to the quantizer's definition
+        flat = padded.reshape(nb, 128, K // 128, 128).transpose(0, 2, 1, 3).reshape(-1, 128 * 128)
+        top = np.abs(flat).max(1)
+        want = F.quant_ref(np.concatenate([top[:, None], np.zeros((len(top), 127))], 1))[1][:, 0]
+        assert np.array_equal(2.0 ** (scales.numpy().astype(np.float64).ravel() - 127), want)
+        s = np.repeat(np.repeat(want.reshape(nb, -1), 128, 0)[:N], 128, 1)
+        assert F.same(F.TABLE[codes.numpy()], F.nearest_e4m3(W.numpy().astype(np.float64) / s))
+        p = Q.quantize(W, S.FP8_B128)
+        assert torch.equal(p.qweight, codes) and torch.equal(p.scales, scales)
+        assert S.FP8_B128.weight_bytes(N, K) == codes.numel() + scales.numel()
+    for bad in (torch.randn(4, 100), torch.full((2, 128), float("nan"))):
+        with pytest.raises(ValueError):
+            Q.fp8_blocks(bad)
+
+
+def test_blocks_of_zeros():
+    codes, scales = Q.fp8_blocks(torch.zeros(128, 128))
+    assert not codes.any() and scales.item() == 1  # 2^-126
+
+
+def test_widths_of_half_blocks_are_refused():
+    with pytest.raises(ValueError):
+        V.Model(1, 192, 64, S.FP8_B128, device="cpu")
+
+
+@pytest.mark.parametrize("plant", ["adapter", "shift", "state"])
+def test_planted_mistakes_show(plant, monkeypatch):
+    """The bound separates.  (The removal key moves these logits by less than it; what
+    leads to the recurrence is the same code as in test_serve.py.)"""
+    model, adapters, prompts = T.build("cpu", S.FP8_B128)
+    tokens = [[1, 2], [3, 4], [5, 6], [7, 8], [9, 10]]
+    right = plain_logits(monkeypatch, model, adapters, prompts, tokens)
+    wrong = plain_logits(monkeypatch, model, adapters, prompts, tokens, plant)
+    assert max(T.difference(w, r).max() for w, r in zip(wrong, right)) > 1.5 * BOUND
+
+
+# ------------------------------------------------------------------------ GPU
+class Checked:
+    """rq's block-scaled calls, each checked on what it was given."""
+
+    def __init__(self, monkeypatch):
+        self.calls = {"rq_quant_fp8": 0, "rq_gemm_fp8": 0, "rq_groupnorm": 0}
+        self.real = {n: getattr(rq, n) for n in self.calls}
+        for n in self.calls:
+            monkeypatch.setattr(rq, n, getattr(self, n))
+
+    def rq_quant_fp8(self, x, q, s, act=rq.RQ_ACT_NONE):
+        self.real["rq_quant_fp8"](x, q, s, act=act)
+        self.calls["rq_quant_fp8"] += 1
+        want, scales = F.quant_ref(F.act(x.cpu().numpy(), act))
+        assert F.same(F.values(q.view(F.E4M3)), want) and F.same(F.values(s.view(F.E8M0)), scales)
+
+    def rq_gemm_fp8(self, problems, act=rq.RQ_ACT_NONE):
+        given = [None if p[4] is None else p[4].clone() for p in problems]
+        self.real["rq_gemm_fp8"](problems, act=act)
+        self.calls["rq_gemm_fp8"] += 1
+        for (w, ws, x, xs, _, y, N, K), y_in in zip(problems, given):
+            ops = (w.view(F.E4M3), ws.view(F.E8M0), x.view(F.E4M3), xs.view(F.E8M0))
+            if isinstance(y, tuple):
+                h = torch.empty((x.shape[0], N), dtype=torch.float16, device="cuda")
+                self.real["rq_gemm_fp8"]([(w, ws, x, xs, None, h, N, K)])
+                want, scales = F.quant_ref(F.act(h.cpu().numpy(), act))
+                assert F.same(F.values(y[0].view(F.E4M3)), want)
+                assert F.same(F.values(y[1].view(F.E8M0)), scales)
+                y, out = h, "f16"
+            else:
+                out = "f32"
+            ref, mag = F.gemm_ref(*ops, y_in)
+            assert bool(((y.double() - ref).abs() <= F.gemm_bound(ref, mag, K, out)).all())
+
+    def rq_groupnorm(self, y, groups, weight, bias, eps, out, bonus, gate):
+        self.real["rq_groupnorm"](y, groups, weight, bias, eps, out, bonus=bonus, gate=gate)
+        self.calls["rq_groupnorm"] += 1
+        h = torch.empty(y.shape, dtype=torch.float16, device="cuda")
+        self.real["rq_groupnorm"](y, groups, weight, bias, eps, h, bonus=bonus, gate=gate)
+        n = lambda t: t.cpu().numpy()  # noqa: E731
+        ref, b = F.norm_ref(n(y), groups, n(weight), n(bias), eps, tuple(map(n, bonus)), n(gate), 0)
+        assert np.all(np.abs(n(h) - ref) <= b + F.HALF * (np.abs(ref) + b) + 2.0 ** -25)
+        want, scales = F.quant_ref(n(h))
+        assert F.same(F.values(out[0].view(F.E4M3)), want)
+        assert F.same(F.values(out[1].view(F.E8M0)), scales)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("with_adapters", [True, False])
+def test_every_call_of_prompts_and_steps(monkeypatch, with_adapters):
+    model, adapters, prompts = T.build("cuda", S.FP8_B128)
+    check = Checked(monkeypatch)
+    V.generate(model, prompts, 2, adapters if with_adapters else None,
+               T.IDS if with_adapters else None)
+    # two passes of two layers: rkv, output, key, value and the head's product; the mixes', the
+    # FFN's (and with adapters its key's) and the head's quantization
+    assert check.calls == {"rq_gemm_fp8": 2 * 9, "rq_groupnorm": 2 * 2,
+                           "rq_quant_fp8": 2 * (7 if with_adapters else 5)}
+
+
+@pytest.mark.gpu
+def test_logits_against_the_plain_form(monkeypatch):
+    model, adapters, prompts = T.build("cuda", S.FP8_B128)
+    seen = []
+    tokens = V.generate(model, prompts, T.STEPS, adapters, T.IDS,
+                        on_step=lambda i, z: seen.append(z.cpu().numpy())).cpu().numpy()
+    want = plain_logits(monkeypatch, model, adapters, prompts, tokens)
+    for i in range(T.STEPS):
+        d = T.difference(seen[i].astype(np.float64), want[i])
+        assert (d < BOUND).all(), (i, d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("with_adapters", [True, False])
+def test_steps_replayed_from_a_graph(with_adapters):
+    model, adapters, prompts = T.build("cuda", S.FP8_B128)
+    runs = []
+    for graph in (False, True):
+        seen = []
+        tokens = V.generate(model, prompts, 7, adapters if with_adapters else None,
+                            T.IDS if with_adapters else None, graph=graph,
+                            on_step=lambda i, z: seen.append(z.clone().cpu()))
+        torch.cuda.synchronize()
+        runs.append((tokens.cpu(), seen))
+    assert torch.equal(runs[0][0], runs[1][0])
+    assert all(torch.equal(a, b) for a, b in zip(runs[0][1], runs[1][1]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("more", [[], ["--adapters", "0"], ["--eager"]])
+def test_the_command(capsys, more):
+    V.main(["--layers", "1", "--width", "256", "--vocab", "517", "--requests", "6", "--prompt",
+            "80", "--steps", "5", "--adapters", "2", "--rank", "8", "--format", "fp8b128"] + more)
+    lines = capsys.readouterr().out.splitlines()
+    assert lines[0].startswith("6 requests") and "tokens/s" in lines[1]
+    assert sum(line.startswith("request ") for line in lines) == 3
