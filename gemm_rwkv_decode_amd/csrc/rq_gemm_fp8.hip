@@ -748,9 +748,13 @@ __global__ void __launch_bounds__(64 * SW, 2) k_rows(const Fp8Args a, const Laun
   __shared__ f4 sums[SW][TW][64];
   const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Where o = where(a, l, 16 * TW, 16);
-  const Fp8Problem& p = a.p[o.problem];
-  const int n0 = o.n0, KB = p.K / 128;
+  // neighbouring tiles to one XCD
+  const u32 xcd = blockIdx.x & 7, each = gridDim.x >> 3, more = gridDim.x & 7;
+  const int tile = xcd * each + min(xcd, more) + (blockIdx.x >> 3);
+  int pi = 0;
+  while (pi + 1 < a.count && tile >= l.tile0[pi + 1]) pi++;
+  const Fp8Problem& p = a.p[pi];
+  const int n0 = (tile - l.tile0[pi]) * 16 * TW, KB = p.K / 128;
   const uint8_t* wp[TW];
 #pragma unroll
   for (int t = 0; t < TW; t++) wp[t] = p.w + (size_t)min(n0 + 16 * t + r, p.N - 1) * p.K + 16 * h;
@@ -802,7 +806,7 @@ __global__ void __launch_bounds__(64 * SW, 2) k_rows(const Fp8Args a, const Laun
 #pragma unroll
     for (int w = 1; w < SW; w++) v += sums[w][t][lane];
     const int n = n0 + 16 * t + 4 * h;
-    if (r < a.M && n < p.N) store4(p, OUT_F32, r, n, v);
+    if (r < a.M && n < p.N) store4(p, a.out, r, n, v);
   }
 }
 
@@ -901,13 +905,26 @@ __global__ void __launch_bounds__(64 * SW, 2) k_ring(const Fp8Args a, const Laun
 #pragma unroll
     for (int j = 0; j < TM; j++) sums[((t * TM + j) * W + wave) * 64 + lane] = acc[t][j];
   __syncthreads();
+  if constexpr (TN == 8) {  // whole blocks of outputs, to be quantized
+    for (int j = wave; j < TM; j += W) {
+      f4 rows[TB][1];
+#pragma unroll
+      for (int t = 0; t < TB; t++) {
+        rows[t][0] = sums[(t * TM + j) * W * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < W; w++) rows[t][0] += sums[((t * TM + j) * W + w) * 64 + lane];
+      }
+      store_tile<1>(a, p, n0, m0 + 16 * j, rows);
+    }
+    return;
+  }
   for (int c = wave; c < TN * TM; c += W) {
     f4 v = sums[c * W * 64 + lane];
 #pragma unroll
     for (int w = 1; w < W; w++) v += sums[(c * W + w) * 64 + lane];
     const size_t m = m0 + 16 * (c % TM) + r;
     const int at = n0 + 16 * (c / TM) + 4 * h;
-    if (m < (size_t)a.M && at < p.N) store4(p, OUT_F32, m, at, v);
+    if (m < (size_t)a.M && at < p.N) store4(p, a.out, m, at, v);
   }
 }
 
@@ -926,25 +943,27 @@ hipError_t launch_ring(const Fp8Args& a, const Launch& l, int tiles, hipStream_t
 // FP8 operands: 128 outputs a wave, so that a row's block is one wave's
 typedef Tile<2, 4, 8, 4, 2> T256;  // 256 outputs x 256 rows
 typedef Tile<1, 4, 8, 2, 2> T128;  // 128 x 128
-typedef Tile<1, 4, 8, 1, 3> T64;   // 128 x 64
-typedef Tile<1, 2, 8, 1, 3> T32;   // 128 x 32
 // binary16 operands, widened by every wave that reads them: as square as they go
 typedef Tile<2, 4, 4, 2, 2> W128;  // 128 x 128
 typedef Tile<4, 2, 2, 2, 3> W64;   // 128 x 64
 
 // What a call runs: a kernel with its tile, and the ranges of K.
-enum Kind { ROWS16, ROWS64, RING16, RING32, RING64, WIDE64, WIDE128, FP32R, FP64R, FP128, FP256 };
+enum Kind {
+  ROWS16, ROWS64, RING1X2, RING2X2, RING4X2, RING4X3, RING4X4, RING8X1, RING8X2, WIDE64, WIDE128, FP128,
+  FP256
+};
 struct Shape {
   int bn, bm, waves;
 };
-constexpr Shape SHAPES[] = {{16, 16, 8},  {64, 16, 8},   {16, 32, 8},  {32, 32, 8},
-                            {64, 64, 8},  {128, 64, 8},  {128, 128, 8}, {128, 32, 2},
-                            {128, 64, 4}, {128, 128, 4}, {256, 256, 8}};
+constexpr Shape SHAPES[] = {{16, 16, 8},  {64, 16, 8},  {16, 32, 8},   {32, 32, 8},  {64, 32, 8},
+                            {64, 48, 8},  {64, 64, 8},  {128, 16, 8},  {128, 32, 8}, {128, 64, 8},
+                            {128, 128, 8}, {128, 128, 4}, {256, 256, 8}};
 struct Plan {
   Kind kind;
   int splits;
 };
 constexpr int CUS = 256;
+constexpr int SMALL_M = 128;  // rows up to which binary16 and E4M3 outputs go that way too
 
 long long tiles_of(const Fp8Args& a, Kind kind) {
   const Shape& s = SHAPES[kind];
@@ -963,30 +982,38 @@ size_t plan_bytes(const Fp8Args& a, const Plan& c) {
   return COUNTERS * 4 + (size_t)tiles_of(a, c.kind) * c.splits * s.bn * s.bm * 4;
 }
 
-// Binary32 outputs: the kernel follows from M and the numbers of tiles.
+// Products in binary16 instructions.  Rows and rings add in one order whatever their
+// tile, each wave's blocks and then the waves, which quantized outputs count on.
 Kind choose_wide(const Fp8Args& a) {
+  if (a.out == OUT_E4M3) return a.M <= 16 ? RING8X1 : RING8X2;
   if (a.M <= 16) return a.M > 4 && tiles_of(a, ROWS64) >= 192 ? ROWS64 : ROWS16;
-  if (a.M <= 64 && tiles_of(a, WIDE64) >= 2 * CUS) return WIDE64;
-  if (tiles_of(a, WIDE128) >= CUS) return WIDE128;
+  if (a.out == OUT_F32) {
+    if (a.M <= 64 && tiles_of(a, WIDE64) >= 2 * CUS) return WIDE64;
+    if (tiles_of(a, WIDE128) >= CUS) return WIDE128;
+  }
   int kb = 0;
   for (int i = 0; i < a.count; i++) kb = a.p[i].K / 128 > kb ? a.p[i].K / 128 : kb;
-  // rounds of workgroups times what a round costs
+  // What a tile costs: its start and end once in a round of all compute units (in
+  // two rounds where two workgroups share one), then the blocks of K one after another.
   const struct {
     Kind kind;
-    double start, block;  // us
-  } rings[] = {{RING16, 4.0, 0.115}, {RING32, 4.0, 0.13}, {RING64, 5.0, 0.28}};
-  Kind best = RING64;
+    int shared;
+    double ends, block;  // us
+  } rings[] = {{RING1X2, 1, 3.4, 0.11}, {RING2X2, 2, 3.2, 0.12}, {RING4X2, 1, 4.3, 0.155},
+               {RING4X3, 1, 5.0, 0.2},  {RING4X4, 1, 5.4, 0.25}};
+  Kind best = RING4X4;
   double least = 1e30;
   for (const auto& q : rings) {
-    const double t = (double)((tiles_of(a, q.kind) + CUS - 1) / CUS) * (q.start + kb * q.block);
+    const long long n = tiles_of(a, q.kind), both = (long long)CUS * q.shared;
+    const double t = (double)((n + CUS - 1) / CUS) * kb * q.block + (double)((n + both - 1) / both) * q.ends;
     if (t < least) least = t, best = q.kind;
   }
   return best;
 }
 
 Plan choose(const Fp8Args& a, bool split) {
-  if (a.out == OUT_F32) return Plan{choose_wide(a), 1};
-  Plan c{a.M <= 32 ? FP32R : a.M <= 64 ? FP64R : tiles_of(a, FP256) >= 192 ? FP256 : FP128, 1};
+  if (a.out == OUT_F32 || a.M <= SMALL_M) return Plan{choose_wide(a), 1};
+  Plan c{tiles_of(a, FP256) >= 192 ? FP256 : FP128, 1};
   const long long tiles = tiles_of(a, c.kind);
   if (!split || c.kind == FP256 || tiles > COUNTERS / SHAPES[c.kind].waves) return c;
   int kb = 1 << 30;
@@ -1042,13 +1069,15 @@ hipError_t launch_fp8(const Fp8Args& a, void* ws, hipStream_t s) {
   switch (c.kind) {
     case ROWS16: return launch_rows<1, 2>(a, l, tiles, s);
     case ROWS64: return launch_rows<4, 1>(a, l, tiles, s);
-    case RING16: return launch_ring<1, 2, 3>(a, l, tiles, s);
-    case RING32: return launch_ring<2, 2, 2>(a, l, tiles, s);
-    case RING64: return launch_ring<4, 4, 1>(a, l, tiles, s);
+    case RING1X2: return launch_ring<1, 2, 2>(a, l, tiles, s);
+    case RING2X2: return launch_ring<2, 2, 1>(a, l, tiles, s);
+    case RING4X2: return launch_ring<4, 2, 1>(a, l, tiles, s);
+    case RING4X3: return launch_ring<4, 3, 1>(a, l, tiles, s);
+    case RING4X4: return launch_ring<4, 4, 1>(a, l, tiles, s);
+    case RING8X1: return launch_ring<8, 1, 1>(a, l, tiles, s);
+    case RING8X2: return launch_ring<8, 2, 1>(a, l, tiles, s);
     case WIDE64: return launch_wide<W64>(a, l, tiles, s);
     case WIDE128: return launch_wide<W128>(a, l, tiles, s);
-    case FP32R: return launch_fp8_tile<T32>(a, l, tiles, s);
-    case FP64R: return launch_fp8_tile<T64>(a, l, tiles, s);
     case FP128: return launch_fp8_tile<T128>(a, l, tiles, s);
     default: return launch_fp8_tile<T256>(a, l, tiles, s);
   }
