@@ -985,7 +985,11 @@ size_t plan_bytes(const Fp8Args& a, const Plan& c) {
 // Products in binary16 instructions.  Rows and rings add in one order whatever their
 // tile, each wave's blocks and then the waves, which quantized outputs count on.
 Kind choose_wide(const Fp8Args& a) {
-  if (a.out == OUT_E4M3) return a.M <= 16 ? RING8X1 : RING8X2;
+  // Tiles of 16 rows while they all run at once (32 rows, us: 4096 outputs of K =
+  // 16384 29.3 and in tiles of 32 rows 38.6; 16384 of 4096 17.0 and 18.8), of 32
+  // where they do not, which read w half as often (96 rows, 8192 outputs of K = 2048:
+  // 11.0, and in tiles of 16 rows 16.2).
+  if (a.out == OUT_E4M3) return a.M <= 16 || tiles_of(a, RING8X1) <= CUS ? RING8X1 : RING8X2;
   if (a.M <= 16) return a.M > 4 && tiles_of(a, ROWS64) >= 192 ? ROWS64 : ROWS16;
   if (a.out == OUT_F32) {
     if (a.M <= 64 && tiles_of(a, WIDE64) >= 2 * CUS) return WIDE64;
