@@ -506,7 +506,7 @@ k_tile(const Fp8Args a, const Launch l) {
 
   const int wave_n0 = n0 + wn * TN * 16;
   const size_t wave_m0 = m0 + wm * TM * 16;
-  if (l.splits > 1) {
+  if (MODE != WIDE && l.splits > 1) {
     // This range's sums, as the lanes hold them, past the caches that other XCDs do
     // not see; then the wave's arrival at its part of the tile.  The last of the
     // ranges' waves to arrive adds them in order, the sums of several ranges asked
@@ -534,7 +534,7 @@ k_tile(const Fp8Args a, const Launch l) {
     for (int t = 0; t < TN; t++)
 #pragma unroll
       for (int j = 0; j < TM; j++) acc[t][j] = f4{0, 0, 0, 0};
-    constexpr int SB = TN * TM > 16 ? 1 : 32 / (TN * TM) > 4 ? 4 : 32 / (TN * TM);
+    constexpr int SB = 2;
     for (int q0 = 0; q0 < l.splits; q0 += SB) {
       u32x4 v[SB][TN][TM];
 #pragma unroll
@@ -963,7 +963,6 @@ struct Plan {
   int splits;
 };
 constexpr int CUS = 256;
-constexpr int SMALL_M = 128;  // rows up to which binary16 and E4M3 outputs go that way too
 
 long long tiles_of(const Fp8Args& a, Kind kind) {
   const Shape& s = SHAPES[kind];
@@ -973,8 +972,7 @@ long long tiles_of(const Fp8Args& a, Kind kind) {
   return n;
 }
 
-constexpr int COUNTERS = 16384;  // arrival counters at the front of a workspace
-constexpr size_t WS_MAX = (size_t)64 << 20;
+constexpr int COUNTERS = 16384;  // dwords at the front of a workspace, of which tiles count in a few
 
 size_t plan_bytes(const Fp8Args& a, const Plan& c) {
   if (c.splits <= 1) return 0;
@@ -1015,18 +1013,39 @@ Kind choose_wide(const Fp8Args& a) {
   return best;
 }
 
+// Rows and rings for all binary32 outputs, and for the others while tiles of 128 x
+// 128 would leave the card empty.  Measured, binary16 outputs, us (tiles with K split
+// through a workspace, and whole):
+//   rows x outputs x K  tiles   ring  split  whole
+//   256 x 4096 x 4096     64    14.8   19.1   28.6
+//   256 x 4096 x 16384    64    41.7   36.4   98.6
+//   512 x 4096 x 4096    128    26.4   23.5   28.9
+//   203 x 12288 x 4096   192    36.7   29.4   29.4
+//   64 x 16384 x 4096    128    17.9   24.5   28.8
+//   64 x 65536 x 2048    512    49.9     -    39.6
+//   17 x 65536 x 2048    512    37.3     -    40.0
+bool few(const Fp8Args& a) {
+  const long long tiles = tiles_of(a, FP128);
+  return a.out == OUT_F32 || a.M <= 16 || tiles <= CUS / 4 || (a.M <= 64 && tiles <= CUS / 2);
+}
+
+// K is split, with a workspace, while two tiles or more would go to a compute unit
+// of their own, in ranges of four blocks at least.
 Plan choose(const Fp8Args& a, bool split) {
-  if (a.out == OUT_F32 || a.M <= SMALL_M) return Plan{choose_wide(a), 1};
-  Plan c{tiles_of(a, FP256) >= 192 ? FP256 : FP128, 1};
-  const long long tiles = tiles_of(a, c.kind);
-  if (!split || c.kind == FP256 || tiles > COUNTERS / SHAPES[c.kind].waves) return c;
+  if (few(a)) return Plan{choose_wide(a), 1};
+  // A round of tiles of 256 x 256, one to a compute unit, takes 1.2 times as long as
+  // one of 128 x 128, two to a compute unit, of half as much; the smaller ones do
+  // not wait for each other's round.  (4096 outputs of K = 4096, us, 256 and 128:
+  // 2048 rows 57.3 and 44.5, 2500 48.4 and 56.0, 4001 55.6 and 79.3, 4352 96.4 and 92.8.)
+  const long long large = (tiles_of(a, FP256) + CUS - 1) / CUS, small = tiles_of(a, FP128);
+  if (12 * large * 2 * CUS < 10 * (small < 2 * CUS ? 2 * CUS : small)) return Plan{FP256, 1};
+  Plan c{FP128, 1};
+  if (!split) return c;
   int kb = 1 << 30;
   for (int i = 0; i < a.count; i++) kb = a.p[i].K / 128 < kb ? a.p[i].K / 128 : kb;
-  int want = (int)(CUS / tiles);
-  if (want > kb / 4) want = kb / 4;
-  if (want > 16) want = 16;
-  for (c.splits = want > 1 ? want : 1; c.splits > 1 && plan_bytes(a, c) > WS_MAX; c.splits--) {
-  }
+  const long long want = CUS / tiles_of(a, FP128);  // 3 at most: `few` has the rest
+  c.splits = (int)(want < kb / 4 ? want : kb / 4);
+  if (c.splits < 1) c.splits = 1;
   return c;
 }
 
@@ -1065,8 +1084,10 @@ hipError_t launch_fp8(const Fp8Args& a, void* ws, hipStream_t s) {
   Launch l{};
   l.mt = (a.M + t.bm - 1) / t.bm;
   l.splits = c.splits;
-  l.counters = static_cast<unsigned*>(ws);
-  l.partial = static_cast<float*>(ws) + COUNTERS;
+  if (c.splits > 1) {
+    l.counters = static_cast<unsigned*>(ws);
+    l.partial = static_cast<float*>(ws) + COUNTERS;
+  }
   for (int i = 0; i < a.count; i++)
     l.tile0[i + 1] = l.tile0[i] + l.mt * ((a.p[i].N + t.bn - 1) / t.bn);
   const int tiles = l.tile0[a.count];

@@ -76,7 +76,8 @@ def two_calls(ops, act, workspace=rq.AUTO):
     (17, 128, 2048), (31, 256, 128), (33, 640, 1024), (48, 128, 256), (63, 256, 896),
     (64, 512, 512), (65, 384, 384), (100, 256, 1280), (127, 128, 128), (128, 256, 256),
     (129, 512, 640), (200, 1024, 384), (255, 256, 1024), (257, 768, 512), (300, 2048, 256),
-    (513, 640, 768), (700, 1280, 384), (1100, 768, 256)])
+    (513, 640, 768), (700, 1280, 384), (1100, 768, 256), (1100, 1152, 384), (140, 8448, 640),
+    (1281, 1408, 1152), (50, 16640, 256), (2400, 4352, 384), (650, 16384, 128), (4500, 3968, 256)])
 def test_sizes(M, N, K, out):
     e8m0 = (M + N // 128 + K // 128) % 2 == 0
     say(f"[gemm_fp8] M {M} N {N} K {K} {out} e8m0 {e8m0}")
@@ -96,6 +97,30 @@ def test_sizes(M, N, K, out):
 def test_odd_numbers_of_outputs(M, N, out, e8m0):
     say(f"[gemm_fp8] odd N {N} M {M} {out}")
     check(operands(M, N, 384, e8m0, M * 1000 + N), out)
+
+
+@pytest.mark.parametrize("e8m0", [True, False])
+@pytest.mark.parametrize("M,N", [(1300, 1025), (129, 8705), (2050, 1157), (2401, 4345), (2305, 4610)])
+def test_many_odd_binary16_outputs(M, N, e8m0):
+    say(f"[gemm_fp8] M {M} odd N {N}")
+    check(operands(M, N, 384, e8m0, M + N), "f16")
+
+
+@pytest.mark.parametrize("e8m0", [True, False])
+@pytest.mark.parametrize("M,N,K,ranges", [
+    (1100, 1152, 1024, 2), (130, 8320, 2176, 1), (130, 8192, 2176, 2), (1500, 1408, 4224, 1),
+    (1500, 1280, 4224, 2), (257, 4096, 10240, 2), (1025, 1024, 1536, 3)])
+def test_ranges_of_k_through_a_workspace(M, N, K, ranges, e8m0):
+    """Sizes on both sides of splitting K, with the workspace and without; binary16
+    and E4M3 alike."""
+    tiles = -(-M // 128) * -(-N // 128)
+    size = rq.rq_gemm_fp8_workspace_size([(N, K)], M, int(e8m0), rq.RQ_TYPE_F16)
+    assert size == (65536 + tiles * ranges * 65536 if ranges > 1 else 0)
+    ops = operands(M, N, K, e8m0, M + N + K)
+    for ws in (rq.AUTO, None, rq.AUTO):
+        check(ops, "f16", workspace=ws)
+        got, want = run(ops, "e4m3", act=1, workspace=ws), two_calls(ops, 1, ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 @pytest.mark.parametrize("M", [1, 5, 16, 40, 64, 90, 250, 520])
@@ -229,12 +254,43 @@ def test_graph_replays_and_the_workspace_stays_zero(M, N, K):
         x.bitwise_xor_(0x80)
 
 
+def test_graph_replays_with_ranges_of_k():
+    M, N, K = 1100, 1152, 2560
+    ops = operands(M, N, K, True, 3)
+    size = rq.rq_gemm_fp8_workspace_size([(N, K)], M, rq.RQ_SCALE_E8M0, rq.RQ_TYPE_F16)
+    area = torch.zeros(size // 4, dtype=torch.int32, device="cuda")
+    st = torch.cuda.Stream()
+    y = torch.empty((M, N), dtype=torch.float16, device="cuda")
+    torch.cuda.synchronize()
+    call = rq.prepare("rq_gemm_fp8", [(*ops, None, y, N, K)], stream=st, workspace=area)
+    x = ops[2].view(torch.uint8)
+    eager = []
+    for k in range(2):
+        call()
+        torch.cuda.synchronize()
+        eager.append(y.clone())
+        x.bitwise_xor_(0x80)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        call()
+    for k in range(4):
+        y.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, eager[k % 2])
+        assert not bool(area[:16384].any())
+        x.bitwise_xor_(0x80)
+
+
 def test_two_streams_at_once():
     """Each stream's calls with the workspace that the binding keeps for it."""
-    work = [(operands(40, 512, 8192, True, s), operands(200, 384, 2560, False, s)) for s in (1, 2)]
+    work = [(operands(40, 512, 8192, True, s), operands(200, 384, 2560, False, s),
+             operands(300, 4096, 2560, False, s)) for s in (1, 2)]
+    outs = ("f32", "f32", "f16")
 
     def step(w):
-        return [run(o) for o in w]
+        return [run(o, out) for o, out in zip(w, outs)]
     want = [step(w) for w in work]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -243,8 +299,9 @@ def test_two_streams_at_once():
         for w, s, g in zip(work, streams, got):
             with torch.cuda.stream(s):
                 ys = []
-                for o in w:
-                    y = torch.empty((o[2].shape[0], o[0].shape[0]), device="cuda")
+                for o, out in zip(w, outs):
+                    y = torch.empty((o[2].shape[0], o[0].shape[0]), device="cuda",
+                                    dtype=torch.float16 if out == "f16" else torch.float32)
                     rq.rq_gemm_fp8([(*o, None, y, *o[0].shape)])
                     ys.append(y)
                 g.append(ys)
