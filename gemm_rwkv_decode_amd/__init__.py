@@ -33,8 +33,8 @@ __all__ = [
     "rq_gemv_batched", "rq_gemm_smallm", "rq_gemm_smallm_ws", "rq_gemm_smallm_workspace_size",
     "rq_gemm_smallm_noalloc", "rq_shift", "rq_lora", "rq_lora_workspace_size", "rq_wkv7",
     "rq_logits", "rq_quant_fp8", "rq_gemm_fp8", "rq_gemm_fp8_workspace_size", "rq_groupnorm",
-    "RQ_ACT_NONE", "RQ_ACT_RELU2", "RQ_ACT_SILU", "rq_status_string", "rq_version", "prepare", "gemm_workspace",
-    "lib", "LIB_PATH",
+    "RQ_ACT_NONE", "RQ_ACT_RELU2", "RQ_ACT_SILU", "rq_status_string", "rq_version", "prepare",
+    "gemm_workspace", "lib", "LIB_PATH",
 ]
 
 RQ_OK = 0
@@ -622,8 +622,21 @@ def _gemm_fp8_cargs(problems, *, act=RQ_ACT_NONE, stream=None, workspace=AUTO):
         arr[i] = RqFp8Problem(_e4m3("w", w, (N, K)), _scales("w_scales", ws, kind, (nb, kb)),
                               _e4m3("x", x, (M, K)), _scales("x_scales", xs, kind, (M, kb)),
                               _typed("y_in", y_in, "float32", (M, N)), py, ps, int(N), int(K))
+    if isinstance(workspace, str) and workspace == AUTO:
+        import torch
+        # none for graphs, which may be replayed on several streams at once
+        if torch.cuda.is_current_stream_capturing() or \
+                not _gemm_fp8_bytes(arr, len(problems), M, kind, out)[1]:
+            workspace = None
     return (arr, len(problems), M, kind, out, int(act),
             *_ws_args(workspace, stream, problems[0][2]), _stream(stream, problems[0][2]))
+
+
+def _gemm_fp8_bytes(arr, count, M, kind, out):
+    """(status, bytes)"""
+    b = ctypes.c_size_t(0)
+    st = lib().rq_gemm_fp8_workspace_size(arr, count, M, kind, out, ctypes.byref(b))
+    return st, b.value
 
 
 def rq_gemm_fp8(problems, act=RQ_ACT_NONE, stream=None, workspace=AUTO):
@@ -634,8 +647,11 @@ def rq_gemm_fp8(problems, act=RQ_ACT_NONE, stream=None, workspace=AUTO):
     None), y float32 or float16 [M][N], or a pair (E4M3 [M][N], scales [M][N /
     128]) for the float16 output quantized as rq_quant_fp8 with ``act`` does.
     All share M, the type of scales and the type of y.  ``workspace``: AUTO
-    (the binding's, per stream), a tensor of rq_gemm_fp8_workspace_size bytes
-    (zero before its first use), or None to keep K whole."""
+    (the binding's, per stream, if the call uses one; None in a graph's
+    capture), a tensor of rq_gemm_fp8_workspace_size bytes (zero before its
+    first use), or None to keep K whole.  A prepared call keeps the workspace
+    that it was prepared with, so give it its own if graphs that hold it run at
+    once."""
     st = lib().rq_gemm_fp8(*_gemm_fp8_cargs(problems, act=act, stream=stream,
                                             workspace=workspace))
     if st != RQ_OK:
@@ -649,12 +665,10 @@ def rq_gemm_fp8_workspace_size(shapes, M, scale_type, out_type):
     arr = (RqFp8Problem * len(shapes))()
     for i, (N, K) in enumerate(shapes):
         arr[i].N, arr[i].K = int(N), int(K)
-    b = ctypes.c_size_t(0)
-    st = lib().rq_gemm_fp8_workspace_size(arr, len(shapes), int(M), int(scale_type),
-                                          int(out_type), ctypes.byref(b))
+    st, need = _gemm_fp8_bytes(arr, len(shapes), int(M), int(scale_type), int(out_type))
     if st != RQ_OK:
         raise RqError("rq_gemm_fp8_workspace_size", st)
-    return b.value
+    return need
 
 
 def _groupnorm_cargs(y, groups, weight, bias, eps, out, *, bonus=None, gate=None,

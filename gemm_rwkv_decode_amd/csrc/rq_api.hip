@@ -2,6 +2,7 @@
 // validation on the host, format dispatch, launch on the caller's stream.
 #include <hip/hip_runtime.h>
 
+#include <float.h>
 #include <stdint.h>
 #include <stdlib.h>
 #include <string.h>
@@ -892,7 +893,7 @@ rq_status rq_groupnorm(const rq_groupnorm_args* args, void* stream) {
     return RQ_ERR_SHAPE;
   const int size = g.C / g.groups;
   if (size != 32 && size != 64 && size != 128 && size != 256) return RQ_ERR_SHAPE;
-  if (!(g.eps >= 0.0f) || g.eps > 3.4e38f) return RQ_ERR_SHAPE;
+  if (!(g.eps >= 0.0f) || g.eps > FLT_MAX) return RQ_ERR_SHAPE;
   const size_t c = g.C, n = (size_t)g.T * c, e = type_bytes(g.input_type);
   const Operand in[] = {array(g.y, n * 4), array(g.weight, c * 4), array(g.bias, c * 4),
                         array(g.r, n * e), array(g.r ? g.k : nullptr, n * e),

@@ -972,6 +972,7 @@ long long tiles_of(const Fp8Args& a, Kind kind) {
   return n;
 }
 
+constexpr int MAX_TILES = 1 << 22;  // of 512 work-items, of which a launch has fewer than 2^32
 constexpr int COUNTERS = 16384;  // dwords at the front of a workspace, of which tiles count in a few
 
 size_t plan_bytes(const Fp8Args& a, const Plan& c) {
@@ -988,7 +989,8 @@ Kind choose_wide(const Fp8Args& a) {
   // where they do not, which read w half as often (96 rows, 8192 outputs of K = 2048:
   // 11.0, and in tiles of 16 rows 16.2).
   if (a.out == OUT_E4M3) return a.M <= 16 || tiles_of(a, RING8X1) <= CUS ? RING8X1 : RING8X2;
-  if (a.M <= 16) return a.M > 4 && tiles_of(a, ROWS64) >= 192 ? ROWS64 : ROWS16;
+  if (a.M <= 16)
+    return (a.M > 4 && tiles_of(a, ROWS64) >= 192) || tiles_of(a, ROWS16) > MAX_TILES ? ROWS64 : ROWS16;
   if (a.out == OUT_F32) {
     if (a.M <= 64 && tiles_of(a, WIDE64) >= 2 * CUS) return WIDE64;
     if (tiles_of(a, WIDE128) >= CUS) return WIDE128;

@@ -36,12 +36,11 @@ __device__ __forceinline__ float silu(float g) {
 template <int LPR, bool HALF>
 __global__ void __launch_bounds__(256)
 k_groupnorm(const GroupnormArgs a) {
-  const u32 parts = (a.C / 4 + 255) / 256;             // workgroups of a token
-  const int c = (blockIdx.x % parts * 256 + threadIdx.x) * 4;  // the lane's four channels
-  if (c >= a.C) return;                                // (whole groups and blocks end here)
+  // the lane's four channels; lanes without any are whole groups and blocks
+  const size_t i = (((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= (size_t)a.T * a.C) return;
+  const int c = (u32)(i / 4) % (u32)(a.C / 4) * 4;
   constexpr float inv_g = 1.0f / (4 * LPR);
-  const size_t t = blockIdx.x / parts;
-  const size_t i = t * a.C + c;
   f4 y = load4(a.y, i);
   f4 z = {0, 0, 0, 0};
   const float mean = group_sum<LPR>(y[0] + y[1] + y[2] + y[3]) * inv_g;
@@ -86,7 +85,10 @@ k_groupnorm(const GroupnormArgs a) {
 
 template <int LPR>
 void launch_lpr(const GroupnormArgs& a, hipStream_t s) {
-  const dim3 grid((a.C / 4 + 255) / 256 * (unsigned)a.T);
+  // a launch has fewer than 2^32 work-items along an axis, so the largest calls take
+  // a second one
+  const size_t n = ((size_t)a.T * (a.C / 4) + 255) / 256, rows = n > 1 << 23 ? 2 : 1;
+  const dim3 grid((unsigned)((n + rows - 1) / rows), (unsigned)rows);
   if (a.half)
     hipLaunchKernelGGL((k_groupnorm<LPR, true>), grid, dim3(256), 0, s, a);
   else

@@ -16,11 +16,6 @@ namespace {
 constexpr int PER = 8;               // values of a lane
 constexpr int LANES = 128 / PER;     // lanes of a block
 
-template <bool HALF>
-struct Values {
-  u32x4 v[HALF ? 1 : 2];
-};
-
 template <bool HALF, bool RELU2>
 __global__ void __launch_bounds__(256)
 k_quant(const void* x, u32x2* q, void* scales, size_t blocks, int e8m0) {

@@ -507,26 +507,32 @@ typedef struct {
  *   out_type RQ_TYPE_F32: binary32.  Every sum is held in binary32: errors are
  *     about 2^-23 of the sum of the products' magnitudes.
  *   RQ_TYPE_F16: rounded to binary16 (past 65504 infinite); no y_in.
- *   RQ_TYPE_E4M3: what rq_quant_fp8 with `act` makes of the RQ_TYPE_F16 output, to
- *     the bit, without that output in memory; no y_in, N % 128 == 0.
- *     Calls of many rows take the FP8 matrix instructions for these two.  Those
+ *   RQ_TYPE_E4M3: what rq_quant_fp8 with `act` makes of the RQ_TYPE_F16 output (of
+ *     a call that has a workspace too, or none too), to the bit, without that output
+ *     in memory; no y_in, N % 128 == 0.
+ *     Calls of more than 16 rows may take the FP8 matrix instructions for these two
+ *     (they do where the outputs fill the card with tiles of 128 x 128).  Those
  *     drop what lies 2^-13 or more below the largest of eight products: within
  *     2^-10 of the sum of the products' magnitudes, about 2^-15 of an ordinary
  *     output.
  *   act: RQ_ACT_NONE, or RQ_ACT_RELU2 with RQ_TYPE_E4M3.
  * NaN in an operand or a scale reaches its outputs.  The product of an x scale and
  * a w scale has to be a normal binary32 number (or zero); what a smaller or larger
- * one gives is not specified.  Rows are independent: what is in row m of x does
+ * one gives is not specified, but for a smaller one of a block whose values of x or
+ * w are all zero, which adds zero.  Rows are independent: what is in row m of x does
  * not change another row's results.
  *   workspace: device memory, 16-byte aligned, overlapping nothing else, whose first
  *   64 KiB are zero before its first use; every call leaves them zero (a workspace of
- *   rq_gemm_smallm_ws will do).  Calls that share it must not overlap in time.  NULL
- *   keeps K whole, which is slower for few rows.  RQ_ERR_SCRATCH: smaller than
+ *   rq_gemm_smallm_ws will do).  Calls that share it must not overlap in time, in
+ *   graphs neither.  Only RQ_TYPE_F16 and RQ_TYPE_E4M3 outputs that make more than 64
+ *   and at most 128 tiles of 128 x 128 use one, to split K; NULL keeps K whole there
+ *   too, which takes up to twice as long.  RQ_ERR_SCRATCH: smaller than
  *   rq_gemm_fp8_workspace_size reports.
  * Results are deterministic; which sums are taken together follows from the sizes
  * of the call (and from whether it has a workspace).
  * Shape rules: 1 <= count <= RQ_FP8_MAX_BATCH, 1 <= M <= RQ_MAX_TOKENS, 1 <= N <=
- * 1 << 24, 128 <= K <= RQ_FP8_MAX_K, K % 128 == 0, at most RQ_FP8_MAX_VALUES outputs of a product.
+ * 1 << 24, 128 <= K <= RQ_FP8_MAX_K, K % 128 == 0, at most RQ_FP8_MAX_VALUES outputs
+ * of a product.
  * `problems` is a host array the call reads before it returns.
  */
 rq_status rq_gemm_fp8(const rq_fp8_problem* problems, int count, int M, int scale_type,
