@@ -1,5 +1,18 @@
 // rq_gemm_fp8.hip -- products of block-scaled E4M3 operands:
 //   y[m][n] = y_in[m][n] + sum_b xs[m][b] ws[n/128][b] sum_{k in b} x[m][k] w[n][k].
+//
+// Few rows are bound by w, a byte a weight from memory; many by the matrix units.
+// Times below are of one MI355X, whose memory copies at 5.07 TB/s and whose library
+// products reach 3077 TFLOP/s in FP8 and 1434 in binary16.
+//
+//   k_rows  up to 16 rows: operands from memory straight to registers.  Three
+//           products of 4096 x 4096 and one row 9.8 us (50.4 MB: 5.2 TB/s).
+//   k_ring  some rows: each wave takes every eighth block of K through LDS of its
+//           own.  32 rows, 4096 x 16384: 17.6 us; 203 rows, 2560 x 10240: 22.6.
+//   k_tile  many rows: tiles of a workgroup staged through LDS.  61 rows of 65536 x
+//           2048, binary32: 38.4 us; 2047 rows of 16384 x 4096, binary32: 262 us.
+//   k_big   256 x 256 tiles for binary16 and E4M3 outputs.  2047 rows of 16384 x 4096
+//           to E4M3 124 us (2220 TFLOP/s); 4001 rows of 4096 x 4096 2420 TFLOP/s.
 #include "rq_common.h"
 #include "rq_fp8.h"
 #include "rq_internal.h"
@@ -17,6 +30,11 @@ typedef int i8v __attribute__((ext_vector_type(8)));
 //          multiply-add by the scales for each block's sum;
 //   FP8S   the FP8 matrix instruction of depth 128, the same multiply-add;
 //   FP8E   the FP8 matrix instruction with the power of two as its own scale.
+// The FP8 instructions align the products of eight neighbouring k to the largest and
+// drop what is 2^-13 of it or less: measured, an error of 1.3e-5 to 4e-5 of the
+// 2-norm of y.  That is far inside the rounding of binary16 or E4M3 outputs, so those
+// take them, and not inside that of binary32 outputs, which are WIDE: 1e-8 to 8e-8,
+// at half the rate and a conversion for each pair of codes.
 enum Mode { WIDE, FP8S, FP8E };
 
 // The 16 E4M3 numbers of a 16-byte piece as two operands of 8.
@@ -71,7 +89,9 @@ struct Launch {
   float* partial;            // [tile][split][outputs of a tile, as the lanes hold them]
 };
 
-// WN x WM waves, each 16 TN outputs of 16 TM rows; ST stages of 128 columns.
+// WN x WM waves, each 16 TN outputs of 16 TM rows; ST stages of 128 columns.  w is
+// the instruction's first operand, so that a lane has four consecutive outputs of a
+// row.
 template <int WN_, int WM_, int TN_, int TM_, int ST_>
 struct Tile {
   static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, ST = ST_;
@@ -416,8 +436,14 @@ __device__ __forceinline__ void phase_end() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
+// Many rows: a ring of ST stages that all waves copy into (memory to LDS, nothing
+// through registers) and read; one barrier a step.  The scales of SC blocks are
+// multiplied together once for a row and 128 outputs and wait in LDS too.  Two
+// workgroups share a compute unit, so one multiplies while the other is at its
+// barrier or its outputs: a tile twice as wide, alone on its compute unit, gains 2%
+// at K = 16384 and loses 5 to 40% at K = 4096 and below.
 template <typename T, Mode MODE, bool E8>
-__global__ void __launch_bounds__(T::THREADS, T::W / 2 > 0 ? T::W / 2 : 1)
+__global__ void __launch_bounds__(T::THREADS, T::W / 2)
 k_tile(const Fp8Args a, const Launch l) {
   constexpr int W = T::W, TN = T::TN, TM = T::TM, ST = T::ST, SC = T::SC;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
@@ -574,8 +600,11 @@ k_tile(const Fp8Args a, const Launch l) {
 // from LDS while the other multiplies.  A step (128 columns) is four phases:
 // read x and half of w, multiply, read the other half, multiply; the second group
 // is one phase behind, so that the matrix units of a SIMD, which has a wave of
-// each group, always have work.
-
+// each group, always have work.  (4001 rows of three 2560 x 2560 to binary16: 246 us
+// with 128 x 128 tiles and a barrier a step, 89 so.)  256 x 256 because a tile's
+// stage is 64 KB for 16.8 MFLOP: LDS reads, 96 KB of them a step, keep below the
+// matrix units' time.  What is left is the clock, which falls to 2.0 to 2.2 GHz under
+// these instructions, and the start and end of a tile (5 and up to 9 us of 60).
 template <typename T, Mode MODE>
 __global__ void __launch_bounds__(T::THREADS, 2) k_big(const Fp8Args a, const Launch l) {
   constexpr int W = T::W, TN = T::TN, TM = T::TM, SC = T::SC;
@@ -733,9 +762,10 @@ __global__ void __launch_bounds__(T::THREADS, 2) k_big(const Fp8Args a, const La
   store_tile<TM>(a, p, n0 + wn * 128, m0 + wm * TM * 16, acc);
 }
 
-// Up to 16 rows, binary32 outputs: a workgroup takes 16 TW outputs and its eight
-// waves every eighth block of K, from memory straight to the operands, D blocks ahead;
-// the eight sums meet in LDS.  No wave waits for another before that.
+// Up to 16 rows: a workgroup takes 16 TW outputs and its eight waves every eighth
+// block of K, from memory straight to the operands, D blocks ahead; the eight sums
+// meet in LDS.  No wave waits for another before that, and no sums go through memory
+// (K split over workgroups instead took 17.1 us where this takes 9.8).
 constexpr int SW = 8;
 template <int TW>
 struct Block {
@@ -819,10 +849,15 @@ hipError_t launch_rows(const Fp8Args& a, const Launch& l, int tiles, hipStream_t
   return hipGetLastError();
 }
 
-// Some rows, binary32 outputs: a workgroup takes 16 TN outputs of 16 TM rows, and
-// each of its eight waves every eighth block of K through a ring of ST stages in LDS
-// of its own; the eight sums meet at the end.  No wave waits for another before that, and
-// no sums go through memory.
+// Some rows: a workgroup takes 16 TN outputs of 16 TM rows, and each of its eight
+// waves every eighth block of K through a ring of ST stages in LDS of its own; the
+// eight sums meet at the end.  No wave waits for another before that, and no sums go
+// through memory (32 rows, 4096 x 16384: 26.4 us with K split over workgroups of
+// k_tile, 17.6 so).  Through LDS because its copies take whole lines of eight rows;
+// the operands' own layout is 64 bytes of sixteen, and loads of that straight to
+// registers are slower from two row tiles on (203 rows, 2560 x 10240: 44.9 us).
+// Bound by the copies (a wave has one stage in flight where ST is 1) and, from three
+// row tiles on, by widening both operands in every wave.
 template <int TN, int TM, int ST, bool E8>
 __global__ void __launch_bounds__(64 * SW, 2) k_ring(const Fp8Args a, const Launch l) {
   constexpr int W = SW;
@@ -944,7 +979,8 @@ hipError_t launch_ring(const Fp8Args& a, const Launch& l, int tiles, hipStream_t
 typedef Tile<2, 4, 8, 4, 2> T256;  // 256 outputs x 256 rows
 typedef Tile<1, 4, 8, 2, 2> T128;  // 128 x 128
 // binary16 operands, widened by every wave that reads them: as square as they go
-typedef Tile<2, 4, 4, 2, 2> W128;  // 128 x 128
+// (2047 rows of 16384 x 4096: 262 us, by eight waves of 64 x 32 280)
+typedef Tile<2, 2, 4, 4, 2> W128;  // 128 x 128
 typedef Tile<4, 2, 2, 2, 3> W64;   // 128 x 64
 
 // What a call runs: a kernel with its tile, and the ranges of K.
@@ -953,11 +989,10 @@ enum Kind {
   FP256
 };
 struct Shape {
-  int bn, bm, waves;
+  int bn, bm;
 };
-constexpr Shape SHAPES[] = {{16, 16, 8},  {64, 16, 8},  {16, 32, 8},   {32, 32, 8},  {64, 32, 8},
-                            {64, 48, 8},  {64, 64, 8},  {128, 16, 8},  {128, 32, 8}, {128, 64, 8},
-                            {128, 128, 8}, {128, 128, 4}, {256, 256, 8}};
+constexpr Shape SHAPES[] = {{16, 16},  {64, 16},  {16, 32},  {32, 32},  {64, 32},   {64, 48},  {64, 64},
+                            {128, 16}, {128, 32}, {128, 64}, {128, 128}, {128, 128}, {256, 256}};
 struct Plan {
   Kind kind;
   int splits;
@@ -972,7 +1007,6 @@ long long tiles_of(const Fp8Args& a, Kind kind) {
   return n;
 }
 
-constexpr int MAX_TILES = 1 << 22;  // of 512 work-items, of which a launch has fewer than 2^32
 constexpr int COUNTERS = 16384;  // dwords at the front of a workspace, of which tiles count in a few
 
 size_t plan_bytes(const Fp8Args& a, const Plan& c) {
@@ -989,27 +1023,41 @@ Kind choose_wide(const Fp8Args& a) {
   // where they do not, which read w half as often (96 rows, 8192 outputs of K = 2048:
   // 11.0, and in tiles of 16 rows 16.2).
   if (a.out == OUT_E4M3) return a.M <= 16 || tiles_of(a, RING8X1) <= CUS ? RING8X1 : RING8X2;
-  if (a.M <= 16)
-    return (a.M > 4 && tiles_of(a, ROWS64) >= 192) || tiles_of(a, ROWS16) > MAX_TILES ? ROWS64 : ROWS16;
-  if (a.out == OUT_F32) {
-    if (a.M <= 64 && tiles_of(a, WIDE64) >= 2 * CUS) return WIDE64;
-    if (tiles_of(a, WIDE128) >= CUS) return WIDE128;
-  }
   int kb = 0;
   for (int i = 0; i < a.count; i++) kb = a.p[i].K / 128 > kb ? a.p[i].K / 128 : kb;
-  // What a tile costs: its start and end once in a round of all compute units (in
-  // two rounds where two workgroups share one), then the blocks of K one after another.
+  // Rows straight to registers, us beside the best of the tiles below:
+  //   rows x outputs x K       64 outputs  16 outputs  tiles
+  //   1 x 16384 x 4096            12.0        12.9      13.4
+  //   1 x 4096 x 4096, three      10.8         9.9      11.3
+  //   8 x 16384 x 4096            12.8        16.2      13.5
+  //   16 x 65536 x 2048           34.1        44.2      31.1
+  //   16 x 768 x 768               4.3         3.1       3.9
+  //   16 x 4096 x 4096, three     13.0        15.7      11.5
+  //   4 x 4096 x 16384            35.0        14.8      13.8
+  //   16 x 4096 x 16384           40.5        19.8      14.6
+  if (a.M <= 16) {
+    const long long n = tiles_of(a, ROWS64);
+    if (n >= CUS && (a.M <= 4 || n < 4 * CUS || a.out != OUT_F32)) return ROWS64;
+    if (a.M <= 4 || (tiles_of(a, ROWS16) <= CUS && kb <= 32)) return ROWS16;
+  }
+  // What a compute unit takes for one tile, and for two (at once, where two fit): the
+  // start and end, and a block of K, in us, fitted to about 30 sizes.  It puts, say,
+  // 61 rows x 32768 x 2048 in tiles of 64 rows (17.0 us; rings 21.7, 128 rows 23.3),
+  // 600 x 4096 x 4096 in rings (37.4; 39.7, 40.3), 800 x 4096 x 4096 in tiles of 128
+  // (41.7; rings 50.9).
   const struct {
     Kind kind;
-    int shared;
-    double ends, block;  // us
-  } rings[] = {{RING1X2, 1, 3.4, 0.11}, {RING2X2, 2, 3.2, 0.12}, {RING4X2, 1, 4.3, 0.155},
-               {RING4X3, 1, 5.0, 0.2},  {RING4X4, 1, 5.4, 0.25}};
+    double ends, block, ends2, block2;
+  } tiles[] = {{RING1X2, 3.4, 0.11, 6.8, 0.22},  {RING2X2, 3.2, 0.12, 3.2, 0.24},
+               {RING4X2, 4.3, 0.155, 8.6, 0.31}, {RING4X3, 5.0, 0.2, 10.0, 0.4},
+               {RING4X4, 5.4, 0.25, 10.8, 0.5},  {WIDE64, 3.0, 0.75, 4.5, 1.2},
+               {WIDE128, 4.5, 1.15, 5.8, 1.85}};
   Kind best = RING4X4;
   double least = 1e30;
-  for (const auto& q : rings) {
-    const long long n = tiles_of(a, q.kind), both = (long long)CUS * q.shared;
-    const double t = (double)((n + CUS - 1) / CUS) * kb * q.block + (double)((n + both - 1) / both) * q.ends;
+  for (const auto& q : tiles) {
+    if ((q.kind == WIDE64 || q.kind == WIDE128) && a.out != OUT_F32) continue;
+    const long long n = (tiles_of(a, q.kind) + CUS - 1) / CUS;  // of a compute unit
+    const double t = (double)(n / 2) * (q.ends2 + kb * q.block2) + (double)(n % 2) * (q.ends + kb * q.block);
     if (t < least) least = t, best = q.kind;
   }
   return best;

@@ -77,7 +77,9 @@ def two_calls(ops, act, workspace=rq.AUTO):
     (64, 512, 512), (65, 384, 384), (100, 256, 1280), (127, 128, 128), (128, 256, 256),
     (129, 512, 640), (200, 1024, 384), (255, 256, 1024), (257, 768, 512), (300, 2048, 256),
     (513, 640, 768), (700, 1280, 384), (1100, 768, 256), (1100, 1152, 384), (140, 8448, 640),
-    (1281, 1408, 1152), (50, 16640, 256), (2400, 4352, 384), (650, 16384, 128), (4500, 3968, 256)])
+    (1281, 1408, 1152), (50, 16640, 256), (2400, 4352, 384), (650, 16384, 128), (4500, 3968, 256),
+    (1, 16384, 256), (3, 16512, 1152), (9, 16640, 640), (16, 65536, 256), (7, 4096, 4096),
+    (12, 4096, 4224), (61, 32768, 384), (800, 4096, 256)])
 def test_sizes(M, N, K, out):
     e8m0 = (M + N // 128 + K // 128) % 2 == 0
     say(f"[gemm_fp8] M {M} N {N} K {K} {out} e8m0 {e8m0}")
