@@ -313,6 +313,54 @@ def test_two_streams_at_once():
             assert all(torch.equal(a, b) for a, b in zip(ys, w))
 
 
+def test_two_graphs_at_once():
+    """Graphs of calls that would split K, captured on one stream that has a workspace
+    and replayed on two: each gives what the call without a workspace does."""
+    M, N, K = 1100, 1152, 2560
+    work = [operands(M, N, K, True, s) for s in (1, 2)]
+    want = [run(o, "f16", workspace=None) for o in work]
+    ys = [torch.empty((M, N), dtype=torch.float16, device="cuda") for _ in work]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs = []
+    with torch.cuda.stream(side):
+        for o, y in zip(work, ys):
+            rq.rq_gemm_fp8([(*o, None, y, N, K)])
+    torch.cuda.synchronize()
+    for o, y in zip(work, ys):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            for _ in range(10):
+                rq.rq_gemm_fp8([(*o, None, y, N, K)])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for y in ys:
+            y.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, w) for y, w in zip(ys, want))
+
+
+@pytest.mark.parametrize("out", OUTS)
+def test_zero_blocks_beside_the_smallest_scales(out):
+    """A row that rq_quant_fp8 makes of zeros (scales of 2^-126) and weights with
+    scales of 2^-20: the products of the scales are below 2^-126, and add zero."""
+    for M, N in ((3, 256), (40, 384), (300, 384), (1300, 1024), (4200, 3840)):
+        w, ws, x, xs = operands(M, N, 256, True, M)
+        x.view(torch.uint8)[1] = 0
+        xs.view(torch.uint8)[1] = 1
+        ws.view(torch.uint8)[:] = 107
+        y = run((w, ws, x, xs), out)
+        if out == "e4m3":
+            assert not bool((y[0][1] & 127).any()) and bool((y[1][1] == 1).all())
+        else:
+            check((w, ws, x, xs), out)
+            assert not bool(y[1].any())
+
+
 def test_the_same_call_gives_the_same_bits():
     ops = operands(61, 1000, 5120, False, 9)
     first = run(ops)

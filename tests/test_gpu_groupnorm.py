@@ -149,3 +149,30 @@ def test_in_place_and_many_tokens():
          for k, v in a.items()}
     check(b, 7)
     assert torch.equal(run(b, 7), want[rows])
+
+
+@pytest.mark.parametrize("out", ["f32", "e4m3"])
+def test_graph_replays_on_a_stream_of_its_own(out):
+    T, C, H = 37, 768, 12
+    a = make(T, C, 3)
+    d = {k: cuda(v) for k, v in a.items()}
+    o = torch.empty((T, C), device="cuda") if out == "f32" else \
+        (torch.empty((T, C), dtype=torch.uint8, device="cuda"),
+         torch.empty((T, C // 128), dtype=torch.uint8, device="cuda"))
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call = rq.prepare("rq_groupnorm", d["y"], H, d["weight"], d["bias"], EPS, o, stream=st,
+                      bonus=d["bonus"], gate=d["gate"], act=rq.RQ_ACT_SILU)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        call()
+    for k in range(3):
+        d["gate"].mul_(-1.5)
+        d["y"].add_(0.25)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        b = dict(a, y=d["y"].cpu().numpy(), gate=d["gate"].cpu().numpy())
+        want = run(b, H, out, rq.RQ_ACT_SILU)
+        for x, y in zip((o,) if out == "f32" else o, (want,) if out == "f32" else want):
+            assert torch.equal(x, y)
