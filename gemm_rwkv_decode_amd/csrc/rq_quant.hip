@@ -4,8 +4,13 @@
 //
 // Rows are whole blocks, so the array is one list of blocks and the scales one
 // list beside it.  Sixteen lanes take a block, eight values each: a maximum over
-// the lanes by DPP, then exact products with 1/s and the conversion.  Bound by
-// memory: 2 or 4 bytes read and 1 written per value.
+// the lanes by DPP, then exact products with 1/s and the conversion.  Eight values
+// are one load of binary16 (two of binary32) and one store of 8 bytes, and sixteen
+// lanes are what DPP reaches without LDS.
+//
+// Bound by memory: 2 or 4 bytes read and 1 written per value.  2047 x 16384 binary32
+// values, squared above zero, take 29.7 us on one MI355X (168 MB: 5.6 TB/s, where a
+// copy does 5.07), 4593 x 2560 binary16 ones 6.8 us (35.6 MB: 5.2), one row a launch.
 #include "rq_common.h"
 #include "rq_fp8.h"
 #include "rq_internal.h"
