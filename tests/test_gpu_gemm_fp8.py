@@ -152,6 +152,14 @@ def test_codes_of_every_size(M, out):
         check(operands(M, 300, 640, e8m0, M, spread=True), out)
 
 
+@pytest.mark.parametrize("M,N", [(1300, 1100), (4200, 3900)])
+def test_codes_of_every_size_in_large_tiles(M, N):
+    for e8m0 in (True, False):
+        ops = operands(M, N, 640, e8m0, M, spread=True)
+        # binary16 outputs stay finite: codes to 448 twice, 640 of them, scales to 2^-3
+        check((ops[0], ops[1], ops[2], (ops[3].float() * 2.0 ** -11).to(ops[3].dtype)), "f16")
+
+
 def test_binary32_outputs_keep_binary32_sums():
     """The 2-norm of the errors beside that of y, on normal values: 640 products
     and five block sums of independent errors of at most 2 U of a partial sum."""
@@ -207,6 +215,41 @@ def test_rows_are_independent_and_nan_reaches_its_outputs(M, out):
         assert torch.equal(got[0][far], clean[0][far])
     else:
         assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("e8m0", [True, False])
+@pytest.mark.parametrize("out", OUTS)
+@pytest.mark.parametrize("M,N", [(1300, 1024), (4200, 3840)])
+def test_nan_and_independent_rows_in_large_tiles(M, N, out, e8m0):
+    """NaN in a row of x, in a row's scales, in an output's weights and in the scales
+    of 128 outputs; other values of the rows before do not matter."""
+    K = 640
+    w, ws, x, xs = operands(M, N, K, e8m0, M, spread=True)
+    clean = run((w, ws, x, xs), out)
+    x2, xs2, w2, ws2 = x.clone(), xs.clone(), w.clone(), ws.clone()
+    x2.view(torch.uint8)[M - 1, 200] = 0x7F
+    x2.view(torch.uint8)[1] = x2.view(torch.uint8)[1].flip(0)
+    w2.view(torch.uint8)[130, 7] = 0xFF
+    if e8m0:
+        xs2.view(torch.uint8)[M // 2, 3] = 0xFF
+        ws2.view(torch.uint8)[3, 4] = 0xFF
+    else:
+        xs2[M // 2, 3] = float("nan")
+        ws2[3, 4] = float("nan")
+    got = run((w2, ws2, x2, xs2), out)
+    hit = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+    hit[M - 1] = hit[M // 2] = True
+    hit[:, 130] = True
+    hit[:, 384:512] = True
+    rest = ~hit
+    rest[1] = False
+    if out == "e4m3":
+        q = (got[0] & 127) == 127
+        assert bool(q[hit].all())
+        rest[:, 128:256] = False                  # the scale of 130's block may move
+        assert torch.equal(got[0][rest], clean[0][rest])
+    else:
+        assert bool(torch.isnan(got[hit]).all()) and torch.equal(got[rest], clean[rest])
 
 
 @pytest.mark.parametrize("M", [3, 40, 200])
