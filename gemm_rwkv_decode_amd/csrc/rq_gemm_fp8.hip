@@ -10,7 +10,7 @@
 //   k_ring  some rows: each wave takes every eighth block of K through LDS of its
 //           own.  32 rows, 4096 x 16384: 17.6 us; 203 rows, 2560 x 10240: 22.6.
 //   k_tile  many rows: tiles of a workgroup staged through LDS.  61 rows of 65529 x
-//           2048, binary32: 33.9 us; 2047 rows of 16384 x 4096, binary32: 262 us.
+//           2048, binary32: 33.2 us; 2047 rows of 16384 x 4096, binary32: 256 us.
 //   k_big   256 x 256 tiles for binary16 and E4M3 outputs.  2047 rows of 16384 x 4096
 //           to E4M3 124 us (2220 TFLOP/s); 4001 rows of 4096 x 4096 2420 TFLOP/s.
 #include "rq_common.h"
@@ -984,7 +984,7 @@ typedef Tile<1, 4, 8, 2, 2> T128;  // 128 x 128
 // binary16 operands, widened by every wave that reads them: as square as they go
 // (2047 rows of 16384 x 4096: 262 us, by eight waves of 64 x 32 280)
 typedef Tile<2, 2, 4, 4, 2> W128;  // 128 x 128
-typedef Tile<4, 2, 2, 2, 3> W64;   // 128 x 64
+typedef Tile<2, 2, 4, 2, 2> W64;   // 128 x 64 (61 rows of 65529 x 2048: 28.1 us, by eight of 32 x 32 30.6)
 
 // What a call runs: a kernel with its tile, and the ranges of K.
 enum Kind {
@@ -1043,24 +1043,32 @@ Kind choose_wide(const Fp8Args& a) {
     if (n >= CUS && (a.M <= 4 || n < 4 * CUS || a.out != OUT_F32)) return ROWS64;
     if (a.M <= 4 || (tiles_of(a, ROWS16) <= CUS && kb <= 32)) return ROWS16;
   }
-  // What a compute unit takes for one tile, and for two (at once, where two fit): the
-  // start and end, and a block of K, in us, fitted to about 30 sizes.  It puts, say,
-  // 61 rows x 32768 x 2048 in tiles of 64 rows (17.0 us; rings 21.7, 128 rows 23.3),
-  // 600 x 4096 x 4096 in rings (37.4; 39.7, 40.3), 800 x 4096 x 4096 in tiles of 128
-  // (41.7; rings 50.9).
+  // What a compute unit takes for as many tiles as it has at once (`most`, or fewer):
+  // their start and end, and a block of K, in us, fitted to about 50 sizes.  It puts,
+  // say, 61 rows x 32768 x 2048 in tiles of 64 rows (18.0 us; rings 21.8, 128 rows
+  // 23.3), 600 x 4096 x 4096 too (38.2; 37.7, 40.7), 256 x 4096 x 4096 in rings (14.6;
+  // 26.9, 40.7), 1500 x 4096 x 4096 in tiles of 64 (55.8; 81.8, 62.5), 2047 x 4096 x
+  // 4096 in tiles of 128 (66.1; 64 rows 79.2).
   const struct {
     Kind kind;
-    double ends, block, ends2, block2;
-  } tiles[] = {{RING1X2, 3.4, 0.11, 6.8, 0.22},  {RING2X2, 3.2, 0.12, 3.2, 0.24},
-               {RING4X2, 4.3, 0.155, 8.6, 0.31}, {RING4X3, 5.0, 0.2, 10.0, 0.4},
-               {RING4X4, 5.4, 0.25, 10.8, 0.5},  {WIDE64, 3.0, 0.75, 4.5, 1.2},
-               {WIDE128, 4.5, 1.15, 5.8, 1.85}};
+    int most;
+    double us[3][2];
+  } tiles[] = {{RING1X2, 1, {{3.4, 0.11}}},
+               {RING2X2, 2, {{3.2, 0.12}, {3.2, 0.24}}},
+               {RING4X2, 1, {{4.3, 0.155}}},
+               {RING4X3, 1, {{5.0, 0.2}}},
+               {RING4X4, 1, {{5.4, 0.25}}},
+               {WIDE64, 3, {{3.0, 0.8}, {4.0, 1.1}, {4.5, 1.6}}},
+               {WIDE128, 2, {{4.5, 1.15}, {5.8, 1.85}}}};
   Kind best = RING4X4;
   double least = 1e30;
   for (const auto& q : tiles) {
     if ((q.kind == WIDE64 || q.kind == WIDE128) && a.out != OUT_F32) continue;
     const long long n = (tiles_of(a, q.kind) + CUS - 1) / CUS;  // of a compute unit
-    const double t = (double)(n / 2) * (q.ends2 + kb * q.block2) + (double)(n % 2) * (q.ends + kb * q.block);
+    auto us = [&](long long at_once) {
+      return at_once ? q.us[at_once - 1][0] + kb * q.us[at_once - 1][1] : 0.0;
+    };
+    const double t = (double)(n / q.most) * us(q.most) + us(n % q.most);
     if (t < least) least = t, best = q.kind;
   }
   return best;
