@@ -95,6 +95,9 @@ const fake::Launch& launched(const char* what, long long a, long long b, long lo
 }
 }  // namespace
 
+// Every kernel has sizes that take it.
+int taken[rq::FP256 + 1][3];
+
 static void products() {
   const int ms[] = {1, 2, 4, 5, 8, 16, 17, 32, 33, 61, 64, 65, 100, 128, 129, 200, 256, 300, 511, 512,
                     700, 1000, 1100, 1500, 2047, 2048, 2500, 4001, 4352, 10000, 1 << 20, 1 << 24};
@@ -127,6 +130,7 @@ static void products() {
               for (int ws = 0; ws < 2; ws++) {
                 a.out = out;
                 const rq::Plan c = rq::choose(a, ws != 0);
+                taken[c.kind][out]++;
                 if (out) plans[out - 1][ws] = c;
                 expect(c.splits > 1 ? ws && bytes == rq::plan_bytes(a, c) : !ws || !bytes, "workspace", m, n, k);
                 expect(c.splits <= k / 128, "ranges of K", m, n, k);
@@ -195,6 +199,13 @@ static void norms() {
 
 int main() {
   products();
+  for (int k = 0; k <= rq::FP256; k++) {
+    const bool quantized = k == rq::RING8X1 || k == rq::RING8X2 || k >= rq::FP128;
+    const bool binary32 = k < rq::RING8X1 || k == rq::WIDE64 || k == rq::WIDE128;
+    const bool binary16 = k < rq::RING8X1 || k >= rq::FP128;
+    expect(!binary32 == !taken[k][0] && !binary16 == !taken[k][1] && !quantized == !taken[k][2],
+           "sizes of a kernel", k);
+  }
   rows();
   norms();
   printf("wrong=%d\n", bad);
