@@ -429,7 +429,8 @@ __device__ __forceinline__ void pin(V& v) {
   asm volatile("" : "+v"(v));
 }
 
-// End of a phase or step (loads of later ones stay in flight): this wave's LDS accesses are done, then everybody's.
+// End of a phase or step (loads of later ones stay in flight): this wave's LDS
+// accesses are done, then everybody's.
 __device__ __forceinline__ void phase_end() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   __builtin_amdgcn_sched_barrier(0);
@@ -604,10 +605,13 @@ k_tile(const Fp8Args a, const Launch l) {
 // read x and half of w, multiply, read the other half, multiply; the second group
 // is one phase behind, so that the matrix units of a SIMD, which has a wave of
 // each group, always have work.  (4001 rows of three 2560 x 2560 to binary16: 246 us
-// with 128 x 128 tiles and a barrier a step, 89 so.)  256 x 256 because a tile's
-// stage is 64 KB for 16.8 MFLOP: LDS reads, 96 KB of them a step, keep below the
-// matrix units' time.  What is left is the clock, which falls to 2.0 to 2.2 GHz under
-// these instructions, and the start and end of a tile (5 and up to 9 us of 60).
+// with 128 x 128 tiles and a barrier a step, 89 so.)  256 x 256 because
+// a step's 1 us of matrix instructions then hides its 64 KB of copies (137 B/ns) and
+// 192 KB of LDS reads (436 B/ns).  A step takes 1.5 us: the 16 products of a phase are
+// 244 ns, but the other group's reads of a phase, their latency and the barrier up to
+// 370.  The start and end of a tile are 5 and up to 9 us of 60.  Waves that read the
+// next operands between their products and meet twice a step, without turns, took 150
+// us where this takes 124.
 template <typename T, Mode MODE>
 __global__ void __launch_bounds__(T::THREADS, 2) k_big(const Fp8Args a, const Launch l) {
   constexpr int W = T::W, TN = T::TN, TM = T::TM, SC = T::SC;
