@@ -985,6 +985,7 @@ hipError_t launch_ring(const Fp8Args& a, const Launch& l, int tiles, hipStream_t
 // FP8 operands: 128 outputs a wave, so that a row's block is one wave's
 typedef Tile<2, 4, 8, 4, 2> T256;  // 256 outputs x 256 rows
 typedef Tile<1, 4, 8, 2, 2> T128;  // 128 x 128
+typedef Tile<1, 4, 8, 1, 2> T64;   // 128 x 64
 // binary16 operands, widened by every wave that reads them: as square as they go
 // (2047 rows of 16384 x 4096: 262 us, by eight waves of 64 x 32 280)
 typedef Tile<2, 2, 4, 4, 2> W128;  // 128 x 128
@@ -993,13 +994,13 @@ typedef Tile<2, 2, 4, 2, 2> W64;   // 128 x 64 (61 rows of 65529 x 2048: 28.1 us
 // What a call runs: a kernel with its tile, and the ranges of K.
 enum Kind {
   ROWS16, ROWS64, RING1X2, RING2X2, RING4X2, RING4X3, RING4X4, RING8X1, RING8X2, WIDE64, WIDE128, FP128,
-  FP256
+  FP256, FP64
 };
 struct Shape {
   int bn, bm;
 };
 constexpr Shape SHAPES[] = {{16, 16},  {64, 16},  {16, 32},  {32, 32},  {64, 32},   {64, 48},  {64, 64},
-                            {128, 16}, {128, 32}, {128, 64}, {128, 128}, {128, 128}, {256, 256}};
+                            {128, 16}, {128, 32}, {128, 64}, {128, 128}, {128, 128}, {256, 256}, {128, 64}};
 struct Plan {
   Kind kind;
   int splits;
@@ -1094,8 +1095,10 @@ bool few(const Fp8Args& a) {
   return a.out == OUT_F32 || a.M <= 16 || tiles <= CUS / 4 || (a.M <= 64 && tiles <= CUS / 2);
 }
 
-// K is split, with a workspace, while two tiles or more would go to a compute unit
-// of their own, in ranges of four blocks at least.
+// K is split, with a workspace, where compute units would have no tile of 128 x 128,
+// in ranges of 16 blocks at least (binary16, us, split and in whole tiles of 64 rows:
+// 512 x 4096 x 4096 21.8 and 22.8, 400 x 4096 x 16384 59.6 and 71.5; with ranges of
+// eight 1000 x 2048 x 2048 15.8 and 13.1, 300 x 4096 x 2048 15.5 and 12.6).
 Plan choose(const Fp8Args& a, bool split) {
   if (few(a)) return Plan{choose_wide(a), 1};
   // A round of tiles of 256 x 256, one to a compute unit, takes 1.2 times as long as
@@ -1104,14 +1107,18 @@ Plan choose(const Fp8Args& a, bool split) {
   // 2048 rows 57.3 and 44.5, 2500 48.4 and 56.0, 4001 55.6 and 79.3, 4352 96.4 and 92.8.)
   const long long large = (tiles_of(a, FP256) + CUS - 1) / CUS, small = tiles_of(a, FP128);
   if (12 * large * 2 * CUS < 10 * (small < 2 * CUS ? 2 * CUS : small)) return Plan{FP256, 1};
-  Plan c{FP128, 1};
-  if (!split) return c;
+  // Where every tile of 128 x 128 has a compute unit to itself, or half its rows would
+  // be past the end, tiles of 64 rows share one and fill each other's waits (binary16,
+  // us, 64 and 128 rows: 1024 x 4096 x 4096 27.2 and 30.6, 203 rows of three 4096 x
+  // 4096 25.0 and 29.4, 64 x 65536 x 2048 29.4 and 32.1; 1300 x 4096 x 4096, which has
+  // more tiles, 33.4 and 31.6).
+  const Plan whole{small <= CUS || a.M <= 64 ? FP64 : FP128, 1};
+  if (!split) return whole;
   int kb = 1 << 30;
   for (int i = 0; i < a.count; i++) kb = a.p[i].K / 128 < kb ? a.p[i].K / 128 : kb;
-  const long long want = CUS / tiles_of(a, FP128);  // 3 at most: `few` has the rest
-  c.splits = (int)(want < kb / 4 ? want : kb / 4);
-  if (c.splits < 1) c.splits = 1;
-  return c;
+  const long long want = CUS / small;  // 3 at most: `few` has the rest
+  const int splits = (int)(want < kb / 16 ? want : kb / 16);
+  return splits > 1 ? Plan{FP128, splits} : whole;
 }
 
 template <typename T, Mode MODE, bool E8>
@@ -1169,6 +1176,7 @@ hipError_t launch_fp8(const Fp8Args& a, void* ws, hipStream_t s) {
     case WIDE64: return launch_wide<W64>(a, l, tiles, s);
     case WIDE128: return launch_wide<W128>(a, l, tiles, s);
     case FP128: return launch_fp8_tile<T128>(a, l, tiles, s);
+    case FP64: return launch_fp8_tile<T64>(a, l, tiles, s);
     default: return launch_fp8_tile<T256>(a, l, tiles, s);
   }
 }

@@ -525,9 +525,9 @@ typedef struct {
  *   64 KiB are zero before its first use; every call leaves them zero (a workspace of
  *   rq_gemm_smallm_ws will do).  Calls that share it must not overlap in time, in
  *   graphs neither.  Only RQ_TYPE_F16 and RQ_TYPE_E4M3 outputs that make more than 64
- *   and at most 128 tiles of 128 x 128 use one, to split K; NULL keeps K whole there
- *   too, which takes up to twice as long.  RQ_ERR_SCRATCH: smaller than
- *   rq_gemm_fp8_workspace_size reports.
+ *   and at most 128 tiles of 128 x 128, of K = 4096 or more, use one, to split K; NULL
+ *   keeps K whole there too, which takes 5 to 20 % longer.  RQ_ERR_SCRATCH: smaller
+ *   than rq_gemm_fp8_workspace_size reports.
  * Results are deterministic; which sums are taken together follows from the sizes
  * of the call (and from whether it has a workspace).
  * Shape rules: 1 <= count <= RQ_FP8_MAX_BATCH, 1 <= M <= RQ_MAX_TOKENS, 1 <= N <=

@@ -96,7 +96,7 @@ const fake::Launch& launched(const char* what, long long a, long long b, long lo
 }  // namespace
 
 // Every kernel has sizes that take it.
-int taken[rq::FP256 + 1][3];
+int taken[rq::FP64 + 1][3];
 
 static void products() {
   const int ms[] = {1, 2, 4, 5, 8, 16, 17, 32, 33, 61, 64, 65, 100, 128, 129, 200, 256, 300, 511, 512,
@@ -199,7 +199,7 @@ static void norms() {
 
 int main() {
   products();
-  for (int k = 0; k <= rq::FP256; k++) {
+  for (int k = 0; k <= rq::FP64; k++) {
     const bool quantized = k == rq::RING8X1 || k == rq::RING8X2 || k >= rq::FP128;
     const bool binary32 = k < rq::RING8X1 || k == rq::WIDE64 || k == rq::WIDE128;
     const bool binary16 = k < rq::RING8X1 || k >= rq::FP128;

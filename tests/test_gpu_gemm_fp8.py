@@ -110,8 +110,9 @@ def test_many_odd_binary16_outputs(M, N, e8m0):
 
 @pytest.mark.parametrize("e8m0", [True, False])
 @pytest.mark.parametrize("M,N,K,ranges", [
-    (1100, 1152, 1024, 2), (130, 8320, 2176, 1), (130, 8192, 2176, 2), (1500, 1408, 4224, 1),
-    (1500, 1280, 4224, 2), (257, 4096, 10240, 2), (1025, 1024, 1536, 3)])
+    (1100, 1152, 1024, 1), (130, 8320, 2176, 1), (130, 8192, 2176, 1), (1500, 1408, 4224, 1),
+    (1500, 1280, 4224, 2), (257, 4096, 10240, 2), (1025, 1024, 1536, 1), (1100, 1152, 4096, 2),
+    (130, 8192, 4224, 2), (1025, 1024, 6272, 3)])
 def test_ranges_of_k_through_a_workspace(M, N, K, ranges, e8m0):
     """Sizes on both sides of splitting K, with the workspace and without; binary16
     and E4M3 alike."""
@@ -300,7 +301,7 @@ def test_graph_replays_and_the_workspace_stays_zero(M, N, K):
 
 
 def test_graph_replays_with_ranges_of_k():
-    M, N, K = 1100, 1152, 2560
+    M, N, K = 1100, 1152, 5120
     ops = operands(M, N, K, True, 3)
     size = rq.rq_gemm_fp8_workspace_size([(N, K)], M, rq.RQ_SCALE_E8M0, rq.RQ_TYPE_F16)
     area = torch.zeros(size // 4, dtype=torch.int32, device="cuda")
@@ -331,7 +332,7 @@ def test_graph_replays_with_ranges_of_k():
 def test_two_streams_at_once():
     """Each stream's calls with the workspace that the binding keeps for it."""
     work = [(operands(40, 512, 8192, True, s), operands(200, 384, 2560, False, s),
-             operands(300, 4096, 2560, False, s)) for s in (1, 2)]
+             operands(300, 4096, 5120, False, s)) for s in (1, 2)]
     outs = ("f32", "f32", "f16")
 
     def step(w):
@@ -359,7 +360,7 @@ def test_two_streams_at_once():
 def test_two_graphs_at_once():
     """Graphs of calls that would split K, captured on one stream that has a workspace
     and replayed on two: each gives what the call without a workspace does."""
-    M, N, K = 1100, 1152, 2560
+    M, N, K = 1100, 1152, 5120
     work = [operands(M, N, K, True, s) for s in (1, 2)]
     want = [run(o, "f16", workspace=None) for o in work]
     ys = [torch.empty((M, N), dtype=torch.float16, device="cuda") for _ in work]
