@@ -1080,16 +1080,17 @@ Kind choose_wide(const Fp8Args& a) {
 }
 
 // Rows and rings for all binary32 outputs, and for the others while tiles of 128 x
-// 128 would leave the card empty.  Measured, binary16 outputs, us (tiles with K split
-// through a workspace, and whole):
-//   rows x outputs x K  tiles   ring  split  whole
-//   256 x 4096 x 4096     64    14.8   19.1   28.6
-//   256 x 4096 x 16384    64    41.7   36.4   98.6
-//   512 x 4096 x 4096    128    26.4   23.5   28.9
-//   203 x 12288 x 4096   192    36.7   29.4   29.4
-//   64 x 16384 x 4096    128    17.9   24.5   28.8
-//   64 x 65536 x 2048    512    49.9     -    39.6
-//   17 x 65536 x 2048    512    37.3     -    40.0
+// 128 would leave the card empty.  Measured, binary16 outputs, us (rings; those tiles
+// with K split through a workspace; tiles of 64 rows):
+//   rows x outputs x K         tiles   rings  split  64 rows
+//   203 x 4096 x 4096            64     15.3   18.3    21.1
+//   256 x 4096 x 16384           64     43.7   36.4    70.2
+//   100 x 4096 x 4096, three     96     25.3   22.5    22.9
+//   512 x 4096 x 4096           128     26.4   22.0    22.8
+//   203 x 4096 x 4096, three    192     36.7     -     25.4
+//   64 x 65536 x 2048           512     49.9     -     29.3
+//   17 x 65536 x 2048           512     37.3     -     40 (128 rows)
+//   64 x 16384 x 4096           128     17.9   24.5    28.8 (128 rows)
 bool few(const Fp8Args& a) {
   const long long tiles = tiles_of(a, FP128);
   return a.out == OUT_F32 || a.M <= 16 || tiles <= CUS / 4 || (a.M <= 64 && tiles <= CUS / 2);
