@@ -646,7 +646,9 @@ def rq_gemm_fp8(problems, act=RQ_ACT_NONE, stream=None, workspace=AUTO):
     scales [M][K / 128], y_in float32 [M][N] (y itself, another tensor, or
     None), y float32 or float16 [M][N], or a pair (E4M3 [M][N], scales [M][N /
     128]) for the float16 output quantized as rq_quant_fp8 with ``act`` does.
-    All share M, the type of scales and the type of y.  ``workspace``: AUTO
+    All share M, the type of scales and the type of y.  Sums of a float32 y are
+    held in float32; those of the others from more than 64 tiles of 128 x 128
+    outputs on to about 2^-15 (include/rq.h).  ``workspace``: AUTO
     (the binding's, per stream, if the call uses one; None in a graph's
     capture), a tensor of rq_gemm_fp8_workspace_size bytes (zero before its
     first use), or None to keep K whole.  A prepared call keeps the workspace

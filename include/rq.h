@@ -509,12 +509,15 @@ typedef struct {
  *   RQ_TYPE_F16: rounded to binary16 (past 65504 infinite); no y_in.
  *   RQ_TYPE_E4M3: what rq_quant_fp8 with `act` makes of the RQ_TYPE_F16 output (of
  *     a call that has a workspace too, or none too), to the bit, without that output
- *     in memory; no y_in, N % 128 == 0.
- *     Calls of more than 16 rows may take the FP8 matrix instructions for these two
- *     (they do where the outputs fill the card with tiles of 128 x 128).  Those
- *     drop what lies 2^-13 or more below the largest of eight products: within
- *     2^-10 of the sum of the products' magnitudes, about 2^-15 of an ordinary
- *     output.
+ *     in memory, and so with its range: NaN past 65504, steps of 2^-24 near zero; no
+ *     y_in, N % 128 == 0.
+ *     For these two, calls of more than 16 rows whose outputs make more than 64 tiles
+ *     of 128 x 128 over all products (more than 128 with up to 64 rows) take the FP8
+ *     matrix instructions, others binary32 sums as for RQ_TYPE_F32.  The FP8
+ *     instructions drop what lies 2^-13 or more below the largest of eight products:
+ *     within 2^-10 of the sum of the products' magnitudes, about 2^-15 of an ordinary
+ *     output.  A caller that wants binary32 sums at every size, or the range of
+ *     binary32 in a quantized output, takes RQ_TYPE_F32 (with rq_quant_fp8 behind it).
  *   act: RQ_ACT_NONE, or RQ_ACT_RELU2 with RQ_TYPE_E4M3.
  * NaN in an operand or a scale reaches its outputs.  The product of an x scale and
  * a w scale has to be a normal binary32 number (or zero); what a smaller or larger
