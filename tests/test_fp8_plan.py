@@ -1,14 +1,17 @@
 """Which kernel a call of rq_gemm_fp8 runs, on the CPU: ``tests/fp8_plan_check.hip``
 is the library's own choice, compiled for the host.  What include/rq.h says about
-the FP8 matrix instructions is held to it."""
+the FP8 matrix instructions is held to it, and the sizes of test_gpu_fp8_sums.py are
+those of the kernels that they are there for."""
 import os
 import re
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 
 import gemm_rwkv_decode_amd as rq
+from tests import test_gpu_fp8_sums as G
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -65,3 +68,26 @@ def test_when_the_fp8_instructions_are_taken(plans):
     text = " ".join(re.sub(r"\n \*", " ", open(os.path.join(ROOT, "include", "rq.h")).read()).split())
     assert "more than 16 rows whose outputs make more than 64 tiles of 128 x 128 over all products " \
            "(more than 128 with up to 64 rows) take the FP8 matrix instructions" in text
+
+
+def test_sizes_of_the_gpu_tests(plans):
+    calls = [(c.M, c.out, c.ws, c.shapes) for c in G.CASES]
+    for c, got in zip(G.CASES, plans(calls)):
+        assert got == (c.kind, c.ranges), (c, got)
+    assert {c.kind for c in G.CASES} >= {"ROWS16", "ROWS64", "RING1X2", "RING2X2", "RING4X2", "RING4X3",
+                                         "RING4X4", "RING8X1", "RING8X2", "WIDE64", "WIDE128", "FP64",
+                                         "FP128", "FP256"}
+    # products that test_gpu_fp8_sums.py expects by themselves to the bit: kernels that
+    # add a block after the other too
+    one = [(c.M, c.out, False, [s]) for c in G.CASES if c.alone for s in c.shapes]
+    assert one and all(k.startswith(("FP", "WIDE")) and r == 1 for k, r in plans(one))
+
+
+def test_the_measure_of_sums_shows_a_scale_that_is_off():
+    """The oracle with one block's scale 5% off at K = 4096: far past the limit."""
+    g = np.random.default_rng(1)
+    x, w = g.standard_normal((200, 32, 128)), g.standard_normal((300, 32, 128))
+    y = np.einsum("mbk,nbk->mn", x, w)
+    off = y + 0.05 * x[:, 3] @ w[:, 3].T
+    assert G.difference(y.astype(np.float16), y) == 0
+    assert G.difference(off.astype(np.float16), y) > 20 * G.FP8_LIMIT
