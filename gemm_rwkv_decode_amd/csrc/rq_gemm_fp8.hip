@@ -868,7 +868,7 @@ hipError_t launch_rows(const Fp8Args& a, const Launch& l, int tiles, hipStream_t
 template <int TN, int TM, int ST, bool E8>
 __global__ void __launch_bounds__(64 * SW, 2) k_ring(const Fp8Args a, const Launch l) {
   constexpr int W = SW;
-  constexpr int STAGE = (TN + TM) * 2048, COPIES = 2 * (TN + TM), OPS = COPIES + TM + 1;
+  constexpr int STAGE = (TN + TM) * 2048, COPIES = 2 * (TN + TM);
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -890,19 +890,32 @@ __global__ void __launch_bounds__(64 * SW, 2) k_ring(const Fp8Args a, const Laun
   size_t xs[TM];
 #pragma unroll
   for (int j = 0; j < TM; j++) xs[j] = (m0 + min(16 * j + r, x_last)) * KB;
-  const size_t ws = (size_t)(n0 / 128) * KB;
+  int lane0 = 0;
+  // of lanes, not of the wave: a scale in a scalar register would be waited for before
+  // the copies behind it
+  if constexpr (ST > 1) pin(lane0);
+  const size_t ws = (size_t)(n0 / 128) * KB + lane0;
   u32 sx[ST][TM], sw[ST];
-  // the wave's step i in slot d; past its last one, the last block again, so that
-  // every step has the same loads behind it
-  auto ask = [&](int i, int d) {
-    const int b = min(wave + i * W, KB - 1);
-#pragma unroll
-    for (int c = 0; c < COPIES; c++)
-      lds_copy16(c < 2 * TN ? wr : xr, ring + d * STAGE + c * 1024, off[c], b * 128);
+  auto ask_scales = [&](int b, int d) {
 #pragma unroll
     for (int j = 0; j < TM; j++) sx[d][j] = load_scale(p.xs, xs[j] + b, E8);
     sw[d] = load_scale(p.ws, ws + b, E8);
-    __builtin_amdgcn_sched_barrier(0);  // the order that the waits count on
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // The wave's step i in slot d; past its last one, the last block again, so that
+  // every step has the same loads behind it.  With several stages the scales come
+  // first: whether they are vector or scalar loads, a slot's copies then have at least
+  // the copies of the later slots behind them, which is what the waits count on.  One
+  // stage waits for all it asked for, and its copies are the longer way (203 rows,
+  // 2560 x 10240: 22.8 us, scales first 24.2).
+  auto ask = [&](int i, int d) {
+    const int b = min(wave + i * W, KB - 1);
+    if constexpr (ST > 1) ask_scales(b, d);
+#pragma unroll
+    for (int c = 0; c < COPIES; c++)
+      lds_copy16(c < 2 * TN ? wr : xr, ring + d * STAGE + c * 1024, off[c], b * 128);
+    if constexpr (ST == 1) ask_scales(b, d);
+    __builtin_amdgcn_sched_barrier(0);
   };
   f4 acc[TN][TM];
 #pragma unroll
@@ -918,7 +931,7 @@ __global__ void __launch_bounds__(64 * SW, 2) k_ring(const Fp8Args a, const Laun
     for (int d = 0; d < ST; d++) {
       if (i + d >= n) break;
       __builtin_amdgcn_sched_barrier(0);
-      wait_vm<(ST - 1) * OPS>();
+      wait_vm<(ST - 1) * COPIES>();
       __atomic_signal_fence(__ATOMIC_SEQ_CST);
       const char* const st = ring + d * STAGE;
       h8 x[TM][2][2];
