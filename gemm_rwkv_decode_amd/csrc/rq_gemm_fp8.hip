@@ -924,34 +924,41 @@ __global__ void __launch_bounds__(64 * SW, 2) k_ring(const Fp8Args a, const Laun
     for (int j = 0; j < TM; j++) acc[t][j] = f4{0, 0, 0, 0};
   const int o0 = r * 128 + ((h ^ (r & 7)) << 4), o1 = r * 128 + (((4 + h) ^ (r & 7)) << 4);
   const int n = (KB - wave + W - 1) / W;
+  auto multiply_step = [&](int d) {
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vm<(ST - 1) * COPIES>();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    const char* const st = ring + d * STAGE;
+    h8 x[TM][2][2];
+#pragma unroll
+    for (int j = 0; j < TM; j++) {
+      widen(*reinterpret_cast<const u32x4*>(st + (TN + j) * 2048 + o0), x[j][0]);
+      widen(*reinterpret_cast<const u32x4*>(st + (TN + j) * 2048 + o1), x[j][1]);
+    }
+    float f[TM];
+#pragma unroll
+    for (int j = 0; j < TM; j++)
+      f[j] = __builtin_bit_cast(float, joint_scale<WIDE>(sx[d][j], sw[d], E8));
+    multiply_wide<TN, TM>(st, o0, o1, x, f, acc);
+    // the slot has been read
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
+    __builtin_amdgcn_sched_barrier(0);
+  };
 #pragma unroll
   for (int d = 0; d < ST; d++) ask(d, d);
-  for (int i = 0; i < n; i += ST) {
+  // whole rounds of the slots, and the rest: a way out of the middle of a round makes
+  // the compiler wait for every load where the ways meet
+  int i = 0;
+  for (; i + ST <= n; i += ST) {
 #pragma unroll
     for (int d = 0; d < ST; d++) {
-      if (i + d >= n) break;
-      __builtin_amdgcn_sched_barrier(0);
-      wait_vm<(ST - 1) * COPIES>();
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
-      const char* const st = ring + d * STAGE;
-      h8 x[TM][2][2];
-#pragma unroll
-      for (int j = 0; j < TM; j++) {
-        widen(*reinterpret_cast<const u32x4*>(st + (TN + j) * 2048 + o0), x[j][0]);
-        widen(*reinterpret_cast<const u32x4*>(st + (TN + j) * 2048 + o1), x[j][1]);
-      }
-      float f[TM];
-#pragma unroll
-      for (int j = 0; j < TM; j++)
-        f[j] = __builtin_bit_cast(float, joint_scale<WIDE>(sx[d][j], sw[d], E8));
-      multiply_wide<TN, TM>(st, o0, o1, x, f, acc);
-      // the slot has been read
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
-      __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
-      __builtin_amdgcn_sched_barrier(0);
+      multiply_step(d);
       ask(i + d + ST, d);
     }
   }
+  static_assert(ST <= 2, "at most one step is left, with the next one's copies behind its own");
+  if (i < n) multiply_step(0);
   wait_vm<0>();
   __syncthreads();
   f4* const sums = reinterpret_cast<f4*>(lds);

@@ -44,6 +44,18 @@ def test_every_ring_is_there(kernels):
     assert len(list(rings(kernels))) >= 12
 
 
+def test_a_ring_waits_for_its_oldest_stage_only(kernels):
+    """Between a ring's first product and its last, the only loads that are waited for
+    are those ahead of the copies of the later stages: 2 (outputs + rows) copies of
+    each stay in flight."""
+    for (tn, tm, stages), code in rings(kernels):
+        mfma = [i for i, c in enumerate(code) if c.startswith("v_mfma")]
+        loop = code[mfma[0]:mfma[-1]]
+        waits = [int(n) for c in loop for n in re.findall(r"vmcnt\((\d+)\)", c)]
+        assert set(waits) <= {(stages - 1) * 2 * (tn + tm)}, (tn, tm, stages, waits)
+        assert waits or stages == 1  # the wait of a ring of one stage is ahead of all products
+
+
 def test_a_ring_asks_for_scales_before_copies(kernels):
     """Where a wait leaves later stages in flight, a stage's copies stand together and
     its scales before them, so that nothing but the copies of later stages has to be
