@@ -797,7 +797,10 @@ __global__ void __launch_bounds__(64 * SW, 2) k_rows(const Fp8Args a, const Laun
   for (int t = 0; t < TW; t++) wp[t] = p.w + (size_t)min(n0 + 16 * t + r, p.N - 1) * p.K + 16 * h;
   const size_t m = min(r, a.M - 1);  // rows past the end repeat the last one
   const uint8_t* xp = p.x + m * p.K + 16 * h;
-  const size_t xs = m * KB, ws = (size_t)(n0 / 128) * KB;
+  // of lanes, not of the wave: a scale in a scalar register is waited for at once
+  int lane0 = 0;
+  pin(lane0);
+  const size_t xs = m * KB, ws = (size_t)(n0 / 128) * KB + lane0;
   Block<TW> ring[D];
   auto load = [&](Block<TW>& v, int b) {
     const size_t at = (size_t)b * 128;
@@ -814,27 +817,50 @@ __global__ void __launch_bounds__(64 * SW, 2) k_rows(const Fp8Args a, const Laun
   f4 acc[TW][1];
 #pragma unroll
   for (int t = 0; t < TW; t++) acc[t][0] = f4{0, 0, 0, 0};
+  auto multiply_block = [&](const Block<TW>& v) {
+    h8 w[TW][2][2], x[1][2][2];
 #pragma unroll
-  for (int d = 0; d < D; d++)
-    if (wave + d * SW < KB) load(ring[d], wave + d * SW);
-  for (int b0 = wave; b0 < KB; b0 += D * SW) {
+    for (int q = 0; q < 2; q++) {
+#pragma unroll
+      for (int t = 0; t < TW; t++) widen(v.w[t][q], w[t][q]);
+      widen(v.x[q], x[0][q]);
+    }
+    const float f[1] = {__builtin_bit_cast(float, joint_scale<WIDE>(v.sx, v.sw, E8))};
+    multiply_wide<TW, 1>(w, x, f, acc);
+  };
+  // Rounds whose next blocks are all there, and the rest: with a condition at every
+  // load the compiler waits for all loads where the ways meet (3 rows, 65536 x 2048:
+  // 30.5 us, and 28.7 so; 8 rows, 16384 x 4096 12.8 and 12.2).
+  int b = wave;
+  if (b + (2 * D - 1) * SW < KB) {
 #pragma unroll
     for (int d = 0; d < D; d++) {
-      const int b = b0 + d * SW;
-      if (b >= KB) break;
-      h8 w[TW][2][2], x[1][2][2];
-#pragma unroll
-      for (int q = 0; q < 2; q++) {
-#pragma unroll
-        for (int t = 0; t < TW; t++) widen(ring[d].w[t][q], w[t][q]);
-        widen(ring[d].x[q], x[0][q]);
-      }
-      const float f[1] = {
-          __builtin_bit_cast(float, joint_scale<WIDE>(ring[d].sx, ring[d].sw, E8))};
-      multiply_wide<TW, 1>(w, x, f, acc);
-      if (b + D * SW < KB) load(ring[d], b + D * SW);
+      load(ring[d], b + d * SW);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    do {
+#pragma unroll
+      for (int d = 0; d < D; d++) {
+        multiply_block(ring[d]);
+        __builtin_amdgcn_sched_barrier(0);
+        load(ring[d], b + (d + D) * SW);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      b += D * SW;
+    } while (b + (2 * D - 1) * SW < KB);
+  } else {
+#pragma unroll
+    for (int d = 0; d < D; d++)
+      if (b + d * SW < KB) load(ring[d], b + d * SW);
   }
+#pragma unroll
+  for (int d = 0; d < D; d++) {
+    if (b + d * SW < KB) multiply_block(ring[d]);
+    if (b + (d + D) * SW < KB) load(ring[d], b + (d + D) * SW);
+  }
+#pragma unroll
+  for (int d = 0; d < D - 1; d++)
+    if (b + (d + D) * SW < KB) multiply_block(ring[d]);
 #pragma unroll
   for (int t = 0; t < TW; t++) sums[wave][t][lane] = acc[t][0];
   __syncthreads();

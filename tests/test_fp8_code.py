@@ -1,5 +1,5 @@
-"""What the compiler makes of the block-scaled product's rings (the kernels' gfx950
-assembly, compiled on the CPU): which waits stand between their copies."""
+"""What the compiler makes of the block-scaled product's kernels for few rows (their
+gfx950 assembly, compiled on the CPU): which waits stand between their loads."""
 import os
 import re
 import shutil
@@ -27,6 +27,8 @@ def kernels(tmp_path_factory):
         label = re.match(r"(_Z\S+):", line)
         if label:
             name = found.setdefault(label.group(1), [])
+        elif name is not None and re.match(r"\.LBB\S+:", line):
+            name.append(line.split()[0])
         elif name is not None and line.startswith("\t") and not line.startswith("\t."):
             name.append(line.split(";")[0].split("//")[0].strip())
     return found
@@ -68,3 +70,28 @@ def test_a_ring_asks_for_scales_before_copies(kernels):
                         if re.match(r"(buffer|global|flat)_load", c))
         kinds = kinds[:kinds.rindex("c") + 1]
         assert re.fullmatch(f"(s+c{{{2 * (tn + tm)}}})+", kinds), (tn, tm, stages, kinds)
+
+
+def loops(code):
+    """Instructions of the innermost loops: from a label to a branch back to it."""
+    for i, c in enumerate(code):
+        m = re.match(r"s_cbranch_\w+ (\S+)", c)
+        if m and m.group(1) + ":" in code[:i]:
+            body = code[code.index(m.group(1) + ":"):i]
+            if not any(x.endswith(":") for x in body[1:]):
+                yield body
+
+
+def test_rows_keep_the_next_block_in_flight(kernels):
+    """k_rows of two blocks: no wait in its loop is for every load, so one block's are on
+    their way while the other is multiplied."""
+    found = 0
+    for name, code in kernels.items():
+        if "k_rowsILi1ELi2E" not in name:
+            continue
+        for body in loops(code):
+            if any(c.startswith("v_mfma") for c in body):
+                waits = [int(n) for c in body for n in re.findall(r"vmcnt\((\d+)\)", c)]
+                assert waits and min(waits) >= 6, waits  # 2 of w, 2 of x, 2 scales
+                found += 1
+    assert found == 2
