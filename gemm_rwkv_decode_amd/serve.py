@@ -232,7 +232,8 @@ def forward(model, state, tokens, offsets, slots, ids=None, adapters=None):
             if adapters is not None:
                 key, = products8(w.mats[4:5], (x8,))
                 adapters.add(adapters.key[l:l + 1], (mixed[0],), (key,), ids)
-                key8 = blocks(key, act=rq.RQ_ACT_RELU2)
+                # through binary16, as all activations here and as in the product below
+                key8 = blocks(key.half(), act=rq.RQ_ACT_RELU2)
             else:  # quantized by the product itself
                 key8, = products8(w.mats[4:5], (x8,), (_room8(T, model.ffn, x.device),),
                                   act=rq.RQ_ACT_RELU2)

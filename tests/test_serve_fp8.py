@@ -204,3 +204,18 @@ def test_the_command(capsys, more):
     lines = capsys.readouterr().out.splitlines()
     assert lines[0].startswith("6 requests") and "tokens/s" in lines[1]
     assert sum(line.startswith("request ") for line in lines) == 3
+
+
+@pytest.mark.gpu
+def test_requests_without_an_adapter_do_not_see_the_others():
+    """One rule for the FFN key, quantized behind the adapters or in its product: where
+    no request has an adapter, logits are those of a model without any, to the bit."""
+    model, adapters, prompts = T.build("cuda", S.FP8_B128)
+    runs = []
+    for ad, ids in ((adapters, [-1] * len(prompts)), (None, None)):
+        seen = []
+        tokens = V.generate(model, prompts, 3, ad, ids,
+                            on_step=lambda i, z: seen.append(z.clone().cpu()))
+        runs.append((tokens.cpu(), seen))
+    assert torch.equal(runs[0][0], runs[1][0])
+    assert all(torch.equal(a, b) for a, b in zip(runs[0][1], runs[1][1]))
