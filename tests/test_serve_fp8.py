@@ -209,7 +209,8 @@ def test_the_command(capsys, more):
 @pytest.mark.gpu
 def test_requests_without_an_adapter_do_not_see_the_others():
     """One rule for the FFN key, quantized behind the adapters or in its product: where
-    no request has an adapter, logits are those of a model without any, to the bit."""
+    no request has an adapter, logits are those of a model without any, to the bit (at
+    sizes like these, whose products all have binary32 sums)."""
     model, adapters, prompts = T.build("cuda", S.FP8_B128)
     runs = []
     for ad, ids in ((adapters, [-1] * len(prompts)), (None, None)):
